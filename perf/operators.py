@@ -133,7 +133,7 @@ def prepare(case, seed):
         weights = torch.full((T,), 1.0 / T, device=DEV)
         weights[row > 0.95] = 0.0  # positions left out of the loss
         s["logits"], s["ids"], s["teacher"], s["weights"] = logits.to(dt), ids, teacher.contiguous(), weights
-        s["loss"], s["lse"] = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+        s["loss"], s["stats"] = torch.empty(T, device=DEV), torch.empty(T, 2, device=DEV)
         if case["form"] != "loss":
             s["grad"] = torch.empty(T, V, device=DEV, dtype=dt)
     return s
@@ -162,8 +162,8 @@ def _run_own(s):
         return {k: s[k] for k in ("out", "dx", "dwg", "dwu", "dwd")}
     a = (s["logits"], s["ids"], s["teacher"])
     if s["form"] == "two":
-        ccl.ccl_distill_loss(*a, s["loss"], lse=s["lse"], weights=s["weights"], temperature=s["tau"])
-        ccl.ccl_distill_grad(*a, s["lse"], s["grad"], weights=s["weights"], temperature=s["tau"])
+        ccl.ccl_distill_loss(*a, s["loss"], stats=s["stats"], weights=s["weights"], temperature=s["tau"])
+        ccl.ccl_distill_grad(*a, s["stats"], s["grad"], weights=s["weights"], temperature=s["tau"])
         return {"loss": s["loss"], "grad": s["grad"]}
     if s["form"] == "fused":
         ccl.ccl_distill_loss(*a, s["loss"], grad=s["grad"], weights=s["weights"], temperature=s["tau"])
