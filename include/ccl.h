@@ -419,6 +419,81 @@ ccl_status_t ccl_allreduce_host(const void *const *send, void *const *recv, int 
                                 cudaStream_t stream);
 
 /* ------------------------------------------------------------------ */
+/* Operators of a training step                                        */
+/* ------------------------------------------------------------------ */
+
+/* What one rank computes between the collectives: the embedding lookup, the
+ * loss and their gradients, whose outputs are buffers that the collectives
+ * above reduce.  Unlike the collectives these calls take one rank's buffers.
+ * The common conventions hold: device buffers owned by the caller, work
+ * enqueued on `stream`, argument errors returned before anything is enqueued,
+ * CCL_ERR_OVERLAP where a written buffer overlaps another one of the call
+ * (except in the in-place forms noted), nothing allocated, so that every call
+ * may be captured in a CUDA graph.  Sums are held in fp32 and each output is
+ * rounded once to its type.  Strides are in elements, from one row to the
+ * next, and at least the row's length; buffers need only their element's
+ * alignment (16-byte aligned rows of whole 16-byte vectors run at full
+ * bandwidth).  No value is added by an atomic: the same inputs give the same
+ * bits. */
+
+/* Embedding lookup: out[t] = round(scale * table[ids[t] - first_row]), t <
+ * ntokens, rows of `dim` elements.  An id outside [first_row, first_row +
+ * rows) -- a padding id, or a row of another rank's shard of the vocabulary --
+ * gives a row of zeros, so that ccl_allreduce (CCL_SUM) over the ranks' outputs
+ * completes a lookup in a table whose rows are sharded.  rows, ntokens < 2^31;
+ * dim <= 2^24. */
+ccl_status_t ccl_embedding(const void *table, size_t rows, size_t dim, size_t table_stride, ccl_dtype_t dtype,
+                           const int64_t *ids, size_t ntokens, int64_t first_row, float scale, void *out,
+                           size_t out_stride, cudaStream_t stream);
+
+/* Its gradient: grad_table[v] = round([grad_table[v] +] scale * sum of
+ * grad_out[t] over the tokens with ids[t] == first_row + v).  The tokens are
+ * sorted by row, stably, and each row's are added in fp32 in runs of
+ * consecutive sorted tokens, joined in order.  accumulate = 0 writes every
+ * row (zeros where no token names it); accumulate != 0 adds to the rows that
+ * a token names and leaves the others untouched (a tied output projection's
+ * gradient, a further micro-batch).  work: device memory of
+ * ccl_plan_embedding_grad_work_bytes bytes, 16-byte aligned, not shared with
+ * a concurrent call; its contents need no initialisation.  Launches: the sort
+ * (which also zeroes), the sums, and the join when there are over 64 tokens. */
+ccl_status_t ccl_embedding_grad(const void *grad_out, size_t grad_out_stride, const int64_t *ids, size_t ntokens,
+                                int64_t first_row, size_t rows, size_t dim, ccl_dtype_t dtype, float scale,
+                                int accumulate, void *grad_table, size_t grad_table_stride, void *work,
+                                size_t work_bytes, cudaStream_t stream);
+ccl_status_t ccl_plan_embedding_grad_work_bytes(size_t ntokens, size_t rows, size_t dim, size_t *bytes);
+
+/* Distillation loss from a teacher's top logits.  Row t's teacher
+ * distribution p is the softmax of teacher_logits[t][0..top) / temperature
+ * over the entries whose id teacher_ids[t][j] is in [0, vocab) (others do not
+ * count, whatever their logit holds; an id may come twice); the student's q
+ * is the softmax of logits[t] / temperature over the whole vocabulary.
+ *   loss[t]    = weights[t] * sum_j p_j (log p_j - log q_{id_j})
+ *   grad[t][v] = weights[t] / temperature * (q_v - sum over {j: id_j = v} p_j),
+ * the derivative of the sum of the losses by logits[t][v].  A row without a
+ * teacher (no valid id, or only -inf logits) and a row of weight 0 have loss 0
+ * and gradient 0; weights == NULL means 1.  (The customary factor
+ * temperature^2 belongs in the weights.)  A logit of -inf leaves that entry
+ * out of the vocabulary.  teacher_ids and teacher_logits are contiguous
+ * [nrows][top] arrays, top <= CCL_MAX_TEACHER_TOP.
+ *
+ * ccl_distill_loss writes the losses, with stats != NULL also every row's
+ * (m, Z) -- its largest logit and sum_v exp((logits[v] - m) / temperature) --
+ * as stats[2t], stats[2t+1], and with grad != NULL also the gradient, the row
+ * then being read from memory once for both (rows of up to 512 KiB).
+ * ccl_distill_grad computes the gradient later from the kept stats, with
+ * weights of its own (weights times the incoming gradient of loss[t]).  In
+ * place: grad == logits with the same stride.  One launch each. */
+#define CCL_MAX_TEACHER_TOP 1024
+ccl_status_t ccl_distill_loss(const void *logits, size_t nrows, size_t vocab, size_t logits_stride, ccl_dtype_t dtype,
+                              const int64_t *teacher_ids, const float *teacher_logits, size_t top, float temperature,
+                              const float *weights, float *loss, float *stats, void *grad, size_t grad_stride,
+                              cudaStream_t stream);
+ccl_status_t ccl_distill_grad(const void *logits, size_t nrows, size_t vocab, size_t logits_stride, ccl_dtype_t dtype,
+                              const int64_t *teacher_ids, const float *teacher_logits, size_t top, float temperature,
+                              const float *weights, const float *stats, void *grad, size_t grad_stride,
+                              cudaStream_t stream);
+
+/* ------------------------------------------------------------------ */
 /* Result checks and tracing                                           */
 /* ------------------------------------------------------------------ */
 

@@ -59,6 +59,7 @@ def lib() -> ctypes.CDLL:
             L = ctypes.CDLL(path)
             vp, pp, i32, sz = ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p), ctypes.c_int, ctypes.c_size_t
             psz = ctypes.POINTER(ctypes.c_size_t)
+            i64, f32 = ctypes.c_int64, ctypes.c_float
             sig = {
                 "ccl_allreduce": [pp, pp, i32, sz, i32, i32, i32, vp],
                 "ccl_reduce_scatter": [pp, pp, i32, sz, i32, i32, i32, vp],
@@ -85,6 +86,11 @@ def lib() -> ctypes.CDLL:
                 "ccl_allreduce_host": [pp, pp, i32, sz, i32, i32, vp, sz, vp],
                 "ccl_plan_host_slices": [sz, i32, i32, sz, psz, psz, sz, psz],
                 "ccl_finalize": [],
+                "ccl_embedding": [vp, sz, sz, sz, i32, vp, sz, i64, f32, vp, sz, vp],
+                "ccl_embedding_grad": [vp, sz, vp, sz, i64, sz, sz, i32, f32, i32, vp, sz, vp, sz, vp],
+                "ccl_plan_embedding_grad_work_bytes": [sz, sz, sz, psz],
+                "ccl_distill_loss": [vp, sz, sz, sz, i32, vp, vp, sz, f32, vp, vp, vp, vp, sz, vp],
+                "ccl_distill_grad": [vp, sz, sz, sz, i32, vp, vp, sz, f32, vp, vp, vp, sz, vp],
             }
             for name, args in sig.items():
                 fn = getattr(L, name)
@@ -476,6 +482,132 @@ class CclBucketer:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------------------------ operators of a training step
+
+def _rows(t: torch.Tensor, name: str, cols: Optional[int] = None, dtype: Optional[torch.dtype] = None):
+    """(pointer, rows, columns, row stride) of a matrix with contiguous rows."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be a matrix with contiguous rows" % name)
+    if cols is not None and t.shape[1] != cols:
+        raise ValueError("%s has %d columns, expected %d" % (name, t.shape[1], cols))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    # the stride of fewer than two rows says nothing
+    return t.data_ptr(), t.shape[0], t.shape[1], max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+
+
+def _flat(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype):
+    """Pointer of a contiguous tensor of the given shape and type (None: a null pointer)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous tensor of shape %s" % (name, tuple(shape)))
+    return t.data_ptr()
+
+
+def _on_gpu(*ts: Optional[torch.Tensor]) -> None:
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("the operators take CUDA tensors")
+        if dev is not None and t.device != dev:
+            raise ValueError("the tensors are on different devices")
+        dev = t.device
+
+
+def _work(work: Optional[torch.Tensor], nbytes: int, like: torch.Tensor, stream):
+    """The caller's work buffer, or one allocated on the call's own stream (so
+    that the allocator hands it out again only after the call's kernels)."""
+    if work is None:
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+        with torch.cuda.stream(stream):
+            work = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    elif not work.is_cuda or not work.is_contiguous():
+        raise ValueError("work must be a contiguous CUDA tensor")
+    return work, work.numel() * work.element_size()
+
+
+def ccl_embedding(table: torch.Tensor, ids: torch.Tensor, out: torch.Tensor, scale: float = 1.0, first_row: int = 0,
+                  stream=None) -> None:
+    """out[t] = scale * table[ids[t] - first_row]; zeros for an id outside the
+    table's rows (padding, or another rank's shard of the vocabulary)."""
+    _on_gpu(table, ids, out)
+    tp, rows, dim, ts = _rows(table, "table")
+    op, n, _, os_ = _rows(out, "out", dim, table.dtype)
+    ip = _flat(ids, "ids", (n,), torch.int64)
+    _check(lib().ccl_embedding(tp, rows, dim, ts, _dtype(table), ip, n, int(first_row), float(scale), op, os_,
+                               _stream(stream)), "ccl_embedding")
+
+
+def ccl_embedding_grad(grad_out: torch.Tensor, ids: torch.Tensor, grad_table: torch.Tensor, scale: float = 1.0,
+                       first_row: int = 0, accumulate: bool = False, work: Optional[torch.Tensor] = None,
+                       stream=None) -> None:
+    """grad_table[v] = [grad_table[v] +] scale * the sum of grad_out[t] over
+    the tokens with ids[t] == first_row + v.  work: a device buffer of at least
+    ccl_plan_embedding_grad_work_bytes bytes (allocated here when omitted)."""
+    _on_gpu(grad_out, ids, grad_table)
+    gp, n, dim, gs = _rows(grad_out, "grad_out")
+    tp, rows, _, ts = _rows(grad_table, "grad_table", dim, grad_out.dtype)
+    ip = _flat(ids, "ids", (n,), torch.int64)
+    work, nbytes = _work(work, 0 if work is not None else ccl_plan_embedding_grad_work_bytes(n, rows, dim), grad_out,
+                         stream)
+    _check(lib().ccl_embedding_grad(gp, gs, ip, n, int(first_row), rows, dim, _dtype(grad_out), float(scale),
+                                    int(bool(accumulate)), tp, ts, work.data_ptr(), nbytes, _stream(stream)),
+           "ccl_embedding_grad")
+
+
+def ccl_plan_embedding_grad_work_bytes(ntokens: int, rows: int, dim: int) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().ccl_plan_embedding_grad_work_bytes(int(ntokens), int(rows), int(dim), ctypes.byref(out)),
+           "ccl_plan_embedding_grad_work_bytes")
+    return out.value
+
+
+def ccl_distill_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, loss: torch.Tensor,
+                     stats: Optional[torch.Tensor] = None, grad: Optional[torch.Tensor] = None,
+                     weights: Optional[torch.Tensor] = None, temperature: float = 1.0, stream=None) -> None:
+    """loss[t] = weights[t] * KL(teacher || student) of row t, the teacher's
+    distribution given by its top logits.  stats ([rows, 2]): kept for
+    ccl_distill_grad.  grad: the gradient by the logits, in the same pass (may
+    be `logits` itself)."""
+    _on_gpu(logits, teacher_ids, teacher_logits, loss, stats, grad, weights)
+    lp, n, vocab, ls = _rows(logits, "logits")
+    gp, gs = None, vocab
+    if grad is not None:
+        gp, gn, _, gs = _rows(grad, "grad", vocab, logits.dtype)
+        if gn != n:
+            raise ValueError("grad has %d rows, expected %d" % (gn, n))
+    top = teacher_ids.shape[-1]
+    _check(lib().ccl_distill_loss(lp, n, vocab, ls, _dtype(logits), _flat(teacher_ids, "teacher_ids", (n, top), torch.int64),
+                                  _flat(teacher_logits, "teacher_logits", (n, top), torch.float32), top,
+                                  float(temperature), _flat(weights, "weights", (n,), torch.float32),
+                                  _flat(loss, "loss", (n,), torch.float32), _flat(stats, "stats", (n, 2), torch.float32),
+                                  gp, gs, _stream(stream)), "ccl_distill_loss")
+
+
+def ccl_distill_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+                     stats: torch.Tensor, grad: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                     temperature: float = 1.0, stream=None) -> None:
+    """The gradient of the sum of ccl_distill_loss's losses by the logits, from
+    the stats it kept; grad may be `logits` itself."""
+    _on_gpu(logits, teacher_ids, teacher_logits, stats, grad, weights)
+    lp, n, vocab, ls = _rows(logits, "logits")
+    gp, gn, _, gs = _rows(grad, "grad", vocab, logits.dtype)
+    if gn != n:
+        raise ValueError("grad has %d rows, expected %d" % (gn, n))
+    top = teacher_ids.shape[-1]
+    _check(lib().ccl_distill_grad(lp, n, vocab, ls, _dtype(logits), _flat(teacher_ids, "teacher_ids", (n, top), torch.int64),
+                                  _flat(teacher_logits, "teacher_logits", (n, top), torch.float32), top,
+                                  float(temperature), _flat(weights, "weights", (n,), torch.float32),
+                                  _flat(stats, "stats", (n, 2), torch.float32), gp, gs, _stream(stream)),
+           "ccl_distill_grad")
 
 
 # ------------------------------------------------------------------ planner
