@@ -462,6 +462,43 @@ ccl_status_t ccl_embedding_grad(const void *grad_out, size_t grad_out_stride, co
                                 size_t work_bytes, cudaStream_t stream);
 ccl_status_t ccl_plan_embedding_grad_work_bytes(size_t ntokens, size_t rows, size_t dim, size_t *bytes);
 
+/* Gated feed-forward block on ntokens rows of `dim` values:
+ *   g = x w_gate^T, u = x w_up^T, h = act(g) * u, out = h w_down^T
+ * with w_gate, w_up [ffn][dim] and w_down [dim][ffn] (an output unit's weights
+ * are a row).  All matrices are contiguous and bf16 (CCL_FP32:
+ * CCL_ERR_UNSUPPORTED); the products accumulate in fp32 and h is rounded to
+ * bf16 once.  saved != NULL keeps g and u for the backward pass, fp32,
+ * [2][ntokens][ffn].  work: device memory of ccl_plan_gated_ffn_work_bytes
+ * bytes, 256-byte aligned, not shared with a concurrent call, contents
+ * irrelevant.  dim and ffn <= 2^24. */
+typedef enum { CCL_ACT_SILU = 0, CCL_ACT_GELU_TANH = 1 } ccl_act_t;
+ccl_status_t ccl_gated_ffn(const void *x, const void *w_gate, const void *w_up, const void *w_down, size_t ntokens,
+                           size_t dim, size_t ffn, ccl_dtype_t dtype, ccl_act_t act, void *out, float *saved, void *work,
+                           size_t work_bytes, cudaStream_t stream);
+
+/* Its gradients, from grad_out and the saved g and u (h is made again):
+ *   dh = grad_out w_down, du = dh * act(g), dg = dh * u * act'(g)
+ *   grad_x = dg w_gate + du w_up, grad_w_gate = dg^T x, grad_w_up = du^T x,
+ *   grad_w_down = grad_out^T h
+ * dg and du are rounded to bf16 once.  A NULL gradient is not computed.
+ * accumulate != 0 adds to the weight gradients (grad_x is always written):
+ * round(old + sum), one rounding.  work: as above, planned with backward = 1. */
+ccl_status_t ccl_gated_ffn_grad(const void *grad_out, const void *x, const void *w_gate, const void *w_up,
+                                const void *w_down, const float *saved, size_t ntokens, size_t dim, size_t ffn,
+                                ccl_dtype_t dtype, ccl_act_t act, int accumulate, void *grad_x, void *grad_w_gate,
+                                void *grad_w_up, void *grad_w_down, void *work, size_t work_bytes, cudaStream_t stream);
+
+/* Bytes of the work buffer.  aligned != 0: every input matrix is 16-byte
+ * aligned (else, or where a width is no multiple of 8, room for padded copies
+ * of the inputs is included: the copy engine that feeds the tensor cores
+ * addresses whole 16-byte vectors). */
+ccl_status_t ccl_plan_gated_ffn_work_bytes(size_t ntokens, size_t dim, size_t ffn, int backward, int aligned, size_t *bytes);
+
+/* How often a gated feed-forward kernel on the current device gave up waiting
+ * for its own copies or products (after 4 s; its results are then missing):
+ * 0 on a sound machine.  Waits for the device. */
+ccl_status_t ccl_gated_ffn_timeouts(unsigned long long *count);
+
 /* Distillation loss from a teacher's top logits.  Row t's teacher
  * distribution p is the softmax of teacher_logits[t][0..top) / temperature
  * over the entries whose id teacher_ids[t][j] is in [0, vocab) (others do not

@@ -22,6 +22,7 @@ FUSED, STEP = 0, 1
 OPS = {"sum": SUM, "avg": AVG, "max": MAX, "prod": PROD, "min": MIN, "avg_premul": AVG_PREMUL}
 MODES = {"fused": FUSED, "step": STEP}
 ALGOS = {"ring": 0, "halving_doubling": 1, "tree": 2, "hierarchical": 3}
+ACTS = {"silu": 0, "gelu": 1}
 COMPRESSORS = {"int8_block": 0, "threshold": 1, "topk": 2}
 STATUS = {0: "CCL_OK", 1: "CCL_ERR_INVALID_ARG", 2: "CCL_ERR_UNSUPPORTED", 3: "CCL_ERR_OVERLAP",
           4: "CCL_ERR_CUDA", 5: "CCL_ERR_NO_MEMORY", 6: "CCL_ERR_TIMEOUT", 7: "CCL_ERR_CHECK_FAILED"}
@@ -89,6 +90,10 @@ def lib() -> ctypes.CDLL:
                 "ccl_embedding": [vp, sz, sz, sz, i32, vp, sz, i64, f32, vp, sz, vp],
                 "ccl_embedding_grad": [vp, sz, vp, sz, i64, sz, sz, i32, f32, i32, vp, sz, vp, sz, vp],
                 "ccl_plan_embedding_grad_work_bytes": [sz, sz, sz, psz],
+                "ccl_gated_ffn": [vp, vp, vp, vp, sz, sz, sz, i32, i32, vp, vp, vp, sz, vp],
+                "ccl_gated_ffn_grad": [vp, vp, vp, vp, vp, vp, sz, sz, sz, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp],
+                "ccl_plan_gated_ffn_work_bytes": [sz, sz, sz, i32, i32, psz],
+                "ccl_gated_ffn_timeouts": [ctypes.POINTER(ctypes.c_ulonglong)],
                 "ccl_distill_loss": [vp, sz, sz, sz, i32, vp, vp, sz, f32, vp, vp, vp, vp, sz, vp],
                 "ccl_distill_grad": [vp, sz, sz, sz, i32, vp, vp, sz, f32, vp, vp, vp, sz, vp],
             }
@@ -568,6 +573,72 @@ def ccl_plan_embedding_grad_work_bytes(ntokens: int, rows: int, dim: int) -> int
     _check(lib().ccl_plan_embedding_grad_work_bytes(int(ntokens), int(rows), int(dim), ctypes.byref(out)),
            "ccl_plan_embedding_grad_work_bytes")
     return out.value
+
+
+def _ffn_shapes(x, w_gate, w_up, w_down):
+    """Pointers of the block's inputs and its sizes (tokens, dim, ffn)."""
+    if x.dim() != 2 or w_gate.dim() != 2:
+        raise ValueError("x and the weights are matrices")
+    n, dim, ffn = x.shape[0], x.shape[1], w_gate.shape[0]
+    dt = x.dtype
+    return (_flat(x, "x", (n, dim), dt), _flat(w_gate, "w_gate", (ffn, dim), dt), _flat(w_up, "w_up", (ffn, dim), dt),
+            _flat(w_down, "w_down", (dim, ffn), dt)), (n, dim, ffn)
+
+
+def _act(act) -> int:
+    return ACTS[act] if isinstance(act, str) else int(act)
+
+
+def ccl_gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, out: torch.Tensor,
+                  act="silu", saved: Optional[torch.Tensor] = None, work: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """out = (act(x w_gate^T) * (x w_up^T)) w_down^T, bfloat16; w_gate, w_up
+    [ffn, dim], w_down [dim, ffn].  saved ([2, tokens, ffn], float32): kept for
+    ccl_gated_ffn_grad.  work: a device buffer of at least
+    ccl_plan_gated_ffn_work_bytes bytes (allocated here when omitted)."""
+    _on_gpu(x, w_gate, w_up, w_down, out, saved)
+    ptrs, (n, dim, ffn) = _ffn_shapes(x, w_gate, w_up, w_down)
+    op = _flat(out, "out", (n, dim), x.dtype)
+    sp = _flat(saved, "saved", (2, n, ffn), torch.float32)
+    work, nbytes = _work(work, 0 if work is not None else
+                         ccl_plan_gated_ffn_work_bytes(n, dim, ffn, False, all(q % 16 == 0 for q in ptrs)), x, stream)
+    _check(lib().ccl_gated_ffn(*ptrs, n, dim, ffn, _dtype(x), _act(act), op, sp, work.data_ptr(), nbytes,
+                               _stream(stream)), "ccl_gated_ffn")
+
+
+def ccl_gated_ffn_grad(grad_out: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                       w_down: torch.Tensor, saved: torch.Tensor, grad_x: Optional[torch.Tensor] = None,
+                       grad_w_gate: Optional[torch.Tensor] = None, grad_w_up: Optional[torch.Tensor] = None,
+                       grad_w_down: Optional[torch.Tensor] = None, act="silu", accumulate: bool = False,
+                       work: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The block's gradients (those given), from the saved pre-activations;
+    accumulate adds to the weights' gradients."""
+    _on_gpu(grad_out, x, w_gate, w_up, w_down, saved, grad_x, grad_w_gate, grad_w_up, grad_w_down)
+    ptrs, (n, dim, ffn) = _ffn_shapes(x, w_gate, w_up, w_down)
+    dt = x.dtype
+    yp = _flat(grad_out, "grad_out", (n, dim), dt)
+    sp = _flat(saved, "saved", (2, n, ffn), torch.float32)
+    grads = (_flat(grad_x, "grad_x", (n, dim), dt), _flat(grad_w_gate, "grad_w_gate", (ffn, dim), dt),
+             _flat(grad_w_up, "grad_w_up", (ffn, dim), dt), _flat(grad_w_down, "grad_w_down", (dim, ffn), dt))
+    work, nbytes = _work(work, 0 if work is not None else
+                         ccl_plan_gated_ffn_work_bytes(n, dim, ffn, True, all(q % 16 == 0 for q in (yp, *ptrs))), x,
+                         stream)
+    _check(lib().ccl_gated_ffn_grad(yp, *ptrs, sp, n, dim, ffn, _dtype(x), _act(act), int(bool(accumulate)), *grads,
+                                    work.data_ptr(), nbytes, _stream(stream)), "ccl_gated_ffn_grad")
+
+
+def ccl_plan_gated_ffn_work_bytes(ntokens: int, dim: int, ffn: int, backward: bool = False, aligned: bool = True) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().ccl_plan_gated_ffn_work_bytes(int(ntokens), int(dim), int(ffn), int(bool(backward)), int(bool(aligned)),
+                                               ctypes.byref(out)), "ccl_plan_gated_ffn_work_bytes")
+    return out.value
+
+
+def ccl_gated_ffn_timeouts() -> int:
+    """Kernels of the block that gave up waiting (0 on a sound machine); waits for the device."""
+    n = ctypes.c_ulonglong()
+    _check(lib().ccl_gated_ffn_timeouts(ctypes.byref(n)), "ccl_gated_ffn_timeouts")
+    return int(n.value)
 
 
 def ccl_distill_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, loss: torch.Tensor,

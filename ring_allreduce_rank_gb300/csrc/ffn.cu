@@ -1,0 +1,1044 @@
+// ffn.cu -- gated feed-forward block, forward and backward.
+//
+//   g = x Wg^T, u = x Wu^T, h = act(g) * u, y = h Wd^T
+//   dh = dy Wd, du = dh * act(g), dg = dh * u * act'(g)
+//   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x, dWd = dy^T h
+//
+// Every product is one kernel, ffn_gemm_kernel: a persistent grid of CTA pairs,
+// each pair computing 256 x 256 fp32 accumulators in tensor memory with
+// tcgen05.mma (cta_group::2, bf16 operands), operands brought by TMA into a
+// ring of shared-memory stages, two accumulators in turn so that one tile's
+// epilogue runs under the next tile's products.  The operands are used where
+// they lie, whichever of their dimensions is contiguous (K-major or MN-major
+// descriptors), so nothing is transposed.  The epilogues carry the activation
+// and its derivative: the forward's first product makes g and u of the same
+// 128 columns side by side in one accumulator (one CTA of the pair loads Wg's
+// rows, the other Wu's), and the backward's first product turns dh into dg,
+// du and h without dh reaching memory.  dx's two products are one longer sum,
+// and the three weight gradients are one launch.
+//
+// h, dg and du are rounded to bf16: they are operands of the next products.
+// g and u are kept in fp32 for the backward pass, since rounding them would
+// add a rounding to every factor of every gradient.
+//
+// Bound by the tensor cores for many tokens, by reading the weights for few.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+#include <vector>
+
+#include "../../include/ccl.h"
+#include "ccl_internal.h"
+#include "step_ops.cuh"
+
+namespace ccl {
+namespace {
+
+constexpr int kTileM = 256, kTileN = 256, kTileK = 64; // a CTA pair's tile
+constexpr int kOperandBytes = 128 * kTileK * 2;        // one CTA's part of A or B in a stage
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kStages = 6;
+constexpr int kGemmThreads = 384; // producer, issuer, tensor memory, one idle warp, eight epilogue warps
+constexpr int kEpiWarps = 8;
+constexpr int kGemmSmem = kStages * kStageBytes + 1024 /* alignment */;
+constexpr int kGroupM = 8; // row tiles walked before the next column tile
+constexpr int kMaxProblems = 3;
+constexpr unsigned long long kWaitLimitNs = 4000000000ull;
+
+enum Epilogue { EPI_GATED = 0, EPI_STORE = 1, EPI_BACKWARD = 2 };
+
+// One product C[M, N] = sum over segments of A_s[M, K] B_s[N, K]^T.
+struct Problem {
+    CUtensorMap a[2], b[2];
+    void *out;        // EPI_STORE: bf16, row stride N
+    float *partial;   // split sums: [splits][M][column tiles * 256]
+    uint32_t m, n;    // n: output columns (EPI_GATED: of h)
+    uint32_t mt, nt;  // tiles
+    uint32_t kblocks; // of one segment
+    uint32_t segs;
+    uint32_t units;   // mt * nt * splits
+};
+
+struct GemmParams {
+    Problem prob[kMaxProblems];
+    uint32_t nprob, splits;
+    int act, accumulate;
+    // EPI_GATED writes h and, if kept, g and u; EPI_BACKWARD reads those and writes h, dg and du
+    uint16_t *h, *dg, *du;
+    float *g, *u;
+    uint32_t ldh; // row stride of h, dg and du (g and u: n)
+};
+
+__device__ unsigned long long g_ffn_timeouts;
+
+// ------------------------------------------------------------------ PTX
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ unsigned long long now_ns()
+{
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+// Waits for the phase of the given parity; false (and the CTA's flag set, and
+// the device's counter raised) after kWaitLimitNs, or once another role gave up.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up)
+{
+    unsigned long long t0 = 0;
+    for (uint32_t n = 0;; ++n) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done)
+                     : "r"(bar), "r"(parity)
+                     : "memory");
+        if (done)
+            return true;
+        if ((n & 255) == 255) {
+            if (*gave_up)
+                return false;
+            const unsigned long long t = now_ns();
+            if (!t0) {
+                t0 = t;
+            } else if (t - t0 > kWaitLimitNs) {
+                *gave_up = 1;
+                atomicAdd(&g_ffn_timeouts, 1ull);
+                return false;
+            }
+        }
+    }
+}
+
+// A 2-D box of a tensor map into this CTA's shared memory; its bytes are
+// counted at `bar`, a barrier of the pair's first CTA.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+                 "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(map), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_commit(uint32_t bar) // arrives at `bar` in both CTAs
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_load32(uint32_t addr, float *f)
+{
+    uint32_t r[32];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        f[i] = __uint_as_float(r[i]);
+}
+
+// Shared-memory descriptor of a 128-byte-swizzled operand tile.  K-major: rows
+// of 64 k values (128 bytes), eight rows a swizzle atom (1024 bytes apart).
+// MN-major: for each 64 rows or columns of the operand, 64 k rows of 128
+// bytes; the next 64 follow 8192 bytes later.
+template <bool MN> __device__ __forceinline__ uint64_t operand_desc(uint32_t addr)
+{
+    const uint64_t lead = MN ? 8192 >> 4 : 1, stride = 1024 >> 4;
+    return (uint64_t)((addr & 0x3ffff) >> 4) | lead << 16 | stride << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// Bytes from one 16-deep step of K to the next within a tile.
+template <bool MN> __device__ __forceinline__ constexpr uint32_t k_step() { return MN ? 16 * 128 : 32; }
+
+template <bool MN> __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *map, int mn, int k, uint32_t bar)
+{
+    if (MN) {
+        tma_load(dst, map, mn, k, bar);
+        tma_load(dst + kOperandBytes / 2, map, mn + 64, k, bar);
+    } else {
+        tma_load(dst, map, k, mn, bar);
+    }
+}
+
+// ------------------------------------------------------------------ activations
+
+__device__ __forceinline__ float sigmoid(float x)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(x, -1.4426950408889634f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, e)));
+    return r;
+}
+
+// act(g) and act'(g).  SiLU: g s(g).  GELU (tanh form): 0.5 g (1 + tanh y) =
+// g s(2y), y = sqrt(2/pi) (g + 0.044715 g^3), which keeps its small values.
+__device__ __forceinline__ void activation(int act, float g, float &a, float &da)
+{
+    if (act == CCL_ACT_SILU) {
+        const float s = sigmoid(g);
+        a = g * s;
+        da = s * __fmaf_rn(g, 1.0f - s, 1.0f);
+    } else {
+        constexpr float c2 = 1.5957691216057308f; // 2 sqrt(2/pi)
+        const float gg = g * g;
+        const float s = sigmoid(c2 * g * __fmaf_rn(0.044715f, gg, 1.0f));
+        const float d = s * (1.0f - s);
+        a = g * s;
+        da = d == 0.0f ? s : __fmaf_rn(g * d, c2 * __fmaf_rn(3 * 0.044715f, gg, 1.0f), s);
+    }
+}
+
+// ------------------------------------------------------------------ epilogues
+
+// Eight bf16 values to row[col..col+8), those before column n.
+__device__ __forceinline__ void store8(uint16_t *row, uint32_t col, uint32_t n, const float *f)
+{
+    uint16_t *q = row + col;
+    if (col + 8 <= n && ((uintptr_t)q & 15) == 0) {
+        st16(q, pack<DT_BF16>(f));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i < n)
+                st_value<DT_BF16>(q, i, f[i]);
+    }
+}
+
+__device__ __forceinline__ void load8(const uint16_t *row, uint32_t col, uint32_t n, float *f)
+{
+    const uint16_t *q = row + col;
+    if (col + 8 <= n && ((uintptr_t)q & 15) == 0) {
+        unpack<DT_BF16>(ld16(q), f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = col + i < n ? ld_value<DT_BF16>(q, i) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void store8(float *row, uint32_t col, uint32_t n, const float *f)
+{
+    float *q = row + col;
+    if (col + 8 <= n && ((uintptr_t)q & 15) == 0) {
+        st16(q, pack<DT_FP32>(f));
+        st16(q + 4, pack<DT_FP32>(f + 4));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i < n)
+                gstore<float>(q + i, f[i]);
+    }
+}
+
+__device__ __forceinline__ void load8(const float *row, uint32_t col, uint32_t n, float *f)
+{
+    const float *q = row + col;
+    if (col + 8 <= n && ((uintptr_t)q & 15) == 0) {
+        unpack<DT_FP32>(ld16(q), f);
+        unpack<DT_FP32>(ld16(q + 4), f + 4);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = col + i < n ? gload<float>(q + i) : 0.0f;
+    }
+}
+
+// The finished sums of eight columns of one row: v, and for EPI_GATED g = v
+// and u = w.
+template <int EPI>
+__device__ __forceinline__ void finish8(const GemmParams &p, const Problem &q, uint32_t row, uint32_t col, float *v,
+                                        float *w)
+{
+    if (row >= q.m || col >= q.n)
+        return;
+    float a[8], da[8];
+    if (EPI == EPI_GATED) {
+        if (p.g) {
+            store8(p.g + (uint64_t)row * q.n, col, q.n, v);
+            store8(p.u + (uint64_t)row * q.n, col, q.n, w);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            activation(p.act, v[i], a[i], da[i]);
+            a[i] *= w[i];
+        }
+        store8(p.h + (uint64_t)row * p.ldh, col, q.n, a);
+    } else if (EPI == EPI_BACKWARD) {
+        float g[8], u[8];
+        load8(p.g + (uint64_t)row * q.n, col, q.n, g);
+        load8(p.u + (uint64_t)row * q.n, col, q.n, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            activation(p.act, g[i], a[i], da[i]);
+            g[i] = v[i] * u[i] * da[i]; // dg
+            v[i] = v[i] * a[i];         // du
+            a[i] = a[i] * u[i];         // h
+        }
+        store8(p.h + (uint64_t)row * p.ldh, col, q.n, a);
+        store8(p.dg + (uint64_t)row * p.ldh, col, q.n, g);
+        store8(p.du + (uint64_t)row * p.ldh, col, q.n, v);
+    } else {
+        uint16_t *out = static_cast<uint16_t *>(q.out) + (uint64_t)row * q.n;
+        if (p.accumulate) {
+            load8(out, col, q.n, a);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = __fadd_rn(a[i], v[i]);
+        }
+        store8(out, col, q.n, v);
+    }
+}
+
+// ------------------------------------------------------------------ the product
+
+struct Unit {
+    uint32_t prob, split, m, n, kb0, kb1;
+};
+
+__device__ __forceinline__ Unit unit_at(const GemmParams &p, uint32_t i)
+{
+    Unit u;
+    u.prob = 0;
+    while (i >= p.prob[u.prob].units)
+        i -= p.prob[u.prob++].units;
+    const Problem &q = p.prob[u.prob];
+    const uint32_t tiles = q.mt * q.nt;
+    u.split = i / tiles;
+    const uint32_t t = i % tiles, per = kGroupM * q.nt, grp = t / per, in = t % per;
+    const uint32_t gm = min(q.mt - grp * kGroupM, (uint32_t)kGroupM);
+    u.m = grp * kGroupM + in % gm;
+    u.n = in / gm;
+    const uint32_t kb = q.kblocks * q.segs;
+    u.kb0 = (uint32_t)((uint64_t)kb * u.split / p.splits);
+    u.kb1 = (uint32_t)((uint64_t)kb * (u.split + 1) / p.splits);
+    return u;
+}
+
+template <int EPI, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_constant__ GemmParams p)
+{
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t bars[2 * kStages + 4];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int gave_up;
+    const uint32_t stages = (smem_u32(raw) + 1023) & ~1023u;
+    const uint32_t full = smem_u32(&bars[0]), empty = smem_u32(&bars[kStages]);
+    const uint32_t acc_full = smem_u32(&bars[2 * kStages]), acc_empty = smem_u32(&bars[2 * kStages + 2]);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + 8 * i, 1);
+            mbar_init(acc_empty + 8 * i, 2 * kEpiWarps);
+        }
+        gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = tmem_slot;
+    chain_entry();
+
+    uint32_t total = 0;
+    for (uint32_t i = 0; i < p.nprob; ++i)
+        total += p.prob[i].units;
+
+    if (warp == 0 && lane == 0) {
+        // producer: this CTA's halves of A and B, stage by stage
+        const uint32_t leader_full = in_cta(full, 0);
+        uint32_t s = 0, phase = 0;
+        bool ok = true;
+        for (uint32_t i = pair; ok && i < total; i += pairs) {
+            const Unit u = unit_at(p, i);
+            const Problem &q = p.prob[u.prob];
+            const int am = (int)(u.m * kTileM + rank * 128);
+            const int bn = EPI == EPI_GATED ? (int)(u.n * 128) : (int)(u.n * kTileN + rank * 128);
+            for (uint32_t kb = u.kb0; kb < u.kb1; ++kb) {
+                if (!(ok = mbar_wait(empty + 8 * s, phase ^ 1, &gave_up)))
+                    break;
+                if (rank == 0)
+                    mbar_expect(full + 8 * s, 2 * kStageBytes);
+                const uint32_t seg = kb >= q.kblocks ? 1 : 0;
+                const int k = (int)((kb - seg * q.kblocks) * kTileK);
+                const uint32_t at = stages + s * kStageBytes;
+                const CUtensorMap *b = EPI == EPI_GATED ? &q.b[rank] : &q.b[seg];
+                load_operand<A_MN>(at, &q.a[seg], am, k, leader_full + 8 * s);
+                load_operand<B_MN>(at + kOperandBytes, b, bn, k, leader_full + 8 * s);
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        // the issuer's last arrivals reach both CTAs while they are here
+        for (int i = 0; ok && i < kStages; ++i) {
+            ok = mbar_wait(empty + 8 * s, phase ^ 1, &gave_up);
+            if (++s == kStages) {
+                s = 0;
+                phase ^= 1;
+            }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // issuer: fp32 accumulator, bf16 operands, their majorness, N, M
+        const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (A_MN ? 1u << 15 : 0) | (B_MN ? 1u << 16 : 0) |
+                               (kTileN >> 3) << 17 | (kTileM >> 4) << 24;
+        uint32_t s = 0, phase = 0, t = 0;
+        bool ok = true;
+        for (uint32_t i = pair; ok && i < total; i += pairs, ++t) {
+            const Unit u = unit_at(p, i);
+            const uint32_t buf = t & 1;
+            if (!(ok = mbar_wait(acc_empty + 8 * buf, ((t >> 1) & 1) ^ 1, &gave_up)))
+                break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            for (uint32_t kb = u.kb0; kb < u.kb1; ++kb) {
+                if (!(ok = mbar_wait(full + 8 * s, phase, &gave_up)))
+                    break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t at = stages + s * kStageBytes;
+#pragma unroll
+                for (int k = 0; k < kTileK / 16; ++k)
+                    tc_mma(tmem + buf * kTileN, operand_desc<A_MN>(at + k * k_step<A_MN>()),
+                           operand_desc<B_MN>(at + kOperandBytes + k * k_step<B_MN>()), idesc, kb > u.kb0 || k > 0);
+                tc_commit(empty + 8 * s);
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1;
+                }
+            }
+            if (ok)
+                tc_commit(acc_full + 8 * buf);
+        }
+    } else if (warp >= 4) {
+        // epilogue: warp w reads lanes 32 (w % 4) .. + 32 and half of the columns
+        const uint32_t half = (warp - 4) / 4;
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32;
+        const uint32_t leader_empty = in_cta(acc_empty, 0);
+        uint32_t t = 0;
+        for (uint32_t i = pair; i < total; i += pairs, ++t) {
+            const Unit u = unit_at(p, i);
+            const Problem &q = p.prob[u.prob];
+            const uint32_t buf = t & 1;
+            if (!__all_sync(0xffffffffu, mbar_wait(acc_full + 8 * buf, (t >> 1) & 1, &gave_up)))
+                break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t row = u.m * kTileM + rank * 128 + lanes + lane;
+            const uint32_t acc = tmem + buf * kTileN + (lanes << 16);
+            if (p.splits > 1) {
+                const uint64_t width = (uint64_t)q.nt * kTileN;
+                float *out = q.partial + ((uint64_t)u.split * q.m + row) * width + u.n * kTileN;
+                for (uint32_t c = half * 128; c < half * 128 + 128; c += 32) {
+                    float v[32];
+                    tc_load32(acc + c, v);
+                    if (row < q.m)
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            st16(out + c + j, pack<DT_FP32>(v + j));
+                }
+            } else if (EPI == EPI_GATED) {
+                for (uint32_t c = half * 64; c < half * 64 + 64; c += 32) {
+                    float v[32], w[32];
+                    tc_load32(acc + c, v);
+                    tc_load32(acc + 128 + c, w);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8)
+                        finish8<EPI>(p, q, row, u.n * 128 + c + j, v + j, w + j);
+                }
+            } else {
+                for (uint32_t c = half * 128; c < half * 128 + 128; c += 32) {
+                    float v[32];
+                    tc_load32(acc + c, v);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8)
+                        finish8<EPI>(p, q, row, u.n * kTileN + c + j, v + j, v + j);
+                }
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster(leader_empty + 8 * buf);
+        }
+    }
+    __syncwarp();
+    if (gave_up) // copies still in flight land before the CTA's memory is given back
+        for (int i = 0; i < 1000; ++i)
+            __nanosleep(1000);
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// ------------------------------------------------------------------ split sums
+
+// The splits' sums of one product, added in order, eight columns a thread.
+template <int EPI> __global__ void __launch_bounds__(256) ffn_join_kernel(const __grid_constant__ GemmParams p)
+{
+    chain_entry();
+    for (uint32_t i = 0; i < p.nprob; ++i) {
+        const Problem &q = p.prob[i];
+        const uint32_t cols = (q.n + 7) / 8;
+        const uint64_t width = (uint64_t)q.nt * kTileN, slab = (uint64_t)q.m * width;
+        for (uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x; e < (uint64_t)q.m * cols; e += (uint64_t)gridDim.x * 256) {
+            const uint32_t row = (uint32_t)(e / cols), col = (uint32_t)(e % cols) * 8;
+            // EPI_GATED: 128 columns of g, then the same of u, in each tile
+            const uint64_t at = row * width + (EPI == EPI_GATED ? col / 128 * 256 + col % 128 : col);
+            float v[8], w[8], f[8];
+            load8(q.partial + at, 0, 8, v);
+            if (EPI == EPI_GATED)
+                load8(q.partial + at + 128, 0, 8, w);
+            for (uint32_t s = 1; s < p.splits; ++s) {
+                load8(q.partial + s * slab + at, 0, 8, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] = __fadd_rn(v[j], f[j]);
+                if (EPI == EPI_GATED) {
+                    load8(q.partial + s * slab + at + 128, 0, 8, f);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        w[j] = __fadd_rn(w[j], f[j]);
+                }
+            }
+            finish8<EPI>(p, q, row, col, v, w);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ operands TMA cannot address
+
+struct PackParams {
+    const uint16_t *src;
+    uint16_t *dst;
+    uint64_t rows;
+    uint32_t cols, ld;
+};
+
+// Rows of `cols` elements to rows `ld` apart (ld a multiple of 8).
+__global__ void __launch_bounds__(256) ffn_pack_kernel(PackParams p)
+{
+    chain_entry();
+    for (uint64_t r = blockIdx.x; r < p.rows; r += gridDim.x)
+        for (uint32_t c = threadIdx.x; c < p.cols; c += 256)
+            gstore<uint16_t>(p.dst + r * p.ld + c, gload<uint16_t>(p.src + r * p.cols + c));
+}
+
+// ------------------------------------------------------------------ host side
+
+struct Matrix { // a row-major bf16 operand as TMA sees it
+    const void *ptr;
+    uint64_t rows, cols, ld;
+};
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return fn;
+}
+
+// A map whose boxes are 64 columns wide: as K-major operand tiles (128 rows of
+// 64 k values) or as MN-major ones (64 k rows of 64 values).  What lies
+// outside the matrix reads as zero.
+bool encode(CUtensorMap *map, const Matrix &m, bool mn)
+{
+    const cuuint64_t dim[2] = {m.cols, m.rows}, stride[1] = {m.ld * 2};
+    const cuuint32_t box[2] = {64, mn ? 64u : 128u}, step[2] = {1, 1};
+    return encode_fn() &&
+           encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(m.ptr), dim, stride, box, step,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+uint32_t tiles_of(uint64_t n, uint32_t t) { return (uint32_t)((n + t - 1) / t); }
+
+constexpr int kPairs = 76; // CTA pairs of the GPU's 152 SMs
+constexpr uint32_t kMaxSplits = 16;
+
+// How many parts the sum over K is cut into: the number that minimises the
+// rounds of CTA pairs times a part's length, plus the join's traffic.  A
+// block of K takes about 0.35 us a pair, a tile's fill and epilogue about 3,
+// a join about 4 and its bytes at 6 TB/s.  Few tiles (few tokens, narrow
+// layers) would otherwise leave most SMs idle.
+uint32_t choose_splits(uint64_t tiles, uint64_t kblocks, uint64_t partial_bytes)
+{
+    uint32_t best = 1;
+    double cost = 0;
+    for (uint32_t s = 1; s <= kMaxSplits && s <= kblocks; ++s) {
+        const double rounds = (double)((tiles * s + kPairs - 1) / kPairs);
+        const double c = rounds * ((double)((kblocks + s - 1) / s) * 0.35 + 3.0) + (s > 1 ? 4.0 + 2.0 * s * (double)partial_bytes / 6e6 : 0.0);
+        if (s == 1 || c < cost * 0.97) {
+            best = s;
+            cost = c;
+        }
+    }
+    return best;
+}
+
+// The products of a pass: problem sizes, splits and partial sums.
+struct Shape {
+    uint64_t m, n, k;
+    uint32_t segs;
+};
+struct Launch {
+    Shape s[kMaxProblems];
+    int n;
+    bool gated;
+    uint32_t splits;
+    size_t partial; // bytes of all splits
+    void plan()
+    {
+        uint64_t tiles = 0, kb = 0;
+        size_t bytes = 0;
+        for (int i = 0; i < n; ++i) {
+            tiles += (uint64_t)tiles_of(s[i].m, kTileM) * tiles_of(s[i].n, gated ? 128 : kTileN);
+            kb = std::max<uint64_t>(kb, (uint64_t)tiles_of(s[i].k, kTileK) * s[i].segs);
+            bytes += up(s[i].m * (size_t)tiles_of(s[i].n, gated ? 128 : kTileN) * kTileN * 4);
+        }
+        splits = choose_splits(tiles, kb, bytes);
+        partial = splits > 1 ? bytes * splits : 0;
+    }
+};
+
+struct FfnPlan {
+    uint64_t t, d, f, dp, fp; // tokens, model width, inner width, padded widths
+    bool pack_d, pack_f, pack_all;
+    Launch up_, down, dh, dx, dw;
+    // offsets into the work buffer
+    size_t h, dg, du, x, wg, wu, wd, dy, partial, bytes;
+};
+
+constexpr uint64_t kMaxTokens = 0x7fffff00, kMaxWidth = 1 << 24;
+
+bool make_plan(size_t t, size_t d, size_t f, bool backward, bool aligned, FfnPlan *p)
+{
+    if (t > kMaxTokens || d > kMaxWidth || f > kMaxWidth || t * std::max(d, f) > (1ull << 44) || (uint64_t)d * f > (1ull << 44))
+        return false;
+    *p = FfnPlan{};
+    p->t = t;
+    p->d = d;
+    p->f = f;
+    p->dp = (d + 7) / 8 * 8;
+    p->fp = (f + 7) / 8 * 8;
+    const bool pd = p->dp != d || !aligned, pf = p->fp != f || !aligned;
+    p->up_ = Launch{{{t, f, d, 1}}, 1, true, 1, 0};
+    p->down = Launch{{{t, d, f, 1}}, 1, false, 1, 0};
+    p->dh = Launch{{{t, f, d, 1}}, 1, false, 1, 0};
+    p->dx = Launch{{{t, d, f, 2}}, 1, false, 1, 0};
+    p->dw = Launch{{{f, d, t, 1}, {f, d, t, 1}, {d, f, t, 1}}, 3, false, 1, 0};
+    size_t at = 0, partial = 0;
+    auto take = [&](size_t n) {
+        const size_t o = at;
+        at += up(n);
+        return o;
+    };
+    p->h = take(t * p->fp * 2);
+    if (backward) {
+        p->dg = take(t * p->fp * 2);
+        p->du = take(t * p->fp * 2);
+    }
+    if (pd) {
+        p->x = take(t * p->dp * 2);
+        p->wg = take(f * p->dp * 2);
+        p->wu = take(f * p->dp * 2);
+        if (backward)
+            p->dy = take(t * p->dp * 2);
+    }
+    if (pf)
+        p->wd = take(d * p->fp * 2);
+    for (Launch *l : {&p->up_, &p->down, &p->dh, &p->dx, &p->dw}) {
+        l->plan();
+        partial = std::max(partial, l->partial);
+    }
+    p->partial = take(partial);
+    p->bytes = at;
+    return true;
+}
+
+cudaError_t launch_pack(const void *src, void *dst, uint64_t rows, uint64_t cols, uint64_t ld, cudaStream_t stream)
+{
+    const PackParams p{static_cast<const uint16_t *>(src), static_cast<uint16_t *>(dst), rows, (uint32_t)cols, (uint32_t)ld};
+    const cudaError_t e = launch_chained(ffn_pack_kernel, dim3((unsigned)std::min<uint64_t>(rows, 8 * 152)), dim3(256), 0, stream, p);
+    if (e == cudaSuccess)
+        count_launches(1);
+    return e;
+}
+
+// The operand as it lies where TMA can address it (16-byte aligned base and
+// rows), else copied to rows of a padded stride.
+cudaError_t operand(const void *src, uint64_t rows, uint64_t cols, uint64_t ld, char *work, size_t at, Matrix *m,
+                    cudaStream_t stream)
+{
+    if ((uintptr_t)src % 16 == 0 && cols == ld) {
+        *m = Matrix{src, rows, cols, cols};
+        return cudaSuccess;
+    }
+    *m = Matrix{work + at, rows, cols, ld};
+    return launch_pack(src, work + at, rows, cols, ld, stream);
+}
+
+template <int EPI, bool A_MN, bool B_MN> cudaError_t launch_gemm(GemmParams &p, const Launch &l, char *partial, cudaStream_t stream)
+{
+    uint64_t units = 0;
+    p.nprob = 0;
+    p.splits = l.splits;
+    for (int i = 0; i < l.n; ++i) {
+        Problem &q = p.prob[i];
+        const Shape &s = l.s[i];
+        q.m = (uint32_t)s.m;
+        q.n = (uint32_t)s.n;
+        q.mt = tiles_of(s.m, kTileM);
+        q.nt = tiles_of(s.n, l.gated ? 128 : kTileN);
+        q.kblocks = tiles_of(s.k, kTileK);
+        q.segs = s.segs;
+        if ((uint64_t)q.mt * q.nt * l.splits > 0x3fffffff)
+            return cudaErrorInvalidValue;
+        q.units = q.mt * q.nt * l.splits;
+        q.partial = reinterpret_cast<float *>(partial);
+        partial += up(s.m * (size_t)q.nt * kTileN * 4) * l.splits;
+        units += q.units;
+        ++p.nprob;
+    }
+    // opt in to the shared memory, once per device (idempotent)
+    static std::atomic<unsigned long long> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(ffn_gemm_kernel<EPI, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
+        if (e != cudaSuccess)
+            return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)std::min<uint64_t>(units, kPairs));
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = kGemmSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if ((e = cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<EPI, A_MN, B_MN>, p)) != cudaSuccess)
+        return e;
+    count_launches(1);
+    if (l.splits > 1) {
+        uint64_t items = 0;
+        for (int i = 0; i < l.n; ++i)
+            items = std::max<uint64_t>(items, l.s[i].m * ((l.s[i].n + 7) / 8));
+        const dim3 grid((unsigned)std::min<uint64_t>((items + 255) / 256, 8 * 152));
+        if ((e = launch_chained(ffn_join_kernel<EPI>, grid, dim3(256), 0, stream, p)) != cudaSuccess)
+            return e;
+        count_launches(1);
+    }
+    return cudaSuccess;
+}
+
+struct FfnArgs {
+    const void *x, *wg, *wu, *wd;
+    size_t t, d, f;
+    ccl_dtype_t dtype;
+    ccl_act_t act;
+    float *saved;
+    void *work;
+    size_t work_bytes;
+};
+
+// The checks that both directions share; on CCL_OK `plan` is ready.
+ccl_status_t check_ffn(const FfnArgs &a, bool backward, bool aligned, FfnPlan *plan)
+{
+    if (!valid_dtype(a.dtype) || (a.act != CCL_ACT_SILU && a.act != CCL_ACT_GELU_TANH))
+        return CCL_ERR_INVALID_ARG;
+    if (a.dtype != CCL_BF16)
+        return CCL_ERR_UNSUPPORTED;
+    if (!make_plan(a.t, a.d, a.f, backward, aligned, plan))
+        return CCL_ERR_INVALID_ARG;
+    return CCL_OK;
+}
+
+bool aligned_all(std::initializer_list<const void *> ps)
+{
+    for (const void *p : ps)
+        if ((uintptr_t)p % 16)
+            return false;
+    return true;
+}
+
+#ifdef CCL_DEBUG_BOUNDS
+cudaError_t dbg_ffn(const std::vector<Range> &w, const std::vector<Range> &r, cudaStream_t stream)
+{
+    std::vector<DbgRange> v;
+    for (const std::vector<Range> *s : {&w, &r})
+        for (const Range &x : *s)
+            v.push_back(DbgRange{reinterpret_cast<const void *>(x.lo), (size_t)(x.hi - x.lo)});
+    return dbg_set_ranges(v, stream);
+}
+#define CCL_DBG_FFN(w, r, st)                                                                                          \
+    do {                                                                                                               \
+        if (cudaError_t e_ = dbg_ffn(w, r, st))                                                                        \
+            return from_cuda(e_);                                                                                      \
+    } while (0)
+#else
+#define CCL_DBG_FFN(w, r, st)                                                                                          \
+    do {                                                                                                               \
+    } while (0)
+#endif
+
+ccl_status_t gated_ffn_impl(const FfnArgs &a, void *out, cudaStream_t stream)
+{
+    FfnPlan pl;
+    if (ccl_status_t st = check_ffn(a, false, aligned_all({a.x, a.wg, a.wu, a.wd}), &pl))
+        return st;
+    if (a.t == 0 || a.d == 0)
+        return CCL_OK;
+    if (!a.x || !out || (a.f && (!a.wg || !a.wu || !a.wd)) || (a.saved && (uintptr_t)a.saved % 4))
+        return CCL_ERR_INVALID_ARG;
+    if (a.f == 0)
+        return from_cuda(cudaMemsetAsync(out, 0, a.t * a.d * 2, stream));
+    if (!a.work || (uintptr_t)a.work % 256 || a.work_bytes < pl.bytes)
+        return CCL_ERR_INVALID_ARG;
+    std::vector<Range> w{range_of(out, a.t * a.d * 2, 0), range_of(a.work, pl.bytes, 0)};
+    if (a.saved)
+        w.push_back(range_of(a.saved, 2 * a.t * a.f * 4, 0));
+    const std::vector<Range> r{range_of(a.x, a.t * a.d * 2, 0), range_of(a.wg, a.f * a.d * 2, 0),
+                               range_of(a.wu, a.f * a.d * 2, 0), range_of(a.wd, a.d * a.f * 2, 0)};
+    if (ccl_status_t st = check_overlaps(w, r, [](const Range &, const Range &) { return false; }))
+        return st;
+    CCL_DBG_FFN(w, r, stream);
+    char *work = static_cast<char *>(a.work);
+    Matrix x, wg, wu, wd;
+    cudaError_t e;
+    if ((e = operand(a.x, a.t, a.d, pl.dp, work, pl.x, &x, stream)) || (e = operand(a.wg, a.f, a.d, pl.dp, work, pl.wg, &wg, stream)) ||
+        (e = operand(a.wu, a.f, a.d, pl.dp, work, pl.wu, &wu, stream)) || (e = operand(a.wd, a.d, a.f, pl.fp, work, pl.wd, &wd, stream)))
+        return from_cuda(e);
+    const Matrix h{work + pl.h, a.t, a.f, pl.fp};
+    GemmParams p{};
+    p.act = (int)a.act;
+    p.h = reinterpret_cast<uint16_t *>(work + pl.h);
+    p.g = a.saved;
+    p.u = a.saved ? a.saved + a.t * a.f : nullptr;
+    p.ldh = (uint32_t)pl.fp;
+    if (!encode(&p.prob[0].a[0], x, false) || !encode(&p.prob[0].b[0], wg, false) || !encode(&p.prob[0].b[1], wu, false))
+        return CCL_ERR_CUDA;
+    if ((e = launch_gemm<EPI_GATED, false, false>(p, pl.up_, work + pl.partial, stream)))
+        return from_cuda(e);
+    p.prob[0].out = out;
+    if (!encode(&p.prob[0].a[0], h, false) || !encode(&p.prob[0].b[0], wd, false))
+        return CCL_ERR_CUDA;
+    return from_cuda(launch_gemm<EPI_STORE, false, false>(p, pl.down, work + pl.partial, stream));
+}
+
+ccl_status_t gated_ffn_grad_impl(const FfnArgs &a, const void *dy, void *dx, void *dwg, void *dwu, void *dwd,
+                                 int accumulate, cudaStream_t stream)
+{
+    FfnPlan pl;
+    if (ccl_status_t st = check_ffn(a, true, aligned_all({a.x, a.wg, a.wu, a.wd, dy}), &pl))
+        return st;
+    if (a.d == 0 || (a.t == 0 && accumulate))
+        return CCL_OK;
+    const size_t tb = a.t * a.d * 2, wb = a.f * a.d * 2;
+    if ((a.t && (!a.x || !dy || (a.f && (!a.wg || !a.wu || !a.wd || !a.saved)))) || (uintptr_t)a.saved % 4)
+        return CCL_ERR_INVALID_ARG;
+    const bool empty = a.t == 0 || a.f == 0;
+    if (!empty && (!a.work || (uintptr_t)a.work % 256 || a.work_bytes < pl.bytes))
+        return CCL_ERR_INVALID_ARG;
+    std::vector<Range> w, r;
+    if (!empty) {
+        w.push_back(range_of(a.work, pl.bytes, 0));
+        r = {range_of(a.x, tb, 0), range_of(dy, tb, 0), range_of(a.wg, wb, 0), range_of(a.wu, wb, 0),
+             range_of(a.wd, wb, 0), range_of(a.saved, 2 * a.t * a.f * 4, 0)};
+    }
+    if (dx)
+        w.push_back(range_of(dx, tb, 0));
+    for (void *g : {dwg, dwu, dwd})
+        if (g)
+            w.push_back(range_of(g, wb, 0));
+    if (ccl_status_t st = check_overlaps(w, r, [](const Range &, const Range &) { return false; }))
+        return st;
+    if (!dx && !dwg && !dwu && !dwd)
+        return CCL_OK;
+    cudaError_t e;
+    if (empty) { // empty sums
+        if (dx && tb && (e = cudaMemsetAsync(dx, 0, tb, stream)))
+            return from_cuda(e);
+        for (void *g : {dwg, dwu, dwd})
+            if (g && wb && !accumulate && (e = cudaMemsetAsync(g, 0, wb, stream)))
+                return from_cuda(e);
+        return CCL_OK;
+    }
+    CCL_DBG_FFN(w, r, stream);
+    char *work = static_cast<char *>(a.work);
+    Matrix x, wg, wu, wd, y;
+    if ((e = operand(a.x, a.t, a.d, pl.dp, work, pl.x, &x, stream)) || (e = operand(a.wg, a.f, a.d, pl.dp, work, pl.wg, &wg, stream)) ||
+        (e = operand(a.wu, a.f, a.d, pl.dp, work, pl.wu, &wu, stream)) || (e = operand(a.wd, a.d, a.f, pl.fp, work, pl.wd, &wd, stream)) ||
+        (e = operand(dy, a.t, a.d, pl.dp, work, pl.dy, &y, stream)))
+        return from_cuda(e);
+    const Matrix h{work + pl.h, a.t, a.f, pl.fp}, dg{work + pl.dg, a.t, a.f, pl.fp}, du{work + pl.du, a.t, a.f, pl.fp};
+    GemmParams p{};
+    p.act = (int)a.act;
+    p.h = reinterpret_cast<uint16_t *>(work + pl.h);
+    p.dg = reinterpret_cast<uint16_t *>(work + pl.dg);
+    p.du = reinterpret_cast<uint16_t *>(work + pl.du);
+    p.g = a.saved;
+    p.u = a.saved + a.t * a.f;
+    p.ldh = (uint32_t)pl.fp;
+    if (!encode(&p.prob[0].a[0], y, false) || !encode(&p.prob[0].b[0], wd, true))
+        return CCL_ERR_CUDA;
+    if ((e = launch_gemm<EPI_BACKWARD, false, true>(p, pl.dh, work + pl.partial, stream)))
+        return from_cuda(e);
+    if (dx) {
+        p.prob[0].out = dx;
+        if (!encode(&p.prob[0].a[0], dg, false) || !encode(&p.prob[0].a[1], du, false) ||
+            !encode(&p.prob[0].b[0], wg, true) || !encode(&p.prob[0].b[1], wu, true))
+            return CCL_ERR_CUDA;
+        if ((e = launch_gemm<EPI_STORE, false, true>(p, pl.dx, work + pl.partial, stream)))
+            return from_cuda(e);
+    }
+    if (!dwg && !dwu && !dwd)
+        return CCL_OK;
+    // the weight gradients asked for, in one launch
+    p.accumulate = accumulate != 0;
+    Launch l = pl.dw;
+    l.n = 0;
+    const Matrix *am[3] = {&dg, &du, &y}, *bm[3] = {&x, &x, &h};
+    void *out[3] = {dwg, dwu, dwd};
+    for (int i = 0; i < 3; ++i)
+        if (out[i]) {
+            l.s[l.n] = pl.dw.s[i];
+            p.prob[l.n].out = out[i];
+            if (!encode(&p.prob[l.n].a[0], *am[i], true) || !encode(&p.prob[l.n].b[0], *bm[i], true))
+                return CCL_ERR_CUDA;
+            ++l.n;
+        }
+    return from_cuda(launch_gemm<EPI_STORE, true, true>(p, l, work + pl.partial, stream));
+}
+
+} // namespace
+} // namespace ccl
+
+using namespace ccl;
+
+extern "C" {
+
+ccl_status_t ccl_plan_gated_ffn_work_bytes(size_t ntokens, size_t dim, size_t ffn, int backward, int aligned, size_t *bytes)
+{
+    FfnPlan p;
+    if (!bytes || !make_plan(ntokens, dim, ffn, backward != 0, aligned != 0, &p))
+        return CCL_ERR_INVALID_ARG;
+    *bytes = p.bytes;
+    return CCL_OK;
+}
+
+ccl_status_t ccl_gated_ffn(const void *x, const void *w_gate, const void *w_up, const void *w_down, size_t ntokens,
+                           size_t dim, size_t ffn, ccl_dtype_t dtype, ccl_act_t act, void *out, float *saved, void *work,
+                           size_t work_bytes, cudaStream_t stream)
+{
+    TraceScope tr("gated_ffn", 1, ntokens, (int)dtype, -1, (int)act, stream);
+    return tr.done(guarded([&] {
+        return gated_ffn_impl(FfnArgs{x, w_gate, w_up, w_down, ntokens, dim, ffn, dtype, act, saved, work, work_bytes},
+                              out, stream);
+    }));
+}
+
+ccl_status_t ccl_gated_ffn_grad(const void *grad_out, const void *x, const void *w_gate, const void *w_up,
+                                const void *w_down, const float *saved, size_t ntokens, size_t dim, size_t ffn,
+                                ccl_dtype_t dtype, ccl_act_t act, int accumulate, void *grad_x, void *grad_w_gate,
+                                void *grad_w_up, void *grad_w_down, void *work, size_t work_bytes, cudaStream_t stream)
+{
+    TraceScope tr("gated_ffn_grad", 1, ntokens, (int)dtype, -1, (int)act, stream);
+    return tr.done(guarded([&] {
+        return gated_ffn_grad_impl(FfnArgs{x, w_gate, w_up, w_down, ntokens, dim, ffn, dtype, act,
+                                           const_cast<float *>(saved), work, work_bytes},
+                                   grad_out, grad_x, grad_w_gate, grad_w_up, grad_w_down, accumulate, stream);
+    }));
+}
+
+ccl_status_t ccl_gated_ffn_timeouts(unsigned long long *count)
+{
+    if (!count)
+        return CCL_ERR_INVALID_ARG;
+    return from_cuda(cudaMemcpyFromSymbol(count, g_ffn_timeouts, sizeof *count));
+}
+
+} // extern "C"
