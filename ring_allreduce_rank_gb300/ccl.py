@@ -49,6 +49,8 @@ class CclError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libccl.so (built in-tree); raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             # CCL_LIBRARY: another build of this library to load (the
@@ -493,14 +495,24 @@ class CclBucketer:
 
 def _rows(t: torch.Tensor, name: str, cols: Optional[int] = None, dtype: Optional[torch.dtype] = None):
     """(pointer, rows, columns, row stride) of a matrix with contiguous rows."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError("%s must be a matrix with contiguous rows" % name)
-    if cols is not None and t.shape[1] != cols:
-        raise ValueError("%s has %d columns, expected %d" % (name, t.shape[1], cols))
+    n, c = shape
+    stride = c
+    if not t.is_contiguous():
+        s0, s1 = t.stride()
+        if c > 1 and s1 != 1:
+            raise ValueError("%s must be a matrix with contiguous rows" % name)
+        if n > 1:  # the stride of a single row says nothing
+            stride = max(s0, c)
+            if s0 < c:
+                raise ValueError("%s has overlapping rows" % name)
+    if cols is not None and c != cols:
+        raise ValueError("%s has %d columns, expected %d" % (name, c, cols))
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    # the stride of fewer than two rows says nothing
-    return t.data_ptr(), t.shape[0], t.shape[1], max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), n, c, stride
 
 
 def _flat(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype):
@@ -509,21 +521,35 @@ def _flat(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype):
         return None
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous tensor of shape %s" % (name, tuple(shape)))
     return t.data_ptr()
 
 
-def _on_gpu(*ts: Optional[torch.Tensor]) -> None:
-    dev = None
+def _on_gpu(*ts: Optional[torch.Tensor]) -> int:
+    """The one device that all the tensors are on."""
+    dev = -1
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
+        d = t.get_device()
+        if d < 0:
             raise ValueError("the operators take CUDA tensors")
-        if dev is not None and t.device != dev:
+        if dev >= 0 and d != dev:
             raise ValueError("the tensors are on different devices")
-        dev = t.device
+        dev = d
+    return dev
+
+
+# the current stream's handle without a Stream object around it, which costs
+# more than a small kernel's launch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, device: int):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return _stream(stream)
 
 
 def _work(work: Optional[torch.Tensor], nbytes: int, like: torch.Tensor, stream):
@@ -543,12 +569,12 @@ def ccl_embedding(table: torch.Tensor, ids: torch.Tensor, out: torch.Tensor, sca
                   stream=None) -> None:
     """out[t] = scale * table[ids[t] - first_row]; zeros for an id outside the
     table's rows (padding, or another rank's shard of the vocabulary)."""
-    _on_gpu(table, ids, out)
+    dev = _on_gpu(table, ids, out)
     tp, rows, dim, ts = _rows(table, "table")
     op, n, _, os_ = _rows(out, "out", dim, table.dtype)
     ip = _flat(ids, "ids", (n,), torch.int64)
     _check(lib().ccl_embedding(tp, rows, dim, ts, _dtype(table), ip, n, int(first_row), float(scale), op, os_,
-                               _stream(stream)), "ccl_embedding")
+                               _stream_on(stream, dev)), "ccl_embedding")
 
 
 def ccl_embedding_grad(grad_out: torch.Tensor, ids: torch.Tensor, grad_table: torch.Tensor, scale: float = 1.0,
@@ -557,14 +583,14 @@ def ccl_embedding_grad(grad_out: torch.Tensor, ids: torch.Tensor, grad_table: to
     """grad_table[v] = [grad_table[v] +] scale * the sum of grad_out[t] over
     the tokens with ids[t] == first_row + v.  work: a device buffer of at least
     ccl_plan_embedding_grad_work_bytes bytes (allocated here when omitted)."""
-    _on_gpu(grad_out, ids, grad_table)
+    dev = _on_gpu(grad_out, ids, grad_table)
     gp, n, dim, gs = _rows(grad_out, "grad_out")
     tp, rows, _, ts = _rows(grad_table, "grad_table", dim, grad_out.dtype)
     ip = _flat(ids, "ids", (n,), torch.int64)
     work, nbytes = _work(work, 0 if work is not None else ccl_plan_embedding_grad_work_bytes(n, rows, dim), grad_out,
                          stream)
     _check(lib().ccl_embedding_grad(gp, gs, ip, n, int(first_row), rows, dim, _dtype(grad_out), float(scale),
-                                    int(bool(accumulate)), tp, ts, work.data_ptr(), nbytes, _stream(stream)),
+                                    int(bool(accumulate)), tp, ts, work.data_ptr(), nbytes, _stream_on(stream, dev)),
            "ccl_embedding_grad")
 
 
@@ -596,14 +622,14 @@ def ccl_gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_d
     [ffn, dim], w_down [dim, ffn].  saved ([2, tokens, ffn], float32): kept for
     ccl_gated_ffn_grad.  work: a device buffer of at least
     ccl_plan_gated_ffn_work_bytes bytes (allocated here when omitted)."""
-    _on_gpu(x, w_gate, w_up, w_down, out, saved)
+    dev = _on_gpu(x, w_gate, w_up, w_down, out, saved)
     ptrs, (n, dim, ffn) = _ffn_shapes(x, w_gate, w_up, w_down)
     op = _flat(out, "out", (n, dim), x.dtype)
     sp = _flat(saved, "saved", (2, n, ffn), torch.float32)
     work, nbytes = _work(work, 0 if work is not None else
                          ccl_plan_gated_ffn_work_bytes(n, dim, ffn, False, all(q % 16 == 0 for q in ptrs)), x, stream)
     _check(lib().ccl_gated_ffn(*ptrs, n, dim, ffn, _dtype(x), _act(act), op, sp, work.data_ptr(), nbytes,
-                               _stream(stream)), "ccl_gated_ffn")
+                               _stream_on(stream, dev)), "ccl_gated_ffn")
 
 
 def ccl_gated_ffn_grad(grad_out: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
@@ -613,7 +639,7 @@ def ccl_gated_ffn_grad(grad_out: torch.Tensor, x: torch.Tensor, w_gate: torch.Te
                        work: Optional[torch.Tensor] = None, stream=None) -> None:
     """The block's gradients (those given), from the saved pre-activations;
     accumulate adds to the weights' gradients."""
-    _on_gpu(grad_out, x, w_gate, w_up, w_down, saved, grad_x, grad_w_gate, grad_w_up, grad_w_down)
+    dev = _on_gpu(grad_out, x, w_gate, w_up, w_down, saved, grad_x, grad_w_gate, grad_w_up, grad_w_down)
     ptrs, (n, dim, ffn) = _ffn_shapes(x, w_gate, w_up, w_down)
     dt = x.dtype
     yp = _flat(grad_out, "grad_out", (n, dim), dt)
@@ -624,7 +650,7 @@ def ccl_gated_ffn_grad(grad_out: torch.Tensor, x: torch.Tensor, w_gate: torch.Te
                          ccl_plan_gated_ffn_work_bytes(n, dim, ffn, True, all(q % 16 == 0 for q in (yp, *ptrs))), x,
                          stream)
     _check(lib().ccl_gated_ffn_grad(yp, *ptrs, sp, n, dim, ffn, _dtype(x), _act(act), int(bool(accumulate)), *grads,
-                                    work.data_ptr(), nbytes, _stream(stream)), "ccl_gated_ffn_grad")
+                                    work.data_ptr(), nbytes, _stream_on(stream, dev)), "ccl_gated_ffn_grad")
 
 
 def ccl_plan_gated_ffn_work_bytes(ntokens: int, dim: int, ffn: int, backward: bool = False, aligned: bool = True) -> int:
@@ -648,7 +674,7 @@ def ccl_distill_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_lo
     distribution given by its top logits.  stats ([rows, 2]): kept for
     ccl_distill_grad.  grad: the gradient by the logits, in the same pass (may
     be `logits` itself)."""
-    _on_gpu(logits, teacher_ids, teacher_logits, loss, stats, grad, weights)
+    dev = _on_gpu(logits, teacher_ids, teacher_logits, loss, stats, grad, weights)
     lp, n, vocab, ls = _rows(logits, "logits")
     gp, gs = None, vocab
     if grad is not None:
@@ -660,7 +686,7 @@ def ccl_distill_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_lo
                                   _flat(teacher_logits, "teacher_logits", (n, top), torch.float32), top,
                                   float(temperature), _flat(weights, "weights", (n,), torch.float32),
                                   _flat(loss, "loss", (n,), torch.float32), _flat(stats, "stats", (n, 2), torch.float32),
-                                  gp, gs, _stream(stream)), "ccl_distill_loss")
+                                  gp, gs, _stream_on(stream, dev)), "ccl_distill_loss")
 
 
 def ccl_distill_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
@@ -668,7 +694,7 @@ def ccl_distill_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_lo
                      temperature: float = 1.0, stream=None) -> None:
     """The gradient of the sum of ccl_distill_loss's losses by the logits, from
     the stats it kept; grad may be `logits` itself."""
-    _on_gpu(logits, teacher_ids, teacher_logits, stats, grad, weights)
+    dev = _on_gpu(logits, teacher_ids, teacher_logits, stats, grad, weights)
     lp, n, vocab, ls = _rows(logits, "logits")
     gp, gn, _, gs = _rows(grad, "grad", vocab, logits.dtype)
     if gn != n:
@@ -677,7 +703,7 @@ def ccl_distill_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_lo
     _check(lib().ccl_distill_grad(lp, n, vocab, ls, _dtype(logits), _flat(teacher_ids, "teacher_ids", (n, top), torch.int64),
                                   _flat(teacher_logits, "teacher_logits", (n, top), torch.float32), top,
                                   float(temperature), _flat(weights, "weights", (n,), torch.float32),
-                                  _flat(stats, "stats", (n, 2), torch.float32), gp, gs, _stream(stream)),
+                                  _flat(stats, "stats", (n, 2), torch.float32), gp, gs, _stream_on(stream, dev)),
            "ccl_distill_grad")
 
 

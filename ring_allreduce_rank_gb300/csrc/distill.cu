@@ -7,11 +7,12 @@
 //     ds_v  = w / tau * (q_v - sum_{j: i_j = v} p_j).
 // With m the row's maximum and Z = sum_v exp((s_v - m) / tau), both need one
 // pass over the row for (m, Z); the gradient needs the row's values again.
-// Bound by memory bandwidth: the row is read once and the gradient written
-// once, so a cluster of CTAs keeps the row in registers between the two uses
-// (kVecs 16-byte vectors a thread; 64 KiB a CTA, so that three CTAs' loads and
-// stores overlap on an SM), joins (m, Z) through distributed shared memory,
-// and reads a row again only where it exceeds eight CTAs' registers.
+// Bound by memory bandwidth: a CTA streams its row once for (m, Z), with the
+// next vectors' loads in flight under the current ones' exponentials, and reads
+// it again from the L2 cache for the gradient, so that memory sees one read of
+// the logits and one write of the gradient.  Where there are few rows, a
+// cluster of CTAs shares each one and joins (m, Z) through distributed shared
+// memory.
 #include <cooperative_groups.h>
 
 #include <vector>
@@ -25,9 +26,10 @@ namespace cg = cooperative_groups;
 namespace ccl {
 namespace {
 
-constexpr int kDThreads = 512;
+constexpr int kDThreads = 256;
 constexpr int kDWarps = kDThreads / 32;
-constexpr int kVecs = 8;         // 16-byte vectors a thread holds
+constexpr int kDCtas = 4;        // resident CTAs per SM
+constexpr int kVecs = 4;         // 16-byte vectors a thread loads at a time
 constexpr int kMaxCluster = 8;   // portable cluster size
 constexpr int kMaxTop = CCL_MAX_TEACHER_TOP;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -66,6 +68,62 @@ __device__ __forceinline__ float row_exp(float s, float m, float scale)
 struct Stat {
     float m, z;
 };
+
+// ------------------------------------------------------------------ two fp32 values at a time
+
+__device__ __forceinline__ float2 add2(const float2 &a, const float2 &b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
+    return reinterpret_cast<const float2 &>(r);
+}
+
+__device__ __forceinline__ float2 mul2(const float2 &a, const float2 &b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
+    return reinterpret_cast<const float2 &>(r);
+}
+
+// row_exp of a pair; neg_m holds -m twice, scale the scale twice
+__device__ __forceinline__ float2 row_exp2(const float2 &s, const float2 &neg_m, const float2 &scale)
+{
+    const float2 x = mul2(add2(s, neg_m), scale);
+    return make_float2(exp2_approx(x.x), exp2_approx(x.y));
+}
+
+// The pairs of a 16-byte vector.
+template <int DT> __device__ __forceinline__ void unpack2(const uint4 &v, float2 *f)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < DType<DT>::kVec / 2; ++i)
+        f[i] = DT == DT_FP32 ? make_float2(__uint_as_float(w[(2 * i) & 3]), __uint_as_float(w[(2 * i + 1) & 3]))
+                             : make_float2(__uint_as_float(w[i & 3] << 16), __uint_as_float(w[i & 3] & 0xffff0000u));
+}
+
+// The largest value of kVecs vectors; a NaN does not count (it reaches the sum).
+template <int DT> __device__ __forceinline__ float max_of(const uint4 *x)
+{
+    if (DT == DT_FP32) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+            m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(x[i].x), __uint_as_float(x[i].y)),
+                               fmaxf(__uint_as_float(x[i].z), __uint_as_float(x[i].w))));
+        return m;
+    }
+    uint32_t m = 0xff80ff80u; // -inf twice
+    auto up = [&](uint32_t w) { asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w)); };
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        up(x[i].x);
+        up(x[i].y);
+        up(x[i].z);
+        up(x[i].w);
+    }
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+}
 
 // The statistics of two parts of a row.
 __device__ __forceinline__ Stat join(const Stat &a, const Stat &b, float scale)
@@ -115,10 +173,12 @@ template <bool MAX> __device__ __forceinline__ float block_reduce(float v, float
 // cluster's CTAs in contiguous parts; the elements before the first 16-byte
 // boundary and after the last one (fewer than a vector each) are CTA 0's.
 template <int DT, int MODE>
-__global__ void __launch_bounds__(kDThreads, 2) distill_kernel(const __grid_constant__ DistillParams p)
+__global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid_constant__ DistillParams p)
 {
     constexpr int VEC = DType<DT>::kVec, ES = DType<DT>::kSize;
-    __shared__ int64_t id[kMaxTop];
+    constexpr uint32_t kNone = 0xffffffffu;
+    constexpr uint32_t kStep = kVecs * kDThreads; // vectors of one load by the CTA
+    __shared__ uint32_t id[kMaxTop];
     __shared__ float prob[kMaxTop];  // p_j, 0 for entries that do not count
     __shared__ float logit[kMaxTop]; // the student's logit at id j
     __shared__ float red[kDWarps];
@@ -133,40 +193,41 @@ __global__ void __launch_bounds__(kDThreads, 2) distill_kernel(const __grid_cons
     const float w = p.weights ? gload<float>(p.weights + t) : 1.0f;
     const char *row = p.logits + t * p.pitch;
     char *grow = MODE == DISTILL_LOSS ? nullptr : p.grad + t * p.grad_pitch;
-    const uint64_t nh = umin64(p.vocab, ((16 - ((uintptr_t)row & 15)) & 15) / ES);
-    const uint64_t nv = (p.vocab - nh) / VEC, nt = p.vocab - nh - nv * VEC;
-    const uint64_t per = (nv + ctas - 1) / ctas, v0 = umin64(nv, per * cta), v1 = umin64(nv, v0 + per);
-    const char *body = row + nh * ES;
+    const uint32_t nh = (uint32_t)umin64(p.vocab, ((16 - ((uintptr_t)row & 15)) & 15) / ES);
+    const uint32_t nv = ((uint32_t)p.vocab - nh) / VEC, nt = (uint32_t)p.vocab - nh - nv * VEC;
+    const uint32_t per = (nv + ctas - 1) / ctas, v0 = min(nv, per * cta), v1 = min(nv, v0 + per);
+    const uint32_t loads = (v1 - v0 + kStep - 1) / kStep;
+    const char *body = row + (uint64_t)nh * ES;
     // an edge element: head, then tail
     const bool edge = cta == 0 && tid < (int)(nh + nt);
-    const uint64_t ei = tid < (int)nh ? tid : p.vocab - nt + (tid - nh);
+    const uint32_t ei = tid < (int)nh ? tid : (uint32_t)p.vocab - nt + (tid - nh);
     // a row whose weight is 0 has loss 0 and gradient 0 whatever it holds
     // (its statistics are still wanted where the caller keeps them)
-    const bool skip = w == 0.0f && (MODE != DISTILL_LOSS || !p.stats) && !(MODE == DISTILL_FUSED && p.stats);
-    const bool vec_store = MODE != DISTILL_LOSS && (((uintptr_t)grow ^ (uintptr_t)row) & 15) == 0;
+    const bool skip = w == 0.0f && (MODE == DISTILL_GRAD || !p.stats);
 
-    uint4 x[kVecs];
-    float xe = 0.0f;
-    const uint64_t rounds = (v1 - v0 + (uint64_t)kVecs * kDThreads - 1) / ((uint64_t)kVecs * kDThreads);
-    auto load = [&](uint64_t round) {
-        const uint64_t b = v0 + round * kVecs * kDThreads + tid;
+    // the vectors of one load; past the part's end -inf, which adds nothing
+    auto load = [&](uint4 *x, uint32_t l) {
+        const uint32_t b = v0 + l * kStep + tid;
+        constexpr uint32_t kNinf = DT == DT_FP32 ? 0xff800000u : 0xff80ff80u;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i)
-            if (b + (uint64_t)i * kDThreads < v1)
-                x[i] = ld16(body + (b + (uint64_t)i * kDThreads) * 16);
+        for (int i = 0; i < kVecs; ++i) {
+            x[i] = make_uint4(kNinf, kNinf, kNinf, kNinf);
+            if (b + i * kDThreads < v1)
+                x[i] = ld16(body + (uint64_t)(b + i * kDThreads) * 16);
+        }
     };
-    Stat st{-INFINITY, 0.0f};
+    uint4 xa[kVecs], xb[kVecs];
+    float xe = 0.0f;
     if (!skip) {
-        load(0);
+        load(xa, 0);
         if (edge)
             xe = ld_value<DT>(row, ei);
     }
-
     // whether element i of the row is in this CTA's part
-    auto mine = [&](uint64_t i) {
+    auto mine = [&](uint32_t i) {
         if (i < nh || i >= nh + nv * VEC)
             return cta == 0;
-        const uint64_t v = (i - nh) / VEC;
+        const uint32_t v = (i - nh) / VEC;
         return v >= v0 && v < v1;
     };
 
@@ -178,8 +239,11 @@ __global__ void __launch_bounds__(kDThreads, 2) distill_kernel(const __grid_cons
             const int64_t i = gload<int64_t>(p.ids + t * p.top + j);
             const bool ok = (uint64_t)i < p.vocab;
             const float l = ok ? gload<float>(p.teacher + t * p.top + j) : -INFINITY;
-            id[j] = ok ? i : -1;
+            id[j] = ok ? (uint32_t)i : kNone;
             prob[j] = l;
+            // CTA 0 needs every listed logit for the loss, the others their own
+            if (ok && (mine((uint32_t)i) || (MODE != DISTILL_GRAD && cta == 0)))
+                logit[j] = ld_value<DT>(row, (uint64_t)i);
             // a NaN counts as present, so that it reaches the result
             tm = l != l ? INFINITY : fmaxf(tm, l);
         }
@@ -188,19 +252,17 @@ __global__ void __launch_bounds__(kDThreads, 2) distill_kernel(const __grid_cons
     float tz = 0.0f;
     if (some)
         for (int j = tid; j < top; j += kDThreads) {
-            const float e = id[j] >= 0 ? exp2f(__fmul_rn(__fsub_rn(prob[j], tm), p.scale)) : 0.0f;
+            const float e = id[j] != kNone ? exp2f(__fmul_rn(__fsub_rn(prob[j], tm), p.scale)) : 0.0f;
             prob[j] = e;
             tz = __fadd_rn(tz, e);
         }
     tz = block_reduce<false>(tz, red);
     if (some)
-        for (int j = tid; j < top; j += kDThreads) {
+        for (int j = tid; j < top; j += kDThreads)
             prob[j] = __fdiv_rn(prob[j], tz);
-            // CTA 0 needs every listed logit for the loss, the others their own
-            if (id[j] >= 0 && (mine((uint64_t)id[j]) || (MODE != DISTILL_GRAD && cta == 0)))
-                logit[j] = ld_value<DT>(row, (uint64_t)id[j]);
-        }
 
+    Stat st{-INFINITY, 0.0f};
+    const float2 scale2 = make_float2(p.scale, p.scale);
     if (MODE == DISTILL_GRAD) {
         st.m = gload<float>(p.stats + 2 * t);
         st.z = gload<float>(p.stats + 2 * t + 1);
@@ -208,31 +270,51 @@ __global__ void __launch_bounds__(kDThreads, 2) distill_kernel(const __grid_cons
     } else {
         // (m, Z): this thread's vectors, then warp, CTA and cluster
         if (!skip) {
-            for (uint64_t r = 0; r < rounds; ++r) {
-                if (r)
-                    load(r);
-                const uint64_t b = v0 + r * kVecs * kDThreads + tid;
-                Stat part{-INFINITY, 0.0f};
+            float2 z = make_float2(0.0f, 0.0f);
+            auto fold = [&](const uint4 *x) {
+                const float bm = max_of<DT>(x);
+                if (bm > st.m) { // the sum so far, relative to the new maximum
+                    const float r = row_exp(st.m, bm, p.scale);
+                    z = mul2(z, make_float2(r, r));
+                    st.m = bm;
+                }
+                if (st.m == -INFINITY) { // nothing yet but -inf, and perhaps a NaN
 #pragma unroll
-                for (int i = 0; i < kVecs; ++i)
-                    if (b + (uint64_t)i * kDThreads < v1) {
+                    for (int i = 0; i < kVecs; ++i) {
                         float f[VEC];
                         unpack<DT>(x[i], f);
 #pragma unroll
                         for (int k = 0; k < VEC; ++k)
-                            part.m = fmaxf(part.m, f[k]);
+                            z.x = f[k] != f[k] ? f[k] : z.x;
                     }
+                    return;
+                }
+                const float2 neg = make_float2(-st.m, -st.m);
 #pragma unroll
-                for (int i = 0; i < kVecs; ++i)
-                    if (b + (uint64_t)i * kDThreads < v1) {
-                        float f[VEC];
-                        unpack<DT>(x[i], f);
+                for (int i = 0; i < kVecs; ++i) {
+                    float2 f[VEC / 2];
+                    unpack2<DT>(x[i], f);
 #pragma unroll
-                        for (int k = 0; k < VEC; ++k)
-                            part.z = __fadd_rn(part.z, f[k] == -INFINITY ? 0.0f : row_exp(f[k], part.m, p.scale));
-                    }
-                st = join(st, part, p.scale);
+                    for (int k = 0; k < VEC / 2; ++k)
+                        f[k] = row_exp2(f[k], neg, scale2);
+#pragma unroll
+                    for (int o = VEC / 4; o; o >>= 1)
+#pragma unroll
+                        for (int k = 0; k < o; ++k)
+                            f[k] = add2(f[k], f[k + o]);
+                    z = add2(z, f[0]);
+                }
+            };
+            for (uint32_t l = 0; l < loads; l += 2) {
+                if (l + 1 < loads)
+                    load(xb, l + 1);
+                fold(xa);
+                if (l + 2 < loads)
+                    load(xa, l + 2);
+                if (l + 1 < loads)
+                    fold(xb);
             }
+            st.z = __fadd_rn(z.x, z.y);
             if (edge)
                 st = join(st, Stat{xe, xe == -INFINITY ? 0.0f : row_exp(xe, xe, p.scale)}, p.scale);
         }
@@ -258,7 +340,7 @@ __global__ void __launch_bounds__(kDThreads, 2) distill_kernel(const __grid_cons
                 gstore<float>(p.stats + 2 * t + 1, st.z);
             }
             float sum = 0.0f;
-            if (some && !skip) {
+            if (some) {
                 const float lz = logf(st.z);
                 for (int j = tid; j < top; j += kDThreads)
                     if (!(prob[j] == 0.0f)) {
@@ -276,54 +358,68 @@ __global__ void __launch_bounds__(kDThreads, 2) distill_kernel(const __grid_cons
         const float a = __fmul_rn(w, p.inv_tau);
         const bool zero = w == 0.0f || !some;
         const float c = zero ? 0.0f : __fdiv_rn(a, st.z);
-        char *gbody = grow + nh * ES;
-        for (uint64_t r = 0; r < rounds; ++r) {
-            if (!skip && (MODE == DISTILL_GRAD ? r > 0 : rounds > 1))
-                load(r);
-            const uint64_t b = v0 + r * kVecs * kDThreads + tid;
+        const float2 c2 = make_float2(c, c), neg = make_float2(-st.m, -st.m);
+        const bool vec_store = (((uintptr_t)grow ^ (uintptr_t)row) & 15) == 0;
+        char *gbody = grow + (uint64_t)nh * ES;
+        auto emit = [&](const uint4 *x, uint32_t l) {
+            const uint32_t b = v0 + l * kStep + tid;
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                const uint64_t v = b + (uint64_t)i * kDThreads;
+                const uint32_t v = b + i * kDThreads;
+                float2 f[VEC / 2];
+                unpack2<DT>(x[i], f);
+#pragma unroll
+                for (int k = 0; k < VEC / 2; ++k)
+                    f[k] = zero ? make_float2(0.0f, 0.0f) : mul2(row_exp2(f[k], neg, scale2), c2);
                 if (v < v1) {
-                    float f[VEC];
-                    if (zero) {
-#pragma unroll
-                        for (int k = 0; k < VEC; ++k)
-                            f[k] = 0.0f;
-                    } else {
-                        unpack<DT>(x[i], f);
-#pragma unroll
-                        for (int k = 0; k < VEC; ++k)
-                            f[k] = __fmul_rn(row_exp(f[k], st.m, p.scale), c);
-                    }
+                    const float *g = reinterpret_cast<const float *>(f);
                     if (vec_store) {
-                        st16(gbody + v * 16, pack<DT>(f));
+                        st16(gbody + (uint64_t)v * 16, pack<DT>(g));
                     } else {
 #pragma unroll
                         for (int k = 0; k < VEC; ++k)
-                            st_value<DT>(grow, nh + v * VEC + k, f[k]);
+                            st_value<DT>(grow, nh + (uint64_t)v * VEC + k, g[k]);
                     }
                 }
             }
+        };
+        const bool again = !skip && (MODE != DISTILL_GRAD ? loads > 1 : false);
+        if (again)
+            load(xa, 0);
+        for (uint32_t l = 0; l < loads; l += 2) {
+            if (!skip && l + 1 < loads)
+                load(xb, l + 1);
+            emit(xa, l);
+            if (!skip && l + 2 < loads)
+                load(xa, l + 2);
+            if (l + 1 < loads)
+                emit(xb, l + 1);
         }
         if (edge)
             st_value<DT>(grow, ei, zero ? 0.0f : __fmul_rn(row_exp(xe, st.m, p.scale), c));
         __syncthreads(); // before the listed ids' gradients replace what was written
+        // `part` neighbouring threads share an entry's search for its id's other places
+        int part = 1;
+        while (part < 32 && 2 * part * top <= kDThreads)
+            part *= 2;
         if (!zero)
-            for (int j = tid; j < top; j += kDThreads) {
-                if (id[j] < 0)
-                    continue;
-                const uint64_t i = (uint64_t)id[j];
-                if (!mine(i))
-                    continue;
+            for (int j0 = 0; j0 < top; j0 += kDThreads / part) {
+                const int j = j0 + tid / part;
+                const uint32_t i = j < top ? id[j] : kNone;
+                const bool own = i != kNone && mine(i);
                 float sum = 0.0f;
-                bool firstj = true;
-                for (int k = 0; k < top; ++k)
-                    if (id[k] == id[j]) {
-                        firstj = firstj && k >= j;
-                        sum = __fadd_rn(sum, prob[k]);
-                    }
-                if (firstj) {
+                int first = top;
+                if (own)
+                    for (int k = tid % part; k < top; k += part)
+                        if (id[k] == i) {
+                            first = min(first, k);
+                            sum = __fadd_rn(sum, prob[k]);
+                        }
+                for (int o = 1; o < part; o *= 2) {
+                    sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+                    first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+                }
+                if (own && first == j && tid % part == 0) {
                     const float q = __fdiv_rn(row_exp(logit[j], st.m, p.scale), st.z);
                     st_value<DT>(grow, i, __fmul_rn(a, __fsub_rn(q, sum)));
                 }
@@ -426,11 +522,11 @@ ccl_status_t distill_impl(int mode, const DistillArgs &a, cudaStream_t stream)
     p.top = a.top;
     p.inv_tau = inv_tau;
     p.scale = inv_tau * kLog2e;
-    // the fewest CTAs whose registers hold a row; more, down to one vector a
-    // thread, while there are fewer of them than SMs
-    const uint64_t bytes = a.vocab * es, cap = (uint64_t)kVecs * kDThreads * 16;
+    // one CTA a row; where that leaves CTAs' places on the GPU empty, up to
+    // eight, as long as each has a full load of vectors
+    const uint64_t bytes = a.vocab * es;
     uint32_t ctas = 1;
-    while (ctas < kMaxCluster && (bytes > ctas * cap || (a.nrows * ctas < 152 && bytes > ctas * cap / kVecs)))
+    while (ctas < kMaxCluster && a.nrows * ctas < 152 * kDCtas && bytes >= 2 * ctas * kVecs * kDThreads * 16)
         ctas *= 2;
     const bool f = a.dtype == CCL_FP32;
     cudaError_t e;

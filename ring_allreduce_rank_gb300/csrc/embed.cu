@@ -11,7 +11,7 @@
 //      stably, by a radix sort that one cluster of eight CTAs runs (the
 //      digits' counts cross the cluster through distributed shared memory);
 //      meanwhile every other CTA writes the zero rows of the dense gradient.
-//   2. embed_sum_kernel: the sorted tokens in pieces of kPiece, each summed in
+//   2. embed_sum_kernel: the sorted tokens in pieces of 8 to 64, each summed in
 //      order; a row whose tokens lie in one piece is finished here, a row that
 //      crosses pieces leaves one fp32 partial sum per piece.
 //   3. embed_join_kernel: those partial sums, added in order.
@@ -34,7 +34,8 @@ constexpr int kSortCtas = 8;       // one portable cluster
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigits = 256;       // bins of one radix pass
-constexpr int kPiece = 64;         // sorted tokens summed by one warp
+constexpr int kMaxPiece = 64;      // sorted tokens summed by one warp, at most
+constexpr int kAhead = 8;          // rows' loads a warp has in flight
 constexpr int kSumThreads = 128;
 
 // ------------------------------------------------------------------ lookup
@@ -161,10 +162,17 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
             for (uint32_t i = tid; i < (n + 31) / 32; i += kSortThreads)
                 mark[i] = 0;
             __syncthreads();
-            for (uint64_t t = tid; t < p.ntokens; t += kSortThreads) {
-                const uint64_t r = (uint64_t)row_key(p, t) - lo;
-                if (r < n)
-                    atomicOr(&mark[r >> 5], 1u << (r & 31));
+            for (uint64_t t0 = tid; t0 < p.ntokens; t0 += 8 * kSortThreads) {
+                uint32_t key[8]; // eight loads in flight
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    key[j] = t0 + j * kSortThreads < p.ntokens ? row_key(p, t0 + j * kSortThreads) : 0xffffffffu;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint64_t r = (uint64_t)key[j] - lo;
+                    if (r < n)
+                        atomicOr(&mark[r >> 5], 1u << (r & 31));
+                }
             }
             __syncthreads();
             for (uint32_t r = warp; r < n; r += kSortWarps)
@@ -182,6 +190,27 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
     const uint64_t lo = ((uint64_t)blockIdx.x * kSortWarps + warp) * slice;
     const uint64_t hi = umin64(p.ntokens, lo + slice);
     const uint32_t below = (1u << lane) - 1;
+
+    if (p.ntokens <= kSortThreads) {
+        // one CTA ranks the few pairs by counting, without passes
+        if (blockIdx.x == 0) {
+            uint64_t *key = reinterpret_cast<uint64_t *>(&cnt[0][0]);
+            const uint32_t n = (uint32_t)p.ntokens;
+            const uint32_t row = tid < (int)n ? row_key(p, tid) : 0;
+            const uint64_t own = (uint64_t)row << 32 | (uint32_t)tid;
+            if (tid < (int)n)
+                key[tid] = own;
+            __syncthreads();
+            if (tid < (int)n) {
+                uint32_t rank = 0;
+#pragma unroll 8
+                for (uint32_t i = 0; i < n; ++i)
+                    rank += key[i] < own;
+                gstore<uint2>(p.buf[(p.passes - 1) & 1] + rank, make_uint2(row, (uint32_t)tid));
+            }
+        }
+        return; // the same for the whole cluster: no other CTA waits
+    }
 
     for (int pass = 0; pass < p.passes; ++pass) {
         const int shift = pass * p.bits;
@@ -271,7 +300,7 @@ struct SumParams {
     char *grad;
     uint64_t pitch;
     float *head, *tail; // [piece][dim_pad] partial sums of rows that cross pieces
-    uint32_t rows;
+    uint32_t rows, piece;
     float scale;
     int accumulate;
 };
@@ -288,19 +317,35 @@ template <int DT, bool VECTOR> struct Columns {
     {
     }
     __device__ __forceinline__ uint64_t col(int j) const { return VECTOR ? c0 + j : c0 + 32 * j; }
-    __device__ __forceinline__ void load(const char *row, float *f) const
+    // a row's values as loaded (nothing waits for them), and as fp32
+    __device__ __forceinline__ uint4 fetch(const char *row) const
     {
+        uint4 v = make_uint4(0, 0, 0, 0);
         if (VECTOR) {
-            uint4 v = make_uint4(0, 0, 0, 0);
             if (c0 < dim)
                 v = ld16(row + c0 * DType<DT>::kSize);
+        } else {
+            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (col(j) < dim)
+                    w[j] = ld_elem<DT>(row, col(j));
+            v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        return v;
+    }
+    __device__ __forceinline__ void values(const uint4 &v, float *f) const
+    {
+        if (VECTOR) {
             unpack<DT>(v, f);
         } else {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-                f[j] = col(j) < dim ? ld_value<DT>(row, col(j)) : 0.0f;
+            for (int j = 0; j < 4; ++j)
+                f[j] = __uint_as_float(DT == DT_BF16 ? w[j] << 16 : w[j]);
         }
     }
+    __device__ __forceinline__ void load(const char *row, float *f) const { values(fetch(row), f); }
     __device__ __forceinline__ void store(char *row, float *f, float scale, bool accumulate) const
     {
         float old[N];
@@ -325,16 +370,31 @@ template <int DT, bool VECTOR> struct Columns {
     }
     __device__ __forceinline__ void load_partial(const float *row, float *f) const
     {
+        if (VECTOR) {
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            f[j] = col(j) < dim ? gload<float>(row + col(j)) : 0.0f;
+            for (int j = 0; j < N; j += 4) {
+                const uint4 v = c0 < dim ? ld16(row + c0 + j) : make_uint4(0, 0, 0, 0);
+                unpack<DT_FP32>(v, f + j);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                f[j] = col(j) < dim ? gload<float>(row + col(j)) : 0.0f;
+        }
     }
     __device__ __forceinline__ void store_partial(float *row, const float *f) const
     {
+        if (VECTOR) {
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (col(j) < dim)
-                gstore<float>(row + col(j), f[j]);
+            for (int j = 0; j < N; j += 4)
+                if (c0 < dim)
+                    st16(row + c0 + j, pack<DT_FP32>(f + j));
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (col(j) < dim)
+                    gstore<float>(row + col(j), f[j]);
+        }
     }
 };
 
@@ -344,16 +404,15 @@ __device__ __forceinline__ uint32_t row_at(const SumParams &p, uint64_t i)
     return i < p.ntokens ? gload<uint2>(p.sorted + i).x : 0xffffffffu;
 }
 
-// One warp sums one piece for its columns, eight rows' loads in flight.
+// One warp sums one piece for its columns, kAhead rows' loads in flight.
 template <int DT, bool VECTOR> __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(SumParams p)
 {
     chain_entry();
-    constexpr int kAhead = 8;
     const int lane = threadIdx.x & 31;
     const Columns<DT, VECTOR> cols(p.dim, lane);
     constexpr int N = Columns<DT, VECTOR>::N;
-    const uint64_t first = (uint64_t)blockIdx.x * kPiece;
-    const int n = (int)umin64(kPiece, p.ntokens - first);
+    const uint64_t first = (uint64_t)blockIdx.x * p.piece;
+    const int n = (int)umin64(p.piece, p.ntokens - first);
     // lane l holds tokens l and l + 32 of the piece
     const uint2 none = make_uint2(0xffffffffu, 0);
     const uint2 a = lane < n ? gload<uint2>(p.sorted + first + lane) : none;
@@ -368,7 +427,7 @@ template <int DT, bool VECTOR> __global__ void __launch_bounds__(kSumThreads) em
         acc[j] = 0.0f;
     for (int i0 = 0; i0 < n; i0 += kAhead) {
         uint32_t r[kAhead];
-        float f[kAhead][N];
+        uint4 v[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const uint32_t ra = __shfl_sync(0xffffffffu, a.x, (i0 + i) & 31);
@@ -378,7 +437,7 @@ template <int DT, bool VECTOR> __global__ void __launch_bounds__(kSumThreads) em
             r[i] = i0 + i < 32 ? ra : rb;
             const uint32_t t = i0 + i < 32 ? ta : tb;
             if (r[i] < p.rows)
-                cols.load(p.dy + (uint64_t)t * p.dy_pitch, f[i]);
+                v[i] = cols.fetch(p.dy + (uint64_t)t * p.dy_pitch);
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
@@ -396,10 +455,13 @@ template <int DT, bool VECTOR> __global__ void __launch_bounds__(kSumThreads) em
                 for (int j = 0; j < N; ++j)
                     acc[j] = 0.0f;
             }
-            if (r[i] < p.rows)
+            if (r[i] < p.rows) {
+                float f[N];
+                cols.values(v[i], f);
 #pragma unroll
                 for (int j = 0; j < N; ++j)
-                    acc[j] = __fadd_rn(acc[j], f[i][j]);
+                    acc[j] = __fadd_rn(acc[j], f[j]);
+            }
         }
     }
     if (row < p.rows) { // the piece's last run (a full piece: it did not end above)
@@ -413,29 +475,46 @@ template <int DT, bool VECTOR> __global__ void __launch_bounds__(kSumThreads) em
 }
 
 // The rows that begin in piece blockIdx.x and go on in the next one: their
-// partial sums, in order.
+// partial sums, in order, four at a time in flight.
 template <int DT, bool VECTOR> __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(SumParams p)
 {
     chain_entry();
     const int lane = threadIdx.x & 31;
     const Columns<DT, VECTOR> cols(p.dim, lane);
     constexpr int N = Columns<DT, VECTOR>::N;
-    const uint64_t first = (uint64_t)blockIdx.x * kPiece;
-    if (first + kPiece >= p.ntokens)
+    const uint64_t first = (uint64_t)blockIdx.x * p.piece;
+    if (first + p.piece >= p.ntokens)
         return; // the last piece
-    const uint32_t row = row_at(p, first + kPiece - 1);
-    if (row >= p.rows || row_at(p, first + kPiece) != row)
+    const uint32_t row = row_at(p, first + p.piece - 1);
+    const uint32_t next = row_at(p, first + p.piece), begin = row_at(p, first);
+    const uint32_t prev = first ? row_at(p, first - 1) : 0xffffffffu;
+    if (row >= p.rows || next != row)
         return;
     // it goes on; it began here unless the whole piece and the token before are its own
-    if (row_at(p, first) == row && first && row_at(p, first - 1) == row)
+    if (begin == row && prev == row)
         return;
-    float acc[N], f[N];
+    float acc[N];
     cols.load_partial(p.tail + blockIdx.x * p.dim_pad, acc);
-    for (uint64_t q = blockIdx.x + 1; row_at(p, q * kPiece) == row; ++q) {
-        cols.load_partial(p.head + q * p.dim_pad, f);
+    for (uint64_t q = blockIdx.x + 1;;) {
+        // the pieces that begin with this row, 32 looked at together
+        const unsigned go = __ballot_sync(0xffffffffu, row_at(p, (q + lane) * p.piece) == row);
+        const int n = go == 0xffffffffu ? 32 : __ffs(~go) - 1;
+        for (int i0 = 0; i0 < n; i0 += 4) {
+            float f[4][N];
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            acc[j] = __fadd_rn(acc[j], f[j]);
+            for (int i = 0; i < 4; ++i)
+                if (i0 + i < n)
+                    cols.load_partial(p.head + (q + i0 + i) * p.dim_pad, f[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i0 + i < n)
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        acc[j] = __fadd_rn(acc[j], f[i][j]);
+        }
+        if (n < 32)
+            break;
+        q += 32;
     }
     cols.store(p.grad + (uint64_t)row * p.pitch, acc, p.scale, p.accumulate);
 }
@@ -447,7 +526,16 @@ bool aligned16(const void *p, size_t pitch, size_t row_bytes)
     return ((uintptr_t)p | pitch | row_bytes) % 16 == 0;
 }
 
-size_t pieces(size_t ntokens) { return (ntokens + kPiece - 1) / kPiece; }
+// Tokens a piece: eight, one batch of loads, doubled up to 64 while that
+// still leaves more warps than the GPU holds about half full (152 SMs x 32
+// warps; a warp covers at least 128 columns).
+uint32_t piece_of(size_t ntokens, size_t dim)
+{
+    uint32_t n = kAhead;
+    while (n < kMaxPiece && (ntokens / n) * ((dim + 127) / 128) > 152 * 32)
+        n *= 2;
+    return n;
+}
 
 constexpr size_t kMaxRows = 0x7fffffff; // rows and tokens are 32-bit in the sorted list
 constexpr size_t kMaxDim = (size_t)1 << 24; // columns: the second dimension of the sums' grid
@@ -515,7 +603,7 @@ struct GradWork {
 
 bool grad_work(size_t ntokens, size_t dim, GradWork *w)
 {
-    const size_t pad = (dim + 3) / 4 * 4, np = pieces(ntokens);
+    const size_t pad = (dim + 3) / 4 * 4, np = (ntokens + piece_of(ntokens, dim) - 1) / piece_of(ntokens, dim);
     if (mul_overflows(np, pad * 16))
         return false;
     w->sorted = up(ntokens * sizeof(uint2));
@@ -603,10 +691,11 @@ ccl_status_t embedding_grad_impl(const void *grad_out, size_t grad_out_stride, c
     p.head = reinterpret_cast<float *>(wp + 2 * gw.sorted);
     p.tail = reinterpret_cast<float *>(wp + 2 * gw.sorted + gw.partial);
     p.rows = s.rows;
+    p.piece = piece_of(ntokens, dim);
     p.scale = scale;
     p.accumulate = accumulate != 0;
     const bool vec = aligned16(grad_out, p.dy_pitch, dim * es) && aligned16(grad_table, p.pitch, dim * es);
-    const uint32_t np = (uint32_t)pieces(ntokens);
+    const uint32_t np = (uint32_t)((ntokens + p.piece - 1) / p.piece);
     return from_cuda(dtype == CCL_FP32 ? launch_sums<DT_FP32>(p, vec, np, stream)
                                        : launch_sums<DT_BF16>(p, vec, np, stream));
 }
