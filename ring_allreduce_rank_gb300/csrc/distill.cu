@@ -7,14 +7,17 @@
 //     ds_v  = w / tau * (q_v - sum_{j: i_j = v} p_j).
 // With m the row's maximum and Z = sum_v exp((s_v - m) / tau), both need one
 // pass over the row for (m, Z); the gradient needs the row's values again.
-// Bound by memory bandwidth: a CTA streams its row once for (m, Z), with the
-// next vectors' loads in flight under the current ones' exponentials, and reads
-// it again from the L2 cache for the gradient, so that memory sees one read of
-// the logits and one write of the gradient.  Where there are few rows, a
-// cluster of CTAs shares each one and joins (m, Z) through distributed shared
-// memory.
+// Bound by memory bandwidth, which sees one read of the logits and one write
+// of the gradient: a cluster of CTAs takes a row, each CTA asks for its whole
+// part at once (up to 64 KiB: half to shared memory by asynchronous copies,
+// half to registers) and keeps it there between the two uses, and the CTAs
+// join (m, Z) through distributed shared memory.  Four CTAs an SM are at
+// different places of this, so that loads, exponentials and stores overlap.
+// Reading the row a second time from the L2 cache instead missed the cache
+// (608 CTAs' rows of 250 KiB exceed it): 471 us for 4096 rows of 128000 bf16.
 #include <cooperative_groups.h>
 
+#include <atomic>
 #include <vector>
 
 #include "../../include/ccl.h"
@@ -29,7 +32,9 @@ namespace {
 constexpr int kDThreads = 256;
 constexpr int kDWarps = kDThreads / 32;
 constexpr int kDCtas = 4;        // resident CTAs per SM
-constexpr int kVecs = 4;         // 16-byte vectors a thread loads at a time
+constexpr int kVecs = 4;         // 16-byte vectors a thread folds at a time
+constexpr int kHeld = 8;         // vectors a thread keeps in registers, and as many in shared memory
+constexpr uint32_t kPart = 2 * kHeld * kDThreads; // vectors a CTA keeps
 constexpr int kMaxCluster = 8;   // portable cluster size
 constexpr int kMaxTop = CCL_MAX_TEACHER_TOP;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -47,6 +52,7 @@ struct DistillParams {
     uint64_t vocab;
     uint64_t pitch, grad_pitch; // bytes
     uint64_t top;
+    uint32_t slot_bits;   // the hash table of the listed ids has 2^slot_bits places
     float scale;          // log2(e) / tau
     float inv_tau;
 };
@@ -68,6 +74,17 @@ __device__ __forceinline__ float row_exp(float s, float m, float scale)
 struct Stat {
     float m, z;
 };
+
+__device__ __forceinline__ void copy16_async(uint4 *dst, const void *src)
+{
+    if (dbg_ok(src, 16))
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // ------------------------------------------------------------------ two fp32 values at a time
 
@@ -148,7 +165,9 @@ __device__ __forceinline__ Stat warp_join(Stat s, float scale)
     return s;
 }
 
-template <bool MAX> __device__ __forceinline__ float block_reduce(float v, float *buf)
+// Sum or maximum over the first `warps` warps, which alone call this; buf
+// holds a value per warp and is used once.
+template <bool MAX> __device__ __forceinline__ float warps_reduce(float v, float *buf, int warps)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -156,17 +175,20 @@ template <bool MAX> __device__ __forceinline__ float block_reduce(float v, float
         const float u = __shfl_xor_sync(0xffffffffu, v, o);
         v = MAX ? fmaxf(v, u) : __fadd_rn(v, u);
     }
-    __syncthreads(); // the buffer's last use
+    if (warps == 1) {
+        __syncwarp();
+        return v;
+    }
     if (lane == 0)
         buf[warp] = v;
-    __syncthreads();
-    v = buf[lane & (kDWarps - 1)];
+    asm volatile("bar.sync 1, %0;" ::"r"(warps * 32) : "memory");
+    v = lane < warps ? buf[lane] : (MAX ? -INFINITY : 0.0f);
 #pragma unroll
     for (int o = kDWarps / 2; o; o >>= 1) {
         const float u = __shfl_xor_sync(0xffffffffu, v, o);
         v = MAX ? fmaxf(v, u) : __fadd_rn(v, u);
     }
-    return v;
+    return __shfl_sync(0xffffffffu, v, 0);
 }
 
 // One cluster per row.  The row's 16-byte vectors are shared out over the
@@ -176,16 +198,19 @@ template <int DT, int MODE>
 __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid_constant__ DistillParams p)
 {
     constexpr int VEC = DType<DT>::kVec, ES = DType<DT>::kSize;
-    constexpr uint32_t kNone = 0xffffffffu;
-    constexpr uint32_t kStep = kVecs * kDThreads; // vectors of one load by the CTA
+    constexpr uint32_t kNone = 0xffffffffu, kEntry = 0x7fffffffu;
+    extern __shared__ uint4 held[]; // [kHeld][kDThreads]: each thread reads back its own vectors
     __shared__ uint32_t id[kMaxTop];
     __shared__ float prob[kMaxTop];  // p_j, 0 for entries that do not count
     __shared__ float logit[kMaxTop]; // the student's logit at id j
-    __shared__ float red[kDWarps];
-    __shared__ Stat wstat[kDWarps];
-    __shared__ Stat cstat; // this CTA's part of the row, read by the cluster
+    __shared__ uint32_t slot[MODE == DISTILL_LOSS ? 1 : 2 * kMaxTop]; // an entry of each id, hashed
+    __shared__ float red[3][kDWarps];
+    __shared__ int present; // whether the row has a teacher
+    __shared__ Stat wstat[kMaxCluster * kDWarps]; // every warp of the cluster's part of the row
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t ctas = cluster.num_blocks(), cta = cluster.block_rank();
+    if (MODE != DISTILL_GRAD)
+        cluster_arrive(); // waited for before the first write to another CTA
     const uint64_t t = blockIdx.x / ctas;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int top = (int)p.top;
@@ -196,7 +221,6 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
     const uint32_t nh = (uint32_t)umin64(p.vocab, ((16 - ((uintptr_t)row & 15)) & 15) / ES);
     const uint32_t nv = ((uint32_t)p.vocab - nh) / VEC, nt = (uint32_t)p.vocab - nh - nv * VEC;
     const uint32_t per = (nv + ctas - 1) / ctas, v0 = min(nv, per * cta), v1 = min(nv, v0 + per);
-    const uint32_t loads = (v1 - v0 + kStep - 1) / kStep;
     const char *body = row + (uint64_t)nh * ES;
     // an edge element: head, then tail
     const bool edge = cta == 0 && tid < (int)(nh + nt);
@@ -205,21 +229,46 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
     // (its statistics are still wanted where the caller keeps them)
     const bool skip = w == 0.0f && (MODE == DISTILL_GRAD || !p.stats);
 
-    // the vectors of one load; past the part's end -inf, which adds nothing
-    auto load = [&](uint4 *x, uint32_t l) {
-        const uint32_t b = v0 + l * kStep + tid;
-        constexpr uint32_t kNinf = DT == DT_FP32 ? 0xff800000u : 0xff80ff80u;
+    // kVecs vectors from vector b on; past the part's end -inf, which adds nothing
+    constexpr uint32_t kNinf = DT == DT_FP32 ? 0xff800000u : 0xff80ff80u;
+    const uint4 ninf = make_uint4(kNinf, kNinf, kNinf, kNinf);
+    auto load = [&](uint4 *x, uint32_t b) {
+        const char *q = body + (uint64_t)b * 16;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            x[i] = make_uint4(kNinf, kNinf, kNinf, kNinf);
+            x[i] = ninf;
             if (b + i * kDThreads < v1)
-                x[i] = ld16(body + (uint64_t)(b + i * kDThreads) * 16);
+                x[i] = ld16(q + i * kDThreads * 16);
         }
     };
-    uint4 xa[kVecs], xb[kVecs];
+    auto from_held = [&](uint4 *x, int i0) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+            x[i] = held[(i0 + i) * kDThreads + tid];
+    };
+    // the teacher's entries are worked on by as many warps as there are
+    // entries for; the loss is CTA 0's.  Their loads go out before the row's,
+    // which would delay them.
+    const int warps = max(1, min(kDWarps, (top + 31) / 32)), step = warps * 32;
+    const bool listed = !skip && warp < warps && (MODE != DISTILL_LOSS || cta == 0);
+    int64_t first_id = -1;
+    float first_logit = 0.0f, first_student = 0.0f;
+    if (listed && tid < top) {
+        first_id = gload<int64_t>(p.ids + t * p.top + tid);
+        first_logit = gload<float>(p.teacher + t * p.top + tid);
+    }
+    uint4 x[kHeld];
     float xe = 0.0f;
     if (!skip) {
-        load(xa, 0);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            if (v0 + tid + i * kDThreads < v1)
+                copy16_async(&held[i * kDThreads + tid], body + (uint64_t)(v0 + tid) * 16 + i * kDThreads * 16);
+            else
+                held[i * kDThreads + tid] = ninf;
+#pragma unroll
+        for (int i = 0; i < kHeld; i += kVecs)
+            load(x + i, v0 + tid + (kHeld + i) * kDThreads);
         if (edge)
             xe = ld_value<DT>(row, ei);
     }
@@ -231,41 +280,69 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
         return v >= v0 && v < v1;
     };
 
-    // the teacher's probabilities; the loss is CTA 0's
-    const bool listed = !skip && (MODE != DISTILL_LOSS || cta == 0);
-    float tm = -INFINITY;
-    if (listed)
-        for (int j = tid; j < top; j += kDThreads) {
-            const int64_t i = gload<int64_t>(p.ids + t * p.top + j);
-            const bool ok = (uint64_t)i < p.vocab;
-            const float l = ok ? gload<float>(p.teacher + t * p.top + j) : -INFINITY;
-            id[j] = ok ? (uint32_t)i : kNone;
-            prob[j] = l;
-            // CTA 0 needs every listed logit for the loss, the others their own
-            if (ok && (mine((uint32_t)i) || (MODE != DISTILL_GRAD && cta == 0)))
-                logit[j] = ld_value<DT>(row, (uint64_t)i);
-            // a NaN counts as present, so that it reaches the result
-            tm = l != l ? INFINITY : fmaxf(tm, l);
-        }
-    tm = block_reduce<true>(tm, red);
-    const bool some = tm > -INFINITY;
-    float tz = 0.0f;
-    if (some)
-        for (int j = tid; j < top; j += kDThreads) {
-            const float e = id[j] != kNone ? exp2f(__fmul_rn(__fsub_rn(prob[j], tm), p.scale)) : 0.0f;
-            prob[j] = e;
-            tz = __fadd_rn(tz, e);
-        }
-    tz = block_reduce<false>(tz, red);
-    if (some)
-        for (int j = tid; j < top; j += kDThreads)
-            prob[j] = __fdiv_rn(prob[j], tz);
+    // the teacher's probabilities
+    if (warp < warps) {
+        float tm = -INFINITY;
+        if (MODE != DISTILL_LOSS)
+            for (uint32_t i = tid; i < 1u << p.slot_bits; i += step)
+                slot[i] = kNone;
+        if (listed)
+            for (int j = tid; j < top; j += step) {
+                const int64_t i = j == tid ? first_id : gload<int64_t>(p.ids + t * p.top + j);
+                const bool ok = (uint64_t)i < p.vocab;
+                const float l = !ok ? -INFINITY : j == tid ? first_logit : gload<float>(p.teacher + t * p.top + j);
+                id[j] = ok ? (uint32_t)i : kNone;
+                prob[j] = l;
+                // CTA 0 needs every listed logit for the loss, the others
+                // their own; the first one's is waited for only later
+                if (ok && (mine((uint32_t)i) || (MODE != DISTILL_GRAD && cta == 0))) {
+                    if (j == tid)
+                        first_student = ld_value<DT>(row, (uint64_t)i);
+                    else
+                        logit[j] = ld_value<DT>(row, (uint64_t)i);
+                }
+                // a NaN counts as present, so that it reaches the result
+                tm = l != l ? INFINITY : fmaxf(tm, l);
+            }
+        tm = warps_reduce<true>(tm, red[0], warps);
+        float tz = 0.0f;
+        if (tm > -INFINITY)
+            for (int j = tid; j < top; j += step) {
+                const float e = id[j] != kNone ? exp2f(__fmul_rn(__fsub_rn(prob[j], tm), p.scale)) : 0.0f;
+                prob[j] = e;
+                tz = __fadd_rn(tz, e);
+                if (MODE != DISTILL_LOSS && id[j] != kNone) {
+                    // one entry stands for each id in an open hash table at most
+                    // half full; the top bit says that the id has others
+                    const uint32_t mask = (1u << p.slot_bits) - 1;
+                    for (uint32_t h = id[j] * 2654435761u >> (32 - p.slot_bits);; h = (h + 1) & mask) {
+                        const uint32_t was = atomicCAS(&slot[h], kNone, (uint32_t)j);
+                        if (was == kNone)
+                            break;
+                        if (id[was & kEntry] == id[j]) {
+                            atomicOr(&slot[h], ~kEntry);
+                            break;
+                        }
+                    }
+                }
+            }
+        tz = warps_reduce<false>(tz, red[1], warps);
+        if (tm > -INFINITY)
+            for (int j = tid; j < top; j += step)
+                prob[j] = __fdiv_rn(prob[j], tz);
+        if (tid == 0)
+            present = tm > -INFINITY;
+    }
+    copies_wait();
 
     Stat st{-INFINITY, 0.0f};
     const float2 scale2 = make_float2(p.scale, p.scale);
+    uint4 y[kVecs];
     if (MODE == DISTILL_GRAD) {
         st.m = gload<float>(p.stats + 2 * t);
         st.z = gload<float>(p.stats + 2 * t + 1);
+        if (tid < top && tid < step)
+            logit[tid] = first_student;
         __syncthreads();
     } else {
         // (m, Z): this thread's vectors, then warp, CTA and cluster
@@ -305,50 +382,54 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
                     z = add2(z, f[0]);
                 }
             };
-            for (uint32_t l = 0; l < loads; l += 2) {
-                if (l + 1 < loads)
-                    load(xb, l + 1);
-                fold(xa);
-                if (l + 2 < loads)
-                    load(xa, l + 2);
-                if (l + 1 < loads)
-                    fold(xb);
+#pragma unroll 1
+            for (int i = 0; i < kHeld; i += kVecs) {
+                from_held(y, i);
+                fold(y);
+            }
+#pragma unroll
+            for (int i = 0; i < kHeld; i += kVecs)
+                fold(x + i);
+#pragma unroll 1
+            for (uint32_t b = v0 + kPart; b < v1; b += kVecs * kDThreads) {
+                load(y, b + tid);
+                fold(y);
             }
             st.z = __fadd_rn(z.x, z.y);
             if (edge)
                 st = join(st, Stat{xe, xe == -INFINITY ? 0.0f : row_exp(xe, xe, p.scale)}, p.scale);
         }
         st = warp_join(st, p.scale);
-        if (lane == 0)
-            wstat[warp] = st;
-        __syncthreads();
-        if (warp == 0) {
-            st = lane < kDWarps ? wstat[lane] : Stat{-INFINITY, 0.0f};
-            st = warp_join(st, p.scale);
-            if (lane == 0)
-                cstat = st;
-        }
+        if (tid < top && tid < step)
+            logit[tid] = first_student;
+        cluster_wait(); // every CTA of the cluster has begun
+        if (lane < (int)ctas)
+            cluster.map_shared_rank(wstat, lane)[cta * kDWarps + warp] = st;
         // from here on a CTA may overwrite its part of the logits (in place):
         // every read of another CTA's part is above
-        cluster.sync();
-        st = *cluster.map_shared_rank(&cstat, 0);
-        for (uint32_t c = 1; c < ctas; ++c)
-            st = join(st, *cluster.map_shared_rank(&cstat, c), p.scale);
-        if (cta == 0) {
+        cluster_arrive();
+        cluster_wait();
+        st = Stat{-INFINITY, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kMaxCluster * kDWarps; i += 32)
+            if (i + lane < (int)ctas * kDWarps)
+                st = join(st, wstat[i + lane], p.scale);
+        st = warp_join(st, p.scale);
+        if (cta == 0 && warp < warps) {
             if (p.stats && tid == 0) {
                 gstore<float>(p.stats + 2 * t, st.m);
                 gstore<float>(p.stats + 2 * t + 1, st.z);
             }
             float sum = 0.0f;
-            if (some) {
+            if (present) {
                 const float lz = logf(st.z);
-                for (int j = tid; j < top; j += kDThreads)
+                for (int j = tid; j < top; j += step)
                     if (!(prob[j] == 0.0f)) {
                         const float logq = __fsub_rn(__fmul_rn(__fsub_rn(logit[j], st.m), p.inv_tau), lz);
                         sum = __fadd_rn(sum, __fmul_rn(prob[j], __fsub_rn(logf(prob[j]), logq)));
                     }
             }
-            sum = block_reduce<false>(sum, red);
+            sum = warps_reduce<false>(sum, red[2], warps);
             if (tid == 0)
                 gstore<float>(p.loss + t, w == 0.0f ? 0.0f : __fmul_rn(w, sum));
         }
@@ -356,77 +437,73 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
 
     if (MODE != DISTILL_LOSS) {
         const float a = __fmul_rn(w, p.inv_tau);
-        const bool zero = w == 0.0f || !some;
+        const bool zero = w == 0.0f || !present;
         const float c = zero ? 0.0f : __fdiv_rn(a, st.z);
         const float2 c2 = make_float2(c, c), neg = make_float2(-st.m, -st.m);
         const bool vec_store = (((uintptr_t)grow ^ (uintptr_t)row) & 15) == 0;
         char *gbody = grow + (uint64_t)nh * ES;
-        auto emit = [&](const uint4 *x, uint32_t l) {
-            const uint32_t b = v0 + l * kStep + tid;
+        auto emit = [&](const uint4 *x, uint32_t b) {
+            char *q = gbody + (uint64_t)b * 16;
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                const uint32_t v = b + i * kDThreads;
+                uint4 o = make_uint4(0, 0, 0, 0);
                 float2 f[VEC / 2];
-                unpack2<DT>(x[i], f);
+                if (!zero) {
+                    unpack2<DT>(x[i], f);
 #pragma unroll
-                for (int k = 0; k < VEC / 2; ++k)
-                    f[k] = zero ? make_float2(0.0f, 0.0f) : mul2(row_exp2(f[k], neg, scale2), c2);
-                if (v < v1) {
-                    const float *g = reinterpret_cast<const float *>(f);
+                    for (int k = 0; k < VEC / 2; ++k)
+                        f[k] = mul2(row_exp2(f[k], neg, scale2), c2);
+                    o = pack<DT>(reinterpret_cast<const float *>(f));
+                }
+                if (b + i * kDThreads < v1) {
                     if (vec_store) {
-                        st16(gbody + (uint64_t)v * 16, pack<DT>(g));
+                        st16(q + i * kDThreads * 16, o);
                     } else {
+                        const uint32_t e[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
                         for (int k = 0; k < VEC; ++k)
-                            st_value<DT>(grow, nh + (uint64_t)v * VEC + k, g[k]);
+                            st_elem<DT>(grow, nh + (uint64_t)(b + i * kDThreads) * VEC + k,
+                                        DT == DT_FP32 ? e[k & 3] : e[k / 2] >> 16 * (k & 1) & 0xffff);
                     }
                 }
             }
         };
-        const bool again = !skip && (MODE != DISTILL_GRAD ? loads > 1 : false);
-        if (again)
-            load(xa, 0);
-        for (uint32_t l = 0; l < loads; l += 2) {
-            if (!skip && l + 1 < loads)
-                load(xb, l + 1);
-            emit(xa, l);
-            if (!skip && l + 2 < loads)
-                load(xa, l + 2);
-            if (l + 1 < loads)
-                emit(xb, l + 1);
+#pragma unroll
+        for (int i = 0; i < kHeld; i += kVecs)
+            emit(x + i, v0 + tid + (kHeld + i) * kDThreads);
+#pragma unroll 1
+        for (int i = 0; i < kHeld; i += kVecs) {
+            from_held(y, i);
+            emit(y, v0 + tid + i * kDThreads);
+        }
+#pragma unroll 1
+        for (uint32_t b = v0 + kPart; b < v1; b += kVecs * kDThreads) {
+            if (!skip)
+                load(y, b + tid);
+            emit(y, b + tid);
         }
         if (edge)
             st_value<DT>(grow, ei, zero ? 0.0f : __fmul_rn(row_exp(xe, st.m, p.scale), c));
         __syncthreads(); // before the listed ids' gradients replace what was written
-        // `part` neighbouring threads share an entry's search for its id's other places
-        int part = 1;
-        while (part < 32 && 2 * part * top <= kDThreads)
-            part *= 2;
         if (!zero)
-            for (int j0 = 0; j0 < top; j0 += kDThreads / part) {
-                const int j = j0 + tid / part;
-                const uint32_t i = j < top ? id[j] : kNone;
-                const bool own = i != kNone && mine(i);
-                float sum = 0.0f;
-                int first = top;
-                if (own)
-                    for (int k = tid % part; k < top; k += part)
-                        if (id[k] == i) {
-                            first = min(first, k);
+            for (uint32_t h = tid; h < 1u << p.slot_bits; h += kDThreads) {
+                const uint32_t e = slot[h];
+                if (e == kNone)
+                    continue;
+                const uint32_t j = e & kEntry, i = id[j];
+                if (!mine(i))
+                    continue;
+                float sum = prob[j];
+                if (e != j) { // the id's entries, in order
+                    sum = 0.0f;
+                    for (int k = 0; k < top; ++k)
+                        if (id[k] == i)
                             sum = __fadd_rn(sum, prob[k]);
-                        }
-                for (int o = 1; o < part; o *= 2) {
-                    sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
-                    first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
                 }
-                if (own && first == j && tid % part == 0) {
-                    const float q = __fdiv_rn(row_exp(logit[j], st.m, p.scale), st.z);
-                    st_value<DT>(grow, i, __fmul_rn(a, __fsub_rn(q, sum)));
-                }
+                const float q = __fdiv_rn(row_exp(logit[j], st.m, p.scale), st.z);
+                st_value<DT>(grow, i, __fmul_rn(a, __fsub_rn(q, sum)));
             }
     }
-    if (MODE != DISTILL_GRAD)
-        cluster.sync(); // no CTA leaves while another may read its statistics
 }
 
 // ------------------------------------------------------------------ host side
@@ -437,7 +514,11 @@ cudaError_t launch_distill(const DistillParams &p, uint64_t rows, uint32_t ctas,
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * ctas));
     cfg.blockDim = dim3(kDThreads);
+    cfg.dynamicSmemBytes = kHeld * kDThreads * 16;
     cfg.stream = stream;
+    static std::atomic<unsigned long long> ready{0};
+    if (cudaError_t e = large_smem_once(reinterpret_cast<const void *>(distill_kernel<DT, MODE>), (int)cfg.dynamicSmemBytes, ready))
+        return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ctas;
@@ -522,11 +603,15 @@ ccl_status_t distill_impl(int mode, const DistillArgs &a, cudaStream_t stream)
     p.top = a.top;
     p.inv_tau = inv_tau;
     p.scale = inv_tau * kLog2e;
-    // one CTA a row; where that leaves CTAs' places on the GPU empty, up to
-    // eight, as long as each has a full load of vectors
+    p.slot_bits = 5;
+    while (1u << p.slot_bits < 2 * a.top)
+        ++p.slot_bits;
+    // the fewest CTAs that hold a row; more, as long as each thread has a
+    // batch of vectors, while they leave places on the GPU empty
     const uint64_t bytes = a.vocab * es;
     uint32_t ctas = 1;
-    while (ctas < kMaxCluster && a.nrows * ctas < 152 * kDCtas && bytes >= 2 * ctas * kVecs * kDThreads * 16)
+    while (ctas < kMaxCluster && (bytes > (uint64_t)ctas * kPart * 16 ||
+                                  (a.nrows * ctas < 152 * kDCtas && bytes >= (uint64_t)2 * ctas * kVecs * kDThreads * 16)))
         ctas *= 2;
     const bool f = a.dtype == CCL_FP32;
     cudaError_t e;

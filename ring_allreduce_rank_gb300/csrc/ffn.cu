@@ -774,19 +774,10 @@ template <int EPI, bool A_MN, bool B_MN> cudaError_t launch_gemm(GemmParams &p, 
         units += q.units;
         ++p.nprob;
     }
-    // opt in to the shared memory, once per device (idempotent)
     static std::atomic<unsigned long long> ready{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    cudaError_t e = large_smem_once(reinterpret_cast<const void *>(ffn_gemm_kernel<EPI, A_MN, B_MN>), kGemmSmem, ready);
     if (e != cudaSuccess)
         return e;
-    const unsigned long long bit = 1ull << (dev & 63);
-    if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(ffn_gemm_kernel<EPI, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
-        if (e != cudaSuccess)
-            return e;
-        ready.fetch_or(bit, std::memory_order_relaxed);
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (unsigned)std::min<uint64_t>(units, kPairs));
     cfg.blockDim = dim3(kGemmThreads);

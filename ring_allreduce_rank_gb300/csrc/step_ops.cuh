@@ -3,6 +3,7 @@
 // host side's extents.
 #pragma once
 
+#include <atomic>
 #include <new>
 
 #include "ccl_internal.h"
@@ -69,6 +70,25 @@ template <class F> inline ccl_status_t guarded(F f)
     } catch (...) {
         return CCL_ERR_NO_MEMORY;
     }
+}
+
+// Opts a kernel in to `bytes` of dynamic shared memory on the current device,
+// once per device (`ready`: the kernel's own bits; doing it twice is harmless).
+inline cudaError_t large_smem_once(const void *kernel, int bytes, std::atomic<unsigned long long> &ready)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (ready.load(std::memory_order_relaxed) & bit)
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess)
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 constexpr size_t kAlign = 256;
