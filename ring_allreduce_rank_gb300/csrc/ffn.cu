@@ -40,9 +40,13 @@ constexpr int kTileM = 256, kTileN = 256, kTileK = 64; // a CTA pair's tile
 constexpr int kOperandBytes = 128 * kTileK * 2;        // one CTA's part of A or B in a stage
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kStages = 6;
+constexpr int kMaxStages = 6; // ffn_few_kernel's
+constexpr int kFewTokens = 256;
+constexpr int kFewBytes = 200 * 1024; // its stages', at most
 constexpr int kGemmThreads = 384; // producer, issuer, tensor memory, one idle warp, eight epilogue warps
 constexpr int kEpiWarps = 8;
-constexpr int kGemmSmem = kStages * kStageBytes + 1024 /* alignment */;
+constexpr int kTurnFloats = 32 * 33; // an epilogue warp's 32 x 32 values, rows padded against bank conflicts
+constexpr int kGemmSmem = kStages * kStageBytes + 1024 /* alignment */ + kEpiWarps * kTurnFloats * 4;
 constexpr int kGroupM = 8; // row tiles walked before the next column tile
 constexpr int kMaxProblems = 3;
 constexpr unsigned long long kWaitLimitNs = 4000000000ull;
@@ -69,6 +73,15 @@ struct GemmParams {
     uint16_t *h, *dg, *du;
     float *g, *u;
     uint32_t ldh; // row stride of h, dg and du (g and u: n)
+    int vectors;  // every row that the epilogue touches is 32-byte aligned and whole 16-column vectors
+};
+
+// ffn_few_kernel's: the same products with the weights as rows.
+struct FewParams {
+    GemmParams p;
+    uint32_t npad;   // tokens, rounded up to 16
+    uint32_t stages; // of 32 KiB of weights and npad * 128 bytes of activations
+    uint32_t bufs;   // accumulators in turn: 2, or 1 for more than 128 tokens
 };
 
 __device__ unsigned long long g_ffn_timeouts;
@@ -159,6 +172,32 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
                  : "memory");
 }
 
+// The same within one CTA.
+__device__ __forceinline__ void tma_load_own(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(map), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_own(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_own(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void tc_commit(uint32_t bar) // arrives at `bar` in both CTAs
 {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
@@ -172,6 +211,20 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
                  "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
                  "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
                  : "memory");
+}
+
+__device__ __forceinline__ void tc_load16(uint32_t addr, float *f)
+{
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        f[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ void tc_load32(uint32_t addr, float *f)
@@ -215,6 +268,16 @@ template <bool MN> __device__ __forceinline__ void load_operand(uint32_t dst, co
     }
 }
 
+template <bool MN> __device__ __forceinline__ void load_weights(uint32_t dst, const CUtensorMap *map, int mn, int k, uint32_t bar)
+{
+    if (MN) {
+        tma_load_own(dst, map, mn, k, bar);
+        tma_load_own(dst + kOperandBytes / 2, map, mn + 64, k, bar);
+    } else {
+        tma_load_own(dst, map, k, mn, bar);
+    }
+}
+
 // ------------------------------------------------------------------ activations
 
 __device__ __forceinline__ float sigmoid(float x)
@@ -245,102 +308,110 @@ __device__ __forceinline__ void activation(int act, float g, float &a, float &da
 
 // ------------------------------------------------------------------ epilogues
 
-// Eight bf16 values to row[col..col+8), those before column n.
-__device__ __forceinline__ void store8(uint16_t *row, uint32_t col, uint32_t n, const float *f)
-{
-    uint16_t *q = row + col;
-    if (col + 8 <= n && ((uintptr_t)q & 15) == 0) {
-        st16(q, pack<DT_BF16>(f));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (col + i < n)
-                st_value<DT_BF16>(q, i, f[i]);
-    }
-}
-
-__device__ __forceinline__ void load8(const uint16_t *row, uint32_t col, uint32_t n, float *f)
-{
-    const uint16_t *q = row + col;
-    if (col + 8 <= n && ((uintptr_t)q & 15) == 0) {
-        unpack<DT_BF16>(ld16(q), f);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            f[i] = col + i < n ? ld_value<DT_BF16>(q, i) : 0.0f;
-    }
-}
-
-__device__ __forceinline__ void store8(float *row, uint32_t col, uint32_t n, const float *f)
-{
-    float *q = row + col;
-    if (col + 8 <= n && ((uintptr_t)q & 15) == 0) {
-        st16(q, pack<DT_FP32>(f));
-        st16(q + 4, pack<DT_FP32>(f + 4));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (col + i < n)
-                gstore<float>(q + i, f[i]);
-    }
-}
-
-__device__ __forceinline__ void load8(const float *row, uint32_t col, uint32_t n, float *f)
-{
-    const float *q = row + col;
-    if (col + 8 <= n && ((uintptr_t)q & 15) == 0) {
-        unpack<DT_FP32>(ld16(q), f);
-        unpack<DT_FP32>(ld16(q + 4), f + 4);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            f[i] = col + i < n ? gload<float>(q + i) : 0.0f;
-    }
-}
-
-// The finished sums of eight columns of one row: v, and for EPI_GATED g = v
-// and u = w.
+// One finished sum: v, and for EPI_GATED g = v and u = w.
 template <int EPI>
-__device__ __forceinline__ void finish8(const GemmParams &p, const Problem &q, uint32_t row, uint32_t col, float *v,
-                                        float *w)
+__device__ __forceinline__ void finish1(const GemmParams &p, const Problem &q, uint32_t row, uint32_t col, float v, float w)
+{
+    const uint64_t at = (uint64_t)row * q.n + col, ath = (uint64_t)row * p.ldh + col;
+    float a, da;
+    if (EPI == EPI_GATED) {
+        if (p.g) {
+            gstore<float>(p.g + at, v);
+            gstore<float>(p.u + at, w);
+        }
+        activation(p.act, v, a, da);
+        st_value<DT_BF16>(p.h, ath, a * w);
+    } else if (EPI == EPI_BACKWARD) {
+        const float g = gload<float>(p.g + at), u = gload<float>(p.u + at);
+        activation(p.act, g, a, da);
+        st_value<DT_BF16>(p.h, ath, a * u);
+        st_value<DT_BF16>(p.dg, ath, v * u * da);
+        st_value<DT_BF16>(p.du, ath, v * a);
+    } else {
+        st_value<DT_BF16>(q.out, at, p.accumulate ? __fadd_rn(ld_value<DT_BF16>(q.out, at), v) : v);
+    }
+}
+
+// Sixteen fp32 values of one row as 32-byte vectors.
+struct Vals16 {
+    uint4 v[4];
+    __device__ __forceinline__ void load(const float *q)
+    {
+        ld32(q, v[0], v[1]);
+        ld32(q + 8, v[2], v[3]);
+    }
+    __device__ __forceinline__ void get(float *f) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            unpack<DT_FP32>(v[i], f + 4 * i);
+    }
+};
+
+__device__ __forceinline__ void store16(float *q, const float *f)
+{
+    st32(q, pack<DT_FP32>(f), pack<DT_FP32>(f + 4));
+    st32(q + 8, pack<DT_FP32>(f + 8), pack<DT_FP32>(f + 12));
+}
+
+__device__ __forceinline__ void store16(uint16_t *q, const float *f) { st32(q, pack<DT_BF16>(f), pack<DT_BF16>(f + 8)); }
+
+// What the epilogue reads of sixteen columns, asked for before it is needed.
+template <int EPI> struct Ahead16 {
+    Vals16 g, u;
+    __device__ __forceinline__ void load(const GemmParams &p, const Problem &q, uint32_t row, uint32_t col)
+    {
+        if (EPI == EPI_BACKWARD && row < q.m && col < q.n) {
+            g.load(p.g + (uint64_t)row * q.n + col);
+            u.load(p.u + (uint64_t)row * q.n + col);
+        }
+        if (EPI == EPI_STORE && p.accumulate && row < q.m && col < q.n)
+            ld32(static_cast<const uint16_t *>(q.out) + (uint64_t)row * q.n + col, g.v[0], g.v[1]);
+    }
+};
+
+// Sixteen finished sums of one row (p.vectors).
+template <int EPI>
+__device__ __forceinline__ void finish16(const GemmParams &p, const Problem &q, uint32_t row, uint32_t col,
+                                         const Ahead16<EPI> &ahead, float *v, float *w)
 {
     if (row >= q.m || col >= q.n)
         return;
-    float a[8], da[8];
+    float a[16], da;
     if (EPI == EPI_GATED) {
         if (p.g) {
-            store8(p.g + (uint64_t)row * q.n, col, q.n, v);
-            store8(p.u + (uint64_t)row * q.n, col, q.n, w);
+            store16(p.g + (uint64_t)row * q.n + col, v);
+            store16(p.u + (uint64_t)row * q.n + col, w);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            activation(p.act, v[i], a[i], da[i]);
+        for (int i = 0; i < 16; ++i) {
+            activation(p.act, v[i], a[i], da);
             a[i] *= w[i];
         }
-        store8(p.h + (uint64_t)row * p.ldh, col, q.n, a);
+        store16(p.h + (uint64_t)row * p.ldh + col, a);
     } else if (EPI == EPI_BACKWARD) {
-        float g[8], u[8];
-        load8(p.g + (uint64_t)row * q.n, col, q.n, g);
-        load8(p.u + (uint64_t)row * q.n, col, q.n, u);
+        float g[16], u[16];
+        ahead.g.get(g);
+        ahead.u.get(u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            activation(p.act, g[i], a[i], da[i]);
-            g[i] = v[i] * u[i] * da[i]; // dg
-            v[i] = v[i] * a[i];         // du
-            a[i] = a[i] * u[i];         // h
+        for (int i = 0; i < 16; ++i) {
+            activation(p.act, g[i], a[i], da);
+            g[i] = v[i] * u[i] * da; // dg
+            v[i] = v[i] * a[i];      // du
+            a[i] = a[i] * u[i];      // h
         }
-        store8(p.h + (uint64_t)row * p.ldh, col, q.n, a);
-        store8(p.dg + (uint64_t)row * p.ldh, col, q.n, g);
-        store8(p.du + (uint64_t)row * p.ldh, col, q.n, v);
+        store16(p.h + (uint64_t)row * p.ldh + col, a);
+        store16(p.dg + (uint64_t)row * p.ldh + col, g);
+        store16(p.du + (uint64_t)row * p.ldh + col, v);
     } else {
-        uint16_t *out = static_cast<uint16_t *>(q.out) + (uint64_t)row * q.n;
         if (p.accumulate) {
-            load8(out, col, q.n, a);
+            unpack<DT_BF16>(ahead.g.v[0], a);
+            unpack<DT_BF16>(ahead.g.v[1], a + 8);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 16; ++i)
                 v[i] = __fadd_rn(a[i], v[i]);
         }
-        store8(out, col, q.n, v);
+        store16(static_cast<uint16_t *>(q.out) + (uint64_t)row * q.n + col, v);
     }
 }
 
@@ -476,47 +547,74 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
                 tc_commit(acc_full + 8 * buf);
         }
     } else if (warp >= 4) {
-        // epilogue: warp w reads lanes 32 (w % 4) .. + 32 and half of the columns
+        // epilogue: warp w reads lanes 32 (w % 4) .. + 32 and half of the
+        // columns.  Vectors: a lane keeps its row, sixteen columns at a time,
+        // what it reads asked for one step ahead.  Otherwise the values are
+        // turned in shared memory, so that a warp's accesses run along a row.
         const uint32_t half = (warp - 4) / 4;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32;
         const uint32_t leader_empty = in_cta(acc_empty, 0);
+        float *turn = reinterpret_cast<float *>(raw + (stages - smem_u32(raw)) + kStages * kStageBytes) + (warp - 4) * kTurnFloats;
         uint32_t t = 0;
         for (uint32_t i = pair; i < total; i += pairs, ++t) {
             const Unit u = unit_at(p, i);
             const Problem &q = p.prob[u.prob];
             const uint32_t buf = t & 1;
+            const uint32_t row0 = u.m * kTileM + rank * 128 + lanes, row = row0 + lane;
+            constexpr uint32_t kCols = EPI == EPI_GATED ? 64 : 128;
+            const uint32_t c0 = half * kCols, col0 = u.n * (2 * kCols) + c0;
+            Ahead16<EPI> ahead;
+            if (p.vectors && p.splits == 1)
+                ahead.load(p, q, row, col0);
             if (!__all_sync(0xffffffffu, mbar_wait(acc_full + 8 * buf, (t >> 1) & 1, &gave_up)))
                 break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t row = u.m * kTileM + rank * 128 + lanes + lane;
             const uint32_t acc = tmem + buf * kTileN + (lanes << 16);
             if (p.splits > 1) {
                 const uint64_t width = (uint64_t)q.nt * kTileN;
                 float *out = q.partial + ((uint64_t)u.split * q.m + row) * width + u.n * kTileN;
-                for (uint32_t c = half * 128; c < half * 128 + 128; c += 32) {
-                    float v[32];
-                    tc_load32(acc + c, v);
+                for (uint32_t c = half * 128; c < half * 128 + 128; c += 16) {
+                    float v[16];
+                    tc_load16(acc + c, v);
                     if (row < q.m)
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            st16(out + c + j, pack<DT_FP32>(v + j));
+                        store16(out + c, v);
                 }
-            } else if (EPI == EPI_GATED) {
-                for (uint32_t c = half * 64; c < half * 64 + 64; c += 32) {
-                    float v[32], w[32];
-                    tc_load32(acc + c, v);
-                    tc_load32(acc + 128 + c, w);
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8)
-                        finish8<EPI>(p, q, row, u.n * 128 + c + j, v + j, w + j);
+            } else if (p.vectors) {
+#pragma unroll 2
+                for (uint32_t c = 0; c < kCols; c += 16) {
+                    float v[16], w[16];
+                    tc_load16(acc + c0 + c, v);
+                    if (EPI == EPI_GATED)
+                        tc_load16(acc + 128 + c0 + c, w);
+                    Ahead16<EPI> next;
+                    if (c + 16 < kCols)
+                        next.load(p, q, row, col0 + c + 16);
+                    finish16<EPI>(p, q, row, col0 + c, ahead, v, w);
+                    ahead = next;
                 }
             } else {
-                for (uint32_t c = half * 128; c < half * 128 + 128; c += 32) {
+                // rows of 32 columns, or of 16 columns of g and the same of u
+                constexpr uint32_t kWide = EPI == EPI_GATED ? 16 : 32, kRows = 32 / kWide;
+                for (uint32_t c = 0; c < kCols; c += kWide) {
                     float v[32];
-                    tc_load32(acc + c, v);
+                    if (EPI == EPI_GATED) {
+                        tc_load16(acc + c0 + c, v);
+                        tc_load16(acc + 128 + c0 + c, v + 16);
+                    } else {
+                        tc_load32(acc + c0 + c, v);
+                    }
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8)
-                        finish8<EPI>(p, q, row, u.n * kTileN + c + j, v + j, v + j);
+                    for (int j = 0; j < 32; ++j)
+                        turn[lane * 33 + j] = v[j];
+                    __syncwarp();
+                    const uint32_t cc = lane % kWide, col = col0 + c + cc;
+#pragma unroll 8
+                    for (uint32_t r = lane / kWide; r < 32; r += kRows) {
+                        const float *from = turn + r * 33 + cc;
+                        if (row0 + r < q.m && col < q.n)
+                            finish1<EPI>(p, q, row0 + r, col, from[0], EPI == EPI_GATED ? from[16] : 0.0f);
+                    }
+                    __syncwarp();
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -537,37 +635,195 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
+// ------------------------------------------------------------------ few tokens
+
+// The same products for at most 256 tokens, with the weights as the
+// accumulator's rows and the tokens as its columns, so that the tensor cores
+// work on the tokens there are and not on a 256-row tile of them: one CTA a
+// unit of two 128-row blocks of weights (EPI_GATED: the same rows of Wg and
+// Wu), which share the tokens' stage.  Bound by reading the weights.
+template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1) ffn_few_kernel(const __grid_constant__ FewParams fp)
+{
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t bars[2 * kMaxStages + 4];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int gave_up;
+    const GemmParams &p = fp.p;
+    const Problem &q = p.prob[0];
+    const uint32_t stages = (smem_u32(raw) + 1023) & ~1023u;
+    const uint32_t stage_bytes = 2 * kOperandBytes + fp.npad * 128;
+    const uint32_t full = smem_u32(&bars[0]), empty = smem_u32(&bars[kMaxStages]);
+    const uint32_t acc_full = smem_u32(&bars[2 * kMaxStages]), acc_empty = smem_u32(&bars[2 * kMaxStages + 2]);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + 8 * i, 1);
+            mbar_init(acc_empty + 8 * i, kEpiWarps);
+        }
+        gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = tmem_slot;
+    chain_entry();
+
+    if (warp == 0 && lane == 0) {
+        uint32_t s = 0, phase = 0;
+        bool ok = true;
+        auto next = [&] {
+            if (++s == fp.stages) {
+                s = 0;
+                phase ^= 1;
+            }
+        };
+        for (uint32_t i = blockIdx.x; ok && i < q.units; i += gridDim.x) {
+            const Unit u = unit_at(p, i);
+            for (uint32_t kb = u.kb0; kb < u.kb1; ++kb) {
+                if (!(ok = mbar_wait(empty + 8 * s, phase ^ 1, &gave_up)))
+                    break;
+                mbar_expect(full + 8 * s, stage_bytes);
+                const uint32_t seg = kb >= q.kblocks ? 1 : 0;
+                const int k = (int)((kb - seg * q.kblocks) * kTileK);
+                const uint32_t at = stages + s * stage_bytes;
+                // a: the weights (EPI_GATED: Wg and Wu; else one per segment); b: the tokens
+                const int r0 = EPI == EPI_GATED ? (int)(u.n * 128) : (int)(u.n * 256);
+                load_weights<A_MN>(at, EPI == EPI_GATED ? &q.a[0] : &q.a[seg], r0, k, full + 8 * s);
+                load_weights<A_MN>(at + kOperandBytes, EPI == EPI_GATED ? &q.a[1] : &q.a[seg], EPI == EPI_GATED ? r0 : r0 + 128, k, full + 8 * s);
+                tma_load_own(at + 2 * kOperandBytes, &q.b[seg], k, 0, full + 8 * s);
+                next();
+            }
+        }
+        // the issuer's last arrivals come while the CTA is here
+        for (uint32_t i = 0; ok && i < fp.stages; ++i) {
+            ok = mbar_wait(empty + 8 * s, phase ^ 1, &gave_up);
+            next();
+        }
+    } else if (warp == 1 && lane == 0) {
+        const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (A_MN ? 1u << 15 : 0) | (fp.npad >> 3) << 17 | (128u >> 4) << 24;
+        uint32_t s = 0, phase = 0, t = 0;
+        bool ok = true;
+        for (uint32_t i = blockIdx.x; ok && i < q.units; i += gridDim.x, ++t) {
+            const Unit u = unit_at(p, i);
+            const uint32_t buf = t % fp.bufs, round = t / fp.bufs;
+            if (!(ok = mbar_wait(acc_empty + 8 * buf, (round & 1) ^ 1, &gave_up)))
+                break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            for (uint32_t kb = u.kb0; kb < u.kb1; ++kb) {
+                if (!(ok = mbar_wait(full + 8 * s, phase, &gave_up)))
+                    break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t at = stages + s * stage_bytes;
+#pragma unroll
+                for (int k = 0; k < kTileK / 16; ++k)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        tc_mma_own(tmem + (buf * 2 + j) * fp.npad, operand_desc<A_MN>(at + j * kOperandBytes + k * k_step<A_MN>()),
+                                   operand_desc<false>(at + 2 * kOperandBytes + k * k_step<false>()), idesc, kb > u.kb0 || k > 0);
+                tc_commit_own(empty + 8 * s);
+                if (++s == fp.stages) {
+                    s = 0;
+                    phase ^= 1;
+                }
+            }
+            if (ok)
+                tc_commit_own(acc_full + 8 * buf);
+        }
+    } else if (warp >= 4) {
+        // a lane is a weight row, so that a warp's accesses run along a token's
+        // row.  EPI_GATED: the two halves of the warps take the tokens in turn,
+        // else one block of rows each.
+        const uint32_t half = (warp - 4) / 4, lanes = (uint32_t)(warp & 3) * 32;
+        uint32_t t = 0;
+        for (uint32_t i = blockIdx.x; i < q.units; i += gridDim.x, ++t) {
+            const Unit u = unit_at(p, i);
+            const uint32_t buf = t % fp.bufs, round = t / fp.bufs;
+            if (!__all_sync(0xffffffffu, mbar_wait(acc_full + 8 * buf, round & 1, &gave_up)))
+                break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t acc = tmem + buf * 2 * fp.npad + (lanes << 16);
+            const uint32_t col = EPI == EPI_GATED ? u.n * 128 + lanes + lane : u.n * 256 + half * 128 + lanes + lane;
+            const uint64_t width = (uint64_t)q.nt * kTileN;
+            for (uint32_t c = EPI == EPI_GATED ? half * 16 : 0; c < fp.npad; c += EPI == EPI_GATED ? 32 : 16) {
+                float v[16], w[16];
+                tc_load16(acc + (EPI == EPI_GATED ? 0 : half * fp.npad) + c, v);
+                if (EPI == EPI_GATED)
+                    tc_load16(acc + fp.npad + c, w);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    if (c + j >= q.m)
+                        break;
+                    if (p.splits > 1) {
+                        float *out = q.partial + ((uint64_t)u.split * q.m + c + j) * width + u.n * kTileN + lanes + lane;
+                        gstore<float>(out + (EPI == EPI_GATED ? 0 : half * 128), v[j]);
+                        if (EPI == EPI_GATED)
+                            gstore<float>(out + 128, w[j]);
+                    } else if (col < q.n) {
+                        finish1<EPI>(p, q, c + j, col, v[j], EPI == EPI_GATED ? w[j] : 0.0f);
+                    }
+                }
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(acc_empty + 8 * buf);
+        }
+    }
+    __syncwarp();
+    if (gave_up) // copies still in flight land before the CTA's memory is given back
+        for (int i = 0; i < 1000; ++i)
+            __nanosleep(1000);
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
 // ------------------------------------------------------------------ split sums
 
-// The splits' sums of one product, added in order, eight columns a thread.
+// The splits' sums of one product, added in order, a column a thread.
 template <int EPI> __global__ void __launch_bounds__(256) ffn_join_kernel(const __grid_constant__ GemmParams p)
 {
     chain_entry();
     for (uint32_t i = 0; i < p.nprob; ++i) {
         const Problem &q = p.prob[i];
-        const uint32_t cols = (q.n + 7) / 8;
         const uint64_t width = (uint64_t)q.nt * kTileN, slab = (uint64_t)q.m * width;
-        for (uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x; e < (uint64_t)q.m * cols; e += (uint64_t)gridDim.x * 256) {
-            const uint32_t row = (uint32_t)(e / cols), col = (uint32_t)(e % cols) * 8;
+        const uint32_t blocks = (q.n + 255) / 256; // of 256 columns
+        for (uint64_t e = blockIdx.x; e < (uint64_t)q.m * blocks; e += gridDim.x) {
+            const uint32_t row = (uint32_t)(e / blocks), col = (uint32_t)(e % blocks) * 256 + threadIdx.x;
+            if (col >= q.n)
+                continue;
             // EPI_GATED: 128 columns of g, then the same of u, in each tile
-            const uint64_t at = row * width + (EPI == EPI_GATED ? col / 128 * 256 + col % 128 : col);
-            float v[8], w[8], f[8];
-            load8(q.partial + at, 0, 8, v);
-            if (EPI == EPI_GATED)
-                load8(q.partial + at + 128, 0, 8, w);
-            for (uint32_t s = 1; s < p.splits; ++s) {
-                load8(q.partial + s * slab + at, 0, 8, f);
+            const float *at = q.partial + row * width + (EPI == EPI_GATED ? col / 128 * 256 + col % 128 : col);
+            float v = 0.0f, w = 0.0f, f[4], h[4];
+            for (uint32_t s0 = 0; s0 < p.splits; s0 += 4) { // four loads in flight
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] = __fadd_rn(v[j], f[j]);
-                if (EPI == EPI_GATED) {
-                    load8(q.partial + s * slab + at + 128, 0, 8, f);
+                for (int s = 0; s < 4; ++s)
+                    if (s0 + s < p.splits) {
+                        f[s] = gload<float>(at + (s0 + s) * slab);
+                        if (EPI == EPI_GATED)
+                            h[s] = gload<float>(at + (s0 + s) * slab + 128);
+                    }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        w[j] = __fadd_rn(w[j], f[j]);
-                }
+                for (int s = 0; s < 4; ++s)
+                    if (s0 + s < p.splits) {
+                        v = __fadd_rn(v, f[s]);
+                        if (EPI == EPI_GATED)
+                            w = __fadd_rn(w, h[s]);
+                    }
             }
-            finish8<EPI>(p, q, row, col, v, w);
+            finish1<EPI>(p, q, row, col, v, w);
         }
     }
 }
@@ -575,19 +831,34 @@ template <int EPI> __global__ void __launch_bounds__(256) ffn_join_kernel(const 
 // ------------------------------------------------------------------ operands TMA cannot address
 
 struct PackParams {
-    const uint16_t *src;
-    uint16_t *dst;
-    uint64_t rows;
-    uint32_t cols, ld;
+    struct {
+        const uint16_t *src;
+        uint16_t *dst;
+        uint32_t cols, ld;
+        uint64_t vectors; // rows * ld / 8
+    } m[5];
+    int n;
 };
 
-// Rows of `cols` elements to rows `ld` apart (ld a multiple of 8).
-__global__ void __launch_bounds__(256) ffn_pack_kernel(PackParams p)
+// Rows of `cols` elements to rows `ld` apart (ld a multiple of 8), the rest of
+// a row zero; a thread writes a vector of eight.
+__global__ void __launch_bounds__(256) ffn_pack_kernel(const __grid_constant__ PackParams p)
 {
     chain_entry();
-    for (uint64_t r = blockIdx.x; r < p.rows; r += gridDim.x)
-        for (uint32_t c = threadIdx.x; c < p.cols; c += 256)
-            gstore<uint16_t>(p.dst + r * p.ld + c, gload<uint16_t>(p.src + r * p.cols + c));
+    for (int k = 0; k < p.n; ++k) {
+        const auto &m = p.m[k];
+        const uint32_t per = m.ld / 8;
+        for (uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x; e < m.vectors; e += (uint64_t)gridDim.x * 256) {
+            const uint64_t r = e / per;
+            const uint32_t c = (uint32_t)(e % per) * 8;
+            const uint16_t *src = m.src + r * m.cols + c;
+            uint32_t h[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                h[i] = c + i < m.cols ? gload<uint16_t>(src + i) : 0;
+            st16(m.dst + e * 8, make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16));
+        }
+    }
 }
 
 // ------------------------------------------------------------------ host side
@@ -615,10 +886,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 // A map whose boxes are 64 columns wide: as K-major operand tiles (128 rows of
 // 64 k values) or as MN-major ones (64 k rows of 64 values).  What lies
 // outside the matrix reads as zero.
-bool encode(CUtensorMap *map, const Matrix &m, bool mn)
+bool encode(CUtensorMap *map, const Matrix &m, bool mn, uint32_t box_rows = 128)
 {
     const cuuint64_t dim[2] = {m.cols, m.rows}, stride[1] = {m.ld * 2};
-    const cuuint32_t box[2] = {64, mn ? 64u : 128u}, step[2] = {1, 1};
+    const cuuint32_t box[2] = {64, mn ? 64u : box_rows}, step[2] = {1, 1};
     return encode_fn() &&
            encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(m.ptr), dim, stride, box, step,
                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -627,21 +898,26 @@ bool encode(CUtensorMap *map, const Matrix &m, bool mn)
 
 uint32_t tiles_of(uint64_t n, uint32_t t) { return (uint32_t)((n + t - 1) / t); }
 
-constexpr int kPairs = 76; // CTA pairs of the GPU's 152 SMs
+constexpr int kPairs = 76, kSms = 152; // CTA pairs and SMs of the GPU
 constexpr uint32_t kMaxSplits = 16;
 
 // How many parts the sum over K is cut into: the number that minimises the
-// rounds of CTA pairs times a part's length, plus the join's traffic.  A
-// block of K takes about 0.35 us a pair, a tile's fill and epilogue about 3,
-// a join about 4 and its bytes at 6 TB/s.  Few tiles (few tokens, narrow
-// layers) would otherwise leave most SMs idle.
-uint32_t choose_splits(uint64_t tiles, uint64_t kblocks, uint64_t partial_bytes)
+// rounds of CTA pairs (CTAs, for few tokens) times a part's length, plus the
+// join's.  A block of K takes a pair about 0.35 us of products; a CTA with few
+// tokens reads its 32 KiB of weights in 0.4 us alone, and at the memory's rate
+// with the others; a unit's fill and epilogue take about 3 us and 1.5 us, a
+// join about 3 and its bytes at 6 TB/s.  Without it a product of few tiles
+// (few tokens, narrow layers) would leave most SMs idle.
+uint32_t choose_splits(uint64_t tiles, uint64_t kblocks, uint64_t partial_bytes, bool few)
 {
     uint32_t best = 1;
     double cost = 0;
+    const uint64_t slots = few ? kSms : kPairs;
     for (uint32_t s = 1; s <= kMaxSplits && s <= kblocks; ++s) {
-        const double rounds = (double)((tiles * s + kPairs - 1) / kPairs);
-        const double c = rounds * ((double)((kblocks + s - 1) / s) * 0.35 + 3.0) + (s > 1 ? 4.0 + 2.0 * s * (double)partial_bytes / 6e6 : 0.0);
+        const double rounds = (double)((tiles * s + slots - 1) / slots);
+        const double block = few ? std::max(0.4, 0.005 * (double)std::min(slots, tiles * s)) : 0.35;
+        const double c = rounds * ((double)((kblocks + s - 1) / s) * block + (few ? 1.5 : 3.0)) +
+                         (s > 1 ? 3.0 + 2.0 * s * (double)partial_bytes / 6e6 : 0.0);
         if (s == 1 || c < cost * 0.97) {
             best = s;
             cost = c;
@@ -658,7 +934,7 @@ struct Shape {
 struct Launch {
     Shape s[kMaxProblems];
     int n;
-    bool gated;
+    bool gated, few; // few: by ffn_few_kernel
     uint32_t splits;
     size_t partial; // bytes of all splits
     void plan()
@@ -666,18 +942,17 @@ struct Launch {
         uint64_t tiles = 0, kb = 0;
         size_t bytes = 0;
         for (int i = 0; i < n; ++i) {
-            tiles += (uint64_t)tiles_of(s[i].m, kTileM) * tiles_of(s[i].n, gated ? 128 : kTileN);
+            tiles += (few ? 1 : (uint64_t)tiles_of(s[i].m, kTileM)) * tiles_of(s[i].n, gated ? 128 : kTileN);
             kb = std::max<uint64_t>(kb, (uint64_t)tiles_of(s[i].k, kTileK) * s[i].segs);
             bytes += up(s[i].m * (size_t)tiles_of(s[i].n, gated ? 128 : kTileN) * kTileN * 4);
         }
-        splits = choose_splits(tiles, kb, bytes);
+        splits = choose_splits(tiles, kb, bytes, few);
         partial = splits > 1 ? bytes * splits : 0;
     }
 };
 
 struct FfnPlan {
     uint64_t t, d, f, dp, fp; // tokens, model width, inner width, padded widths
-    bool pack_d, pack_f, pack_all;
     Launch up_, down, dh, dx, dw;
     // offsets into the work buffer
     size_t h, dg, du, x, wg, wu, wd, dy, partial, bytes;
@@ -694,13 +969,13 @@ bool make_plan(size_t t, size_t d, size_t f, bool backward, bool aligned, FfnPla
     p->d = d;
     p->f = f;
     p->dp = (d + 7) / 8 * 8;
-    p->fp = (f + 7) / 8 * 8;
-    const bool pd = p->dp != d || !aligned, pf = p->fp != f || !aligned;
-    p->up_ = Launch{{{t, f, d, 1}}, 1, true, 1, 0};
-    p->down = Launch{{{t, d, f, 1}}, 1, false, 1, 0};
-    p->dh = Launch{{{t, f, d, 1}}, 1, false, 1, 0};
-    p->dx = Launch{{{t, d, f, 2}}, 1, false, 1, 0};
-    p->dw = Launch{{{f, d, t, 1}, {f, d, t, 1}, {d, f, t, 1}}, 3, false, 1, 0};
+    p->fp = (f + 15) / 16 * 16; // h, dg and du in rows of whole 32-byte vectors
+    const bool pd = p->dp != d || !aligned, pf = f % 8 || !aligned, few = t <= kFewTokens;
+    p->up_ = Launch{{{t, f, d, 1}}, 1, true, few, 1, 0};
+    p->down = Launch{{{t, d, f, 1}}, 1, false, few, 1, 0};
+    p->dh = Launch{{{t, f, d, 1}}, 1, false, few, 1, 0};
+    p->dx = Launch{{{t, d, f, 2}}, 1, false, few, 1, 0};
+    p->dw = Launch{{{f, d, t, 1}, {f, d, t, 1}, {d, f, t, 1}}, 3, false, false, 1, 0};
     size_t at = 0, partial = 0;
     auto take = [&](size_t n) {
         const size_t o = at;
@@ -730,39 +1005,53 @@ bool make_plan(size_t t, size_t d, size_t f, bool backward, bool aligned, FfnPla
     return true;
 }
 
-cudaError_t launch_pack(const void *src, void *dst, uint64_t rows, uint64_t cols, uint64_t ld, cudaStream_t stream)
-{
-    const PackParams p{static_cast<const uint16_t *>(src), static_cast<uint16_t *>(dst), rows, (uint32_t)cols, (uint32_t)ld};
-    const cudaError_t e = launch_chained(ffn_pack_kernel, dim3((unsigned)std::min<uint64_t>(rows, 8 * 152)), dim3(256), 0, stream, p);
-    if (e == cudaSuccess)
-        count_launches(1);
-    return e;
-}
-
-// The operand as it lies where TMA can address it (16-byte aligned base and
-// rows), else copied to rows of a padded stride.
-cudaError_t operand(const void *src, uint64_t rows, uint64_t cols, uint64_t ld, char *work, size_t at, Matrix *m,
-                    cudaStream_t stream)
-{
-    if ((uintptr_t)src % 16 == 0 && cols == ld) {
-        *m = Matrix{src, rows, cols, cols};
-        return cudaSuccess;
+// The operands as they lie where TMA can address them (16-byte aligned base
+// and rows), else copied to rows of a padded stride, all in one launch.
+class Operands {
+  public:
+    explicit Operands(char *work) : work_(work) {}
+    Matrix add(const void *src, uint64_t rows, uint64_t cols, size_t at)
+    {
+        const uint64_t ld = (cols + 7) / 8 * 8;
+        if ((uintptr_t)src % 16 == 0 && cols == ld)
+            return Matrix{src, rows, cols, cols};
+        auto &m = p_.m[p_.n++];
+        m.src = static_cast<const uint16_t *>(src);
+        m.dst = reinterpret_cast<uint16_t *>(work_ + at);
+        m.cols = (uint32_t)cols;
+        m.ld = (uint32_t)ld;
+        m.vectors = rows * ld / 8;
+        most_ = std::max(most_, m.vectors);
+        return Matrix{m.dst, rows, cols, ld};
     }
-    *m = Matrix{work + at, rows, cols, ld};
-    return launch_pack(src, work + at, rows, cols, ld, stream);
-}
+    cudaError_t copy(cudaStream_t stream)
+    {
+        if (p_.n == 0)
+            return cudaSuccess;
+        const cudaError_t e = launch_chained(ffn_pack_kernel, dim3((unsigned)std::min<uint64_t>((most_ + 255) / 256, 8 * kSms)), dim3(256), 0, stream, p_);
+        if (e == cudaSuccess)
+            count_launches(1);
+        return e;
+    }
 
-template <int EPI, bool A_MN, bool B_MN> cudaError_t launch_gemm(GemmParams &p, const Launch &l, char *partial, cudaStream_t stream)
+  private:
+    PackParams p_{};
+    char *work_;
+    uint64_t most_ = 0;
+};
+
+// Fills in what the launch's problems share; the maps are the caller's.
+cudaError_t set_problems(GemmParams &p, const Launch &l, char *partial, uint64_t *units)
 {
-    uint64_t units = 0;
-    p.nprob = 0;
+    *units = 0;
+    p.nprob = (uint32_t)l.n;
     p.splits = l.splits;
     for (int i = 0; i < l.n; ++i) {
         Problem &q = p.prob[i];
         const Shape &s = l.s[i];
         q.m = (uint32_t)s.m;
         q.n = (uint32_t)s.n;
-        q.mt = tiles_of(s.m, kTileM);
+        q.mt = l.few ? 1 : tiles_of(s.m, kTileM);
         q.nt = tiles_of(s.n, l.gated ? 128 : kTileN);
         q.kblocks = tiles_of(s.k, kTileK);
         q.segs = s.segs;
@@ -771,12 +1060,32 @@ template <int EPI, bool A_MN, bool B_MN> cudaError_t launch_gemm(GemmParams &p, 
         q.units = q.mt * q.nt * l.splits;
         q.partial = reinterpret_cast<float *>(partial);
         partial += up(s.m * (size_t)q.nt * kTileN * 4) * l.splits;
-        units += q.units;
-        ++p.nprob;
+        *units += q.units;
     }
+    return cudaSuccess;
+}
+
+template <int EPI> cudaError_t launch_join(const GemmParams &p, cudaStream_t stream)
+{
+    if (p.splits == 1)
+        return cudaSuccess;
+    uint64_t blocks = 0;
+    for (uint32_t i = 0; i < p.nprob; ++i)
+        blocks = std::max<uint64_t>(blocks, (uint64_t)p.prob[i].m * ((p.prob[i].n + 255) / 256));
+    const cudaError_t e = launch_chained(ffn_join_kernel<EPI>, dim3((unsigned)std::min<uint64_t>(blocks, 8 * kSms)), dim3(256), 0, stream, p);
+    if (e == cudaSuccess)
+        count_launches(1);
+    return e;
+}
+
+// A product (A rows: tokens, or for weight gradients units) on CTA pairs.
+template <int EPI, bool A_MN, bool B_MN> cudaError_t launch_gemm(GemmParams &p, const Launch &l, char *partial, cudaStream_t stream)
+{
+    uint64_t units;
+    cudaError_t e = set_problems(p, l, partial, &units);
     static std::atomic<unsigned long long> ready{0};
-    cudaError_t e = large_smem_once(reinterpret_cast<const void *>(ffn_gemm_kernel<EPI, A_MN, B_MN>), kGemmSmem, ready);
-    if (e != cudaSuccess)
+    if (e != cudaSuccess ||
+        (e = large_smem_once(reinterpret_cast<const void *>(ffn_gemm_kernel<EPI, A_MN, B_MN>), kGemmSmem, ready)) != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (unsigned)std::min<uint64_t>(units, kPairs));
@@ -794,16 +1103,33 @@ template <int EPI, bool A_MN, bool B_MN> cudaError_t launch_gemm(GemmParams &p, 
     if ((e = cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<EPI, A_MN, B_MN>, p)) != cudaSuccess)
         return e;
     count_launches(1);
-    if (l.splits > 1) {
-        uint64_t items = 0;
-        for (int i = 0; i < l.n; ++i)
-            items = std::max<uint64_t>(items, l.s[i].m * ((l.s[i].n + 7) / 8));
-        const dim3 grid((unsigned)std::min<uint64_t>((items + 255) / 256, 8 * 152));
-        if ((e = launch_chained(ffn_join_kernel<EPI>, grid, dim3(256), 0, stream, p)) != cudaSuccess)
-            return e;
-        count_launches(1);
-    }
-    return cudaSuccess;
+    return launch_join<EPI>(p, stream);
+}
+
+// A product of few tokens: weights w[0], w[1] (EPI_GATED: of g and u, else of
+// each segment; MN: their columns are the product's rows), tokens' rows x[].
+template <int EPI, bool A_MN>
+ccl_status_t launch_few(GemmParams &p, const Launch &l, const Matrix *w, const Matrix *x, char *partial, cudaStream_t stream)
+{
+    FewParams fp;
+    fp.npad = (uint32_t)(l.s[0].m + 15) / 16 * 16;
+    fp.stages = std::min<uint32_t>(kMaxStages, kFewBytes / (2 * kOperandBytes + fp.npad * 128));
+    fp.bufs = fp.npad > 128 ? 1 : 2;
+    uint64_t units;
+    cudaError_t e = set_problems(p, l, partial, &units);
+    static std::atomic<unsigned long long> ready{0};
+    if (e != cudaSuccess ||
+        (e = large_smem_once(reinterpret_cast<const void *>(ffn_few_kernel<EPI, A_MN>), kFewBytes + 1024, ready)) != cudaSuccess)
+        return from_cuda(e);
+    Problem &q = p.prob[0];
+    for (uint32_t i = 0; i < (l.gated ? 2 : q.segs); ++i)
+        if (!encode(&q.a[i], w[i], A_MN) || (i < q.segs && !encode(&q.b[i], x[i], false, fp.npad)))
+            return CCL_ERR_CUDA;
+    fp.p = p;
+    if ((e = launch_chained(ffn_few_kernel<EPI, A_MN>, dim3((unsigned)std::min<uint64_t>(units, kSms)), dim3(kGemmThreads), kFewBytes + 1024, stream, fp)) != cudaSuccess)
+        return from_cuda(e);
+    count_launches(1);
+    return from_cuda(launch_join<EPI>(p, stream));
 }
 
 struct FfnArgs {
@@ -878,26 +1204,36 @@ ccl_status_t gated_ffn_impl(const FfnArgs &a, void *out, cudaStream_t stream)
         return st;
     CCL_DBG_FFN(w, r, stream);
     char *work = static_cast<char *>(a.work);
-    Matrix x, wg, wu, wd;
-    cudaError_t e;
-    if ((e = operand(a.x, a.t, a.d, pl.dp, work, pl.x, &x, stream)) || (e = operand(a.wg, a.f, a.d, pl.dp, work, pl.wg, &wg, stream)) ||
-        (e = operand(a.wu, a.f, a.d, pl.dp, work, pl.wu, &wu, stream)) || (e = operand(a.wd, a.d, a.f, pl.fp, work, pl.wd, &wd, stream)))
-        return from_cuda(e);
+    Operands ops(work);
+    const Matrix x = ops.add(a.x, a.t, a.d, pl.x), wd = ops.add(a.wd, a.d, a.f, pl.wd);
+    const Matrix w2[2] = {ops.add(a.wg, a.f, a.d, pl.wg), ops.add(a.wu, a.f, a.d, pl.wu)};
     const Matrix h{work + pl.h, a.t, a.f, pl.fp};
+    if (cudaError_t e = ops.copy(stream))
+        return from_cuda(e);
     GemmParams p{};
     p.act = (int)a.act;
     p.h = reinterpret_cast<uint16_t *>(work + pl.h);
     p.g = a.saved;
     p.u = a.saved ? a.saved + a.t * a.f : nullptr;
     p.ldh = (uint32_t)pl.fp;
-    if (!encode(&p.prob[0].a[0], x, false) || !encode(&p.prob[0].b[0], wg, false) || !encode(&p.prob[0].b[1], wu, false))
+    char *partial = work + pl.partial;
+    p.vectors = a.f % 16 == 0 && (uintptr_t)a.saved % 32 == 0;
+    Problem &q = p.prob[0];
+    if (pl.up_.few) {
+        if (ccl_status_t st = launch_few<EPI_GATED, false>(p, pl.up_, w2, &x, partial, stream))
+            return st;
+        q.out = out;
+        return launch_few<EPI_STORE, false>(p, pl.down, &wd, &h, partial, stream);
+    }
+    if (!encode(&q.a[0], x, false) || !encode(&q.b[0], w2[0], false) || !encode(&q.b[1], w2[1], false))
         return CCL_ERR_CUDA;
-    if ((e = launch_gemm<EPI_GATED, false, false>(p, pl.up_, work + pl.partial, stream)))
+    if (cudaError_t e = launch_gemm<EPI_GATED, false, false>(p, pl.up_, partial, stream))
         return from_cuda(e);
-    p.prob[0].out = out;
-    if (!encode(&p.prob[0].a[0], h, false) || !encode(&p.prob[0].b[0], wd, false))
+    q.out = out;
+    p.vectors = a.d % 16 == 0 && (uintptr_t)out % 32 == 0;
+    if (!encode(&q.a[0], h, false) || !encode(&q.b[0], wd, false))
         return CCL_ERR_CUDA;
-    return from_cuda(launch_gemm<EPI_STORE, false, false>(p, pl.down, work + pl.partial, stream));
+    return from_cuda(launch_gemm<EPI_STORE, false, false>(p, pl.down, partial, stream));
 }
 
 ccl_status_t gated_ffn_grad_impl(const FfnArgs &a, const void *dy, void *dx, void *dwg, void *dwu, void *dwd,
@@ -940,12 +1276,13 @@ ccl_status_t gated_ffn_grad_impl(const FfnArgs &a, const void *dy, void *dx, voi
     }
     CCL_DBG_FFN(w, r, stream);
     char *work = static_cast<char *>(a.work);
-    Matrix x, wg, wu, wd, y;
-    if ((e = operand(a.x, a.t, a.d, pl.dp, work, pl.x, &x, stream)) || (e = operand(a.wg, a.f, a.d, pl.dp, work, pl.wg, &wg, stream)) ||
-        (e = operand(a.wu, a.f, a.d, pl.dp, work, pl.wu, &wu, stream)) || (e = operand(a.wd, a.d, a.f, pl.fp, work, pl.wd, &wd, stream)) ||
-        (e = operand(dy, a.t, a.d, pl.dp, work, pl.dy, &y, stream)))
+    Operands ops(work);
+    const Matrix x = ops.add(a.x, a.t, a.d, pl.x), y = ops.add(dy, a.t, a.d, pl.dy), wd = ops.add(a.wd, a.d, a.f, pl.wd);
+    const Matrix w2[2] = {ops.add(a.wg, a.f, a.d, pl.wg), ops.add(a.wu, a.f, a.d, pl.wu)};
+    const Matrix h{work + pl.h, a.t, a.f, pl.fp};
+    const Matrix d2[2] = {{work + pl.dg, a.t, a.f, pl.fp}, {work + pl.du, a.t, a.f, pl.fp}};
+    if ((e = ops.copy(stream)))
         return from_cuda(e);
-    const Matrix h{work + pl.h, a.t, a.f, pl.fp}, dg{work + pl.dg, a.t, a.f, pl.fp}, du{work + pl.du, a.t, a.f, pl.fp};
     GemmParams p{};
     p.act = (int)a.act;
     p.h = reinterpret_cast<uint16_t *>(work + pl.h);
@@ -954,35 +1291,51 @@ ccl_status_t gated_ffn_grad_impl(const FfnArgs &a, const void *dy, void *dx, voi
     p.g = a.saved;
     p.u = a.saved + a.t * a.f;
     p.ldh = (uint32_t)pl.fp;
-    if (!encode(&p.prob[0].a[0], y, false) || !encode(&p.prob[0].b[0], wd, true))
-        return CCL_ERR_CUDA;
-    if ((e = launch_gemm<EPI_BACKWARD, false, true>(p, pl.dh, work + pl.partial, stream)))
-        return from_cuda(e);
-    if (dx) {
-        p.prob[0].out = dx;
-        if (!encode(&p.prob[0].a[0], dg, false) || !encode(&p.prob[0].a[1], du, false) ||
-            !encode(&p.prob[0].b[0], wg, true) || !encode(&p.prob[0].b[1], wu, true))
+    char *partial = work + pl.partial;
+    p.vectors = a.f % 16 == 0 && (uintptr_t)a.saved % 32 == 0;
+    Problem &q = p.prob[0];
+    if (pl.dh.few) {
+        if (ccl_status_t st = launch_few<EPI_BACKWARD, true>(p, pl.dh, &wd, &y, partial, stream))
+            return st;
+    } else {
+        if (!encode(&q.a[0], y, false) || !encode(&q.b[0], wd, true))
             return CCL_ERR_CUDA;
-        if ((e = launch_gemm<EPI_STORE, false, true>(p, pl.dx, work + pl.partial, stream)))
+        if ((e = launch_gemm<EPI_BACKWARD, false, true>(p, pl.dh, partial, stream)))
             return from_cuda(e);
+    }
+    if (dx) {
+        q.out = dx;
+        p.vectors = a.d % 16 == 0 && (uintptr_t)dx % 32 == 0;
+        if (pl.dx.few) {
+            if (ccl_status_t st = launch_few<EPI_STORE, true>(p, pl.dx, w2, d2, partial, stream))
+                return st;
+        } else {
+            for (int i = 0; i < 2; ++i)
+                if (!encode(&q.a[i], d2[i], false) || !encode(&q.b[i], w2[i], true))
+                    return CCL_ERR_CUDA;
+            if ((e = launch_gemm<EPI_STORE, false, true>(p, pl.dx, partial, stream)))
+                return from_cuda(e);
+        }
     }
     if (!dwg && !dwu && !dwd)
         return CCL_OK;
     // the weight gradients asked for, in one launch
     p.accumulate = accumulate != 0;
+    p.vectors = a.d % 16 == 0 && a.f % 16 == 0;
     Launch l = pl.dw;
     l.n = 0;
-    const Matrix *am[3] = {&dg, &du, &y}, *bm[3] = {&x, &x, &h};
+    const Matrix *am[3] = {&d2[0], &d2[1], &y}, *bm[3] = {&x, &x, &h};
     void *out[3] = {dwg, dwu, dwd};
     for (int i = 0; i < 3; ++i)
         if (out[i]) {
             l.s[l.n] = pl.dw.s[i];
             p.prob[l.n].out = out[i];
+            p.vectors = p.vectors && (uintptr_t)out[i] % 32 == 0;
             if (!encode(&p.prob[l.n].a[0], *am[i], true) || !encode(&p.prob[l.n].b[0], *bm[i], true))
                 return CCL_ERR_CUDA;
             ++l.n;
         }
-    return from_cuda(launch_gemm<EPI_STORE, true, true>(p, l, work + pl.partial, stream));
+    return from_cuda(launch_gemm<EPI_STORE, true, true>(p, l, partial, stream));
 }
 
 } // namespace

@@ -59,6 +59,24 @@ template <int DT> __device__ __forceinline__ void st_value(void *base, uint64_t 
     }
 }
 
+// 32-byte vectors (32-byte aligned): a full memory sector per lane.
+__device__ __forceinline__ void ld32(const void *p, uint4 &a, uint4 &b)
+{
+    a = b = make_uint4(0, 0, 0, 0);
+    if (dbg_ok(p, 32))
+        asm volatile("ld.global.L1::no_allocate.v8.u32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                     : "l"(p));
+}
+
+__device__ __forceinline__ void st32(void *p, const uint4 &a, const uint4 &b)
+{
+    if (dbg_ok(p, 32))
+        asm volatile("st.global.L1::no_allocate.v8.u32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y),
+                     "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                     : "memory");
+}
+
 // ------------------------------------------------------------------ host side
 
 // Runs an entry point's body; an exception (the host vectors of the argument
