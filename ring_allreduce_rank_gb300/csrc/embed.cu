@@ -6,11 +6,12 @@
 // a few tokens.
 //
 // Gradient: dE[v] = round([dE[v] +] scale * sum over {t: id_t = v} of dY[t]),
-// the sum in fp32.  Three launches:
-//   1. embed_sort_kernel: the tokens' (row, position) pairs sorted by row,
-//      stably, by a radix sort that one cluster of eight CTAs runs (the
-//      digits' counts cross the cluster through distributed shared memory);
-//      meanwhile every other CTA writes the zero rows of the dense gradient.
+// the sum in fp32.  Launches, chained so that each starts under the one before:
+//   0. embed_zero_kernel (dense gradient): zeros to the rows that no token
+//      names, which need no sort to be found.
+//   1. embed_sort_kernel, beside it: the tokens' (row, position) pairs sorted
+//      by row, stably, by a radix sort that one cluster of eight CTAs runs (the
+//      digits' counts cross the cluster through distributed shared memory).
 //   2. embed_sum_kernel: the sorted tokens in pieces of 8 to 64, each summed in
 //      order; a row whose tokens lie in one piece is finished here, a row that
 //      crosses pieces leaves one fp32 partial sum per piece.
@@ -34,6 +35,7 @@ constexpr int kSortCtas = 8;       // one portable cluster
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigits = 256;       // bins of one radix pass
+constexpr int kZeroThreads = 256;
 constexpr int kMaxPiece = 64;      // sorted tokens summed by one warp, at most
 constexpr int kAhead = 8;          // rows' loads a warp has in flight
 constexpr int kSumThreads = 128;
@@ -110,10 +112,9 @@ struct SortParams {
     uint32_t rows;
     uint2 *buf[2]; // (row, position) pairs, written in turn by the passes
     int passes, bits;
-    char *grad; // zero rows are written here when fill != 0
+    char *grad; // the dense gradient, for its zero rows
     uint64_t pitch, row_bytes;
     int elem;
-    int fill;
 };
 
 __device__ __forceinline__ uint32_t row_key(const SortParams &p, uint64_t t)
@@ -142,47 +143,47 @@ __device__ __forceinline__ void warp_zero(char *q, uint64_t n, int elem, int lan
             gstore<uint32_t>(e + i, 0);
 }
 
+// A range of rows per CTA: the rows that tokens name marked from all the ids,
+// the others zeroed.
+__global__ void __launch_bounds__(kZeroThreads, 4) embed_zero_kernel(const __grid_constant__ SortParams p)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); // the sort does not wait for the zeros
+    constexpr uint32_t kBits = 65536;
+    __shared__ uint32_t mark[kBits / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t per = (p.rows + gridDim.x - 1) / gridDim.x;
+    const uint64_t end = umin64(p.rows, (uint64_t)(blockIdx.x + 1) * per);
+    for (uint64_t lo = (uint64_t)blockIdx.x * per; lo < end; lo += kBits) {
+        const uint32_t n = (uint32_t)umin64(kBits, end - lo);
+        for (uint32_t i = tid; i < (n + 31) / 32; i += kZeroThreads)
+            mark[i] = 0;
+        __syncthreads();
+        for (uint64_t t0 = tid; t0 < p.ntokens; t0 += 8 * kZeroThreads) {
+            uint32_t key[8]; // eight loads in flight
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                key[j] = t0 + j * kZeroThreads < p.ntokens ? row_key(p, t0 + j * kZeroThreads) : 0xffffffffu;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint64_t r = (uint64_t)key[j] - lo;
+                if (r < n)
+                    atomicOr(&mark[r >> 5], 1u << (r & 31));
+            }
+        }
+        __syncthreads();
+        for (uint32_t r = warp; r < n; r += kZeroThreads / 32)
+            if (!(mark[r >> 5] >> (r & 31) & 1))
+                warp_zero(p.grad + (lo + r) * p.pitch, p.row_bytes, p.elem, lane);
+        __syncthreads();
+    }
+}
+
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_constant__ SortParams p)
 {
     __shared__ uint32_t cnt[kSortWarps][kDigits];
     __shared__ uint32_t total[kDigits];
     __shared__ uint32_t wsum[kDigits / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-
-    if (blockIdx.x >= kSortCtas) {
-        // The rows of the dense gradient that no token names: this CTA's
-        // range of rows, marked from all the ids, the unmarked ones zeroed.
-        constexpr uint32_t kBits = kSortWarps * kDigits * 32;
-        uint32_t *mark = &cnt[0][0];
-        const uint32_t nf = gridDim.x - kSortCtas, f = blockIdx.x - kSortCtas;
-        const uint32_t per = (p.rows + nf - 1) / nf;
-        const uint64_t end = umin64(p.rows, (uint64_t)(f + 1) * per);
-        for (uint64_t lo = (uint64_t)f * per; lo < end; lo += kBits) {
-            const uint32_t n = (uint32_t)umin64(kBits, end - lo);
-            for (uint32_t i = tid; i < (n + 31) / 32; i += kSortThreads)
-                mark[i] = 0;
-            __syncthreads();
-            for (uint64_t t0 = tid; t0 < p.ntokens; t0 += 8 * kSortThreads) {
-                uint32_t key[8]; // eight loads in flight
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    key[j] = t0 + j * kSortThreads < p.ntokens ? row_key(p, t0 + j * kSortThreads) : 0xffffffffu;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint64_t r = (uint64_t)key[j] - lo;
-                    if (r < n)
-                        atomicOr(&mark[r >> 5], 1u << (r & 31));
-                }
-            }
-            __syncthreads();
-            for (uint32_t r = warp; r < n; r += kSortWarps)
-                if (!(mark[r >> 5] >> (r & 31) & 1))
-                    warp_zero(p.grad + (lo + r) * p.pitch, p.row_bytes, p.elem, lane);
-            __syncthreads();
-        }
-        return;
-    }
-
     cg::cluster_group cluster = cg::this_cluster();
     // each warp owns a contiguous run of positions, so that the order within
     // a bin is the order of the positions
@@ -209,6 +210,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
                 gstore<uint2>(p.buf[(p.passes - 1) & 1] + rank, make_uint2(row, (uint32_t)tid));
             }
         }
+        // the sums come after this kernel, and with it after the zeros
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         return; // the same for the whole cluster: no other CTA waits
     }
 
@@ -288,6 +291,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
         // leaves or reuses its totals while another may read them
         cluster.sync();
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ gradient: sums
@@ -658,27 +662,34 @@ ccl_status_t embedding_grad_impl(const void *grad_out, size_t grad_out_stride, c
     s.pitch = grad_table_stride * es;
     s.row_bytes = dim * es;
     s.elem = (int)es;
-    s.fill = !accumulate;
     cudaLaunchConfig_t cfg = {};
-    // one cluster sorts; the others, a CTA per SM, zero the rows without tokens
-    int sms = 0, dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return CCL_ERR_CUDA;
-    cfg.gridDim = dim3(s.fill ? kSortCtas + std::max(1, sms / kSortCtas) * kSortCtas : kSortCtas);
-    cfg.blockDim = dim3(kSortThreads);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    if (!accumulate) {
+        int sms = 0, dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return CCL_ERR_CUDA;
+        cfg.gridDim = dim3((unsigned)std::min<size_t>(rows, 4 * (size_t)sms)); // all resident
+        cfg.blockDim = dim3(kZeroThreads);
+        if (cudaError_t e = cudaLaunchKernelEx(&cfg, embed_zero_kernel, s))
+            return from_cuda(e);
+        count_launches(1);
+        if (ntokens == 0)
+            return CCL_OK;
+    }
+    cfg.gridDim = dim3(kSortCtas);
+    cfg.blockDim = dim3(kSortThreads);
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = kSortCtas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = accumulate ? 1 : 2; // beside the zeros, when there are any
     if (cudaError_t e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, s))
         return from_cuda(e);
     count_launches(1);
-    if (ntokens == 0)
-        return CCL_OK;
     SumParams p{};
     p.sorted = s.buf[(s.passes - 1) & 1];
     p.ntokens = ntokens;

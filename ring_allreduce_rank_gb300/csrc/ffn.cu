@@ -308,10 +308,28 @@ __device__ __forceinline__ void activation(int act, float g, float &a, float &da
 
 // ------------------------------------------------------------------ epilogues
 
+// What the epilogue reads of one column: the saved g and u, or the old value.
+template <int EPI> struct Ahead1 {
+    float g, u;
+    __device__ __forceinline__ void load(const GemmParams &p, const Problem &q, uint32_t row, uint32_t col)
+    {
+        const uint64_t at = (uint64_t)row * q.n + col;
+        if (EPI == EPI_BACKWARD && row < q.m && col < q.n) {
+            g = gload<float>(p.g + at);
+            u = gload<float>(p.u + at);
+        }
+        if (EPI == EPI_STORE && p.accumulate && row < q.m && col < q.n)
+            g = ld_value<DT_BF16>(q.out, at);
+    }
+};
+
 // One finished sum: v, and for EPI_GATED g = v and u = w.
 template <int EPI>
-__device__ __forceinline__ void finish1(const GemmParams &p, const Problem &q, uint32_t row, uint32_t col, float v, float w)
+__device__ __forceinline__ void finish1(const GemmParams &p, const Problem &q, uint32_t row, uint32_t col,
+                                        const Ahead1<EPI> &ahead, float v, float w)
 {
+    if (row >= q.m || col >= q.n)
+        return;
     const uint64_t at = (uint64_t)row * q.n + col, ath = (uint64_t)row * p.ldh + col;
     float a, da;
     if (EPI == EPI_GATED) {
@@ -322,13 +340,12 @@ __device__ __forceinline__ void finish1(const GemmParams &p, const Problem &q, u
         activation(p.act, v, a, da);
         st_value<DT_BF16>(p.h, ath, a * w);
     } else if (EPI == EPI_BACKWARD) {
-        const float g = gload<float>(p.g + at), u = gload<float>(p.u + at);
-        activation(p.act, g, a, da);
-        st_value<DT_BF16>(p.h, ath, a * u);
-        st_value<DT_BF16>(p.dg, ath, v * u * da);
+        activation(p.act, ahead.g, a, da);
+        st_value<DT_BF16>(p.h, ath, a * ahead.u);
+        st_value<DT_BF16>(p.dg, ath, v * ahead.u * da);
         st_value<DT_BF16>(p.du, ath, v * a);
     } else {
-        st_value<DT_BF16>(q.out, at, p.accumulate ? __fadd_rn(ld_value<DT_BF16>(q.out, at), v) : v);
+        st_value<DT_BF16>(q.out, at, p.accumulate ? __fadd_rn(ahead.g, v) : v);
     }
 }
 
@@ -608,11 +625,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
                         turn[lane * 33 + j] = v[j];
                     __syncwarp();
                     const uint32_t cc = lane % kWide, col = col0 + c + cc;
-#pragma unroll 8
-                    for (uint32_t r = lane / kWide; r < 32; r += kRows) {
-                        const float *from = turn + r * 33 + cc;
-                        if (row0 + r < q.m && col < q.n)
-                            finish1<EPI>(p, q, row0 + r, col, from[0], EPI == EPI_GATED ? from[16] : 0.0f);
+                    for (uint32_t r0 = lane / kWide; r0 < 32; r0 += 8 * kRows) { // eight rows' reads in flight
+                        Ahead1<EPI> old[8];
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            old[r].load(p, q, row0 + r0 + r * kRows, col);
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            const float *from = turn + (r0 + r * kRows) * 33 + cc;
+                            finish1<EPI>(p, q, row0 + r0 + r * kRows, col, old[r], from[0], EPI == EPI_GATED ? from[16] : 0.0f);
+                        }
                     }
                     __syncwarp();
                 }
@@ -759,6 +781,11 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
                 tc_load16(acc + (EPI == EPI_GATED ? 0 : half * fp.npad) + c, v);
                 if (EPI == EPI_GATED)
                     tc_load16(acc + fp.npad + c, w);
+                Ahead1<EPI> old[16];
+                if (p.splits == 1)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        old[j].load(p, q, c + j, col);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     if (c + j >= q.m)
@@ -768,8 +795,8 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
                         gstore<float>(out + (EPI == EPI_GATED ? 0 : half * 128), v[j]);
                         if (EPI == EPI_GATED)
                             gstore<float>(out + 128, w[j]);
-                    } else if (col < q.n) {
-                        finish1<EPI>(p, q, c + j, col, v[j], EPI == EPI_GATED ? w[j] : 0.0f);
+                    } else {
+                        finish1<EPI>(p, q, c + j, col, old[j], v[j], EPI == EPI_GATED ? w[j] : 0.0f);
                     }
                 }
             }
@@ -807,6 +834,8 @@ template <int EPI> __global__ void __launch_bounds__(256) ffn_join_kernel(const 
             // EPI_GATED: 128 columns of g, then the same of u, in each tile
             const float *at = q.partial + row * width + (EPI == EPI_GATED ? col / 128 * 256 + col % 128 : col);
             float v = 0.0f, w = 0.0f, f[4], h[4];
+            Ahead1<EPI> old;
+            old.load(p, q, row, col);
             for (uint32_t s0 = 0; s0 < p.splits; s0 += 4) { // four loads in flight
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
@@ -823,7 +852,7 @@ template <int EPI> __global__ void __launch_bounds__(256) ffn_join_kernel(const 
                             w = __fadd_rn(w, h[s]);
                     }
             }
-            finish1<EPI>(p, q, row, col, v, w);
+            finish1<EPI>(p, q, row, col, old, v, w);
         }
     }
 }
@@ -849,9 +878,24 @@ __global__ void __launch_bounds__(256) ffn_pack_kernel(const __grid_constant__ P
         const auto &m = p.m[k];
         const uint32_t per = m.ld / 8;
         for (uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x; e < m.vectors; e += (uint64_t)gridDim.x * 256) {
-            const uint64_t r = e / per;
-            const uint32_t c = (uint32_t)(e % per) * 8;
+            const uint64_t r = m.vectors >> 32 ? e / per : (uint32_t)e / per;
+            const uint32_t c = (uint32_t)(e - r * per) * 8;
             const uint16_t *src = m.src + r * m.cols + c;
+            if (c && c + 9 <= m.cols) {
+                // inside a row: the words around the eight values
+                const uint32_t odd = (uintptr_t)src & 2;
+                const uint16_t *word = src - odd / 2;
+                uint32_t x[5];
+#pragma unroll
+                for (int i = 0; i < 5; ++i)
+                    x[i] = i < 4 || odd ? gload<uint32_t>(word + 2 * i) : 0;
+                uint32_t o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[i] = __funnelshift_r(x[i], x[i + 1], odd * 8);
+                st16(m.dst + e * 8, make_uint4(o[0], o[1], o[2], o[3]));
+                continue;
+            }
             uint32_t h[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -902,21 +946,24 @@ constexpr int kPairs = 76, kSms = 152; // CTA pairs and SMs of the GPU
 constexpr uint32_t kMaxSplits = 16;
 
 // How many parts the sum over K is cut into: the number that minimises the
-// rounds of CTA pairs (CTAs, for few tokens) times a part's length, plus the
-// join's.  A block of K takes a pair about 0.35 us of products; a CTA with few
-// tokens reads its 32 KiB of weights in 0.4 us alone, and at the memory's rate
-// with the others; a unit's fill and epilogue take about 3 us and 1.5 us, a
-// join about 3 and its bytes at 6 TB/s.  Without it a product of few tiles
-// (few tokens, narrow layers) would leave most SMs idle.
-uint32_t choose_splits(uint64_t tiles, uint64_t kblocks, uint64_t partial_bytes, bool few)
+// rounds of CTA pairs (CTAs, for few tokens), each as long as the longer of a
+// part's products and a unit's epilogue, which overlap, plus the join.  A block
+// of K takes a pair about 0.35 us; a CTA with few tokens reads its 32 KiB of
+// weights in 0.5 us alone, and at the memory's rate with the others.  An
+// epilogue takes a pair about 3 us, or 15 us on rows that no 32-byte vector
+// divides, and a CTA with few tokens 0.5 us; a join about 3 us and its bytes
+// at 6 TB/s.  Without it a product of few tiles (few tokens, narrow layers)
+// would leave most SMs idle.
+uint32_t choose_splits(uint64_t tiles, uint64_t kblocks, uint64_t partial_bytes, bool few, bool odd)
 {
     uint32_t best = 1;
     double cost = 0;
     const uint64_t slots = few ? kSms : kPairs;
     for (uint32_t s = 1; s <= kMaxSplits && s <= kblocks; ++s) {
         const double rounds = (double)((tiles * s + slots - 1) / slots);
-        const double block = few ? std::max(0.4, 0.005 * (double)std::min(slots, tiles * s)) : 0.35;
-        const double c = rounds * ((double)((kblocks + s - 1) / s) * block + (few ? 1.5 : 3.0)) +
+        const double block = few ? std::max(0.5, 0.005 * (double)std::min(slots, tiles * s)) : 0.35;
+        const double products = (double)kblocks / s * block, epilogue = few ? 0.5 : odd && s == 1 ? 15.0 : 3.0;
+        const double c = rounds * std::max(products, epilogue) + std::min(products, epilogue) +
                          (s > 1 ? 3.0 + 2.0 * s * (double)partial_bytes / 6e6 : 0.0);
         if (s == 1 || c < cost * 0.97) {
             best = s;
@@ -934,7 +981,7 @@ struct Shape {
 struct Launch {
     Shape s[kMaxProblems];
     int n;
-    bool gated, few; // few: by ffn_few_kernel
+    bool gated, few, odd; // few: by ffn_few_kernel; odd: the epilogue's rows are no 32-byte vectors
     uint32_t splits;
     size_t partial; // bytes of all splits
     void plan()
@@ -946,7 +993,7 @@ struct Launch {
             kb = std::max<uint64_t>(kb, (uint64_t)tiles_of(s[i].k, kTileK) * s[i].segs);
             bytes += up(s[i].m * (size_t)tiles_of(s[i].n, gated ? 128 : kTileN) * kTileN * 4);
         }
-        splits = choose_splits(tiles, kb, bytes, few);
+        splits = choose_splits(tiles, kb, bytes, few, odd);
         partial = splits > 1 ? bytes * splits : 0;
     }
 };
@@ -970,12 +1017,13 @@ bool make_plan(size_t t, size_t d, size_t f, bool backward, bool aligned, FfnPla
     p->f = f;
     p->dp = (d + 7) / 8 * 8;
     p->fp = (f + 15) / 16 * 16; // h, dg and du in rows of whole 32-byte vectors
-    const bool pd = p->dp != d || !aligned, pf = f % 8 || !aligned, few = t <= kFewTokens;
-    p->up_ = Launch{{{t, f, d, 1}}, 1, true, few, 1, 0};
-    p->down = Launch{{{t, d, f, 1}}, 1, false, few, 1, 0};
-    p->dh = Launch{{{t, f, d, 1}}, 1, false, few, 1, 0};
-    p->dx = Launch{{{t, d, f, 2}}, 1, false, few, 1, 0};
-    p->dw = Launch{{{f, d, t, 1}, {f, d, t, 1}, {d, f, t, 1}}, 3, false, false, 1, 0};
+    const bool pd = p->dp != d || !aligned, pf = f % 8 || !aligned, few = t <= kFewTokens,
+               od = d % 16 != 0, of = f % 16 != 0;
+    p->up_ = Launch{{{t, f, d, 1}}, 1, true, few, of, 1, 0};
+    p->down = Launch{{{t, d, f, 1}}, 1, false, few, od, 1, 0};
+    p->dh = Launch{{{t, f, d, 1}}, 1, false, few, of, 1, 0};
+    p->dx = Launch{{{t, d, f, 2}}, 1, false, few, od, 1, 0};
+    p->dw = Launch{{{f, d, t, 1}, {f, d, t, 1}, {d, f, t, 1}}, 3, false, false, od || of, 1, 0};
     size_t at = 0, partial = 0;
     auto take = [&](size_t n) {
         const size_t o = at;
@@ -998,7 +1046,8 @@ bool make_plan(size_t t, size_t d, size_t f, bool backward, bool aligned, FfnPla
         p->wd = take(d * p->fp * 2);
     for (Launch *l : {&p->up_, &p->down, &p->dh, &p->dx, &p->dw}) {
         l->plan();
-        partial = std::max(partial, l->partial);
+        if (backward == (l != &p->up_ && l != &p->down))
+            partial = std::max(partial, l->partial);
     }
     p->partial = take(partial);
     p->bytes = at;
