@@ -492,7 +492,8 @@ ccl_status_t ccl_gated_ffn_grad(const void *grad_out, const void *x, const void 
 /* Bytes of the work buffer.  aligned != 0: every input matrix is 16-byte
  * aligned (else, or where a width is no multiple of 8, room for padded copies
  * of the inputs is included: the copy engine that feeds the tensor cores
- * addresses whole 16-byte vectors). */
+ * addresses whole 16-byte vectors).  backward != 0: for ccl_gated_ffn_grad, and
+ * enough for ccl_gated_ffn of the same sizes. */
 ccl_status_t ccl_plan_gated_ffn_work_bytes(size_t ntokens, size_t dim, size_t ffn, int backward, int aligned, size_t *bytes);
 
 /* How often a gated feed-forward kernel on the current device gave up waiting

@@ -119,21 +119,24 @@ template <int DT> __device__ __forceinline__ void unpack2(const uint4 &v, float2
                              : make_float2(__uint_as_float(w[i & 3] << 16), __uint_as_float(w[i & 3] & 0xffff0000u));
 }
 
-// The largest value of kVecs vectors; a NaN does not count (it reaches the sum).
-template <int DT> __device__ __forceinline__ float max_of(const uint4 *x)
+// The largest value of the first n of kVecs vectors; a NaN does not count (it reaches the sum).
+template <int DT> __device__ __forceinline__ float max_of(const uint4 *x, int n)
 {
     if (DT == DT_FP32) {
         float m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i)
-            m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(x[i].x), __uint_as_float(x[i].y)),
-                               fmaxf(__uint_as_float(x[i].z), __uint_as_float(x[i].w))));
+            if (i < n)
+                m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(x[i].x), __uint_as_float(x[i].y)),
+                                   fmaxf(__uint_as_float(x[i].z), __uint_as_float(x[i].w))));
         return m;
     }
     uint32_t m = 0xff80ff80u; // -inf twice
     auto up = [&](uint32_t w) { asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w)); };
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
+        if (i >= n)
+            break;
         up(x[i].x);
         up(x[i].y);
         up(x[i].z);
@@ -246,6 +249,9 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
         for (int i = 0; i < kVecs; ++i)
             x[i] = held[(i0 + i) * kDThreads + tid];
     };
+    // vectors a thread has to work on (some threads one less): registers
+    // first, then shared memory, then what does not fit
+    const int mine_n = (int)((v1 - v0 + kDThreads - 1) / kDThreads);
     // the teacher's entries are worked on by as many warps as there are
     // entries for; the loss is CTA 0's.  Their loads go out before the row's,
     // which would delay them.
@@ -262,13 +268,15 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
     if (!skip) {
 #pragma unroll
         for (int i = 0; i < kHeld; ++i)
-            if (v0 + tid + i * kDThreads < v1)
-                copy16_async(&held[i * kDThreads + tid], body + (uint64_t)(v0 + tid) * 16 + i * kDThreads * 16);
-            else
-                held[i * kDThreads + tid] = ninf;
+            if (kHeld + i < mine_n) {
+                if (v0 + tid + (kHeld + i) * kDThreads < v1)
+                    copy16_async(&held[i * kDThreads + tid], body + (uint64_t)(v0 + tid) * 16 + (kHeld + i) * kDThreads * 16);
+                else
+                    held[i * kDThreads + tid] = ninf;
+            }
 #pragma unroll
         for (int i = 0; i < kHeld; i += kVecs)
-            load(x + i, v0 + tid + (kHeld + i) * kDThreads);
+            load(x + i, v0 + tid + i * kDThreads);
         if (edge)
             xe = ld_value<DT>(row, ei);
     }
@@ -333,14 +341,13 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
         if (tid == 0)
             present = tm > -INFINITY;
     }
-    copies_wait();
-
     Stat st{-INFINITY, 0.0f};
     const float2 scale2 = make_float2(p.scale, p.scale);
     uint4 y[kVecs];
     if (MODE == DISTILL_GRAD) {
         st.m = gload<float>(p.stats + 2 * t);
         st.z = gload<float>(p.stats + 2 * t + 1);
+        copies_wait();
         if (tid < top && tid < step)
             logit[tid] = first_student;
         __syncthreads();
@@ -348,8 +355,8 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
         // (m, Z): this thread's vectors, then warp, CTA and cluster
         if (!skip) {
             float2 z = make_float2(0.0f, 0.0f);
-            auto fold = [&](const uint4 *x) {
-                const float bm = max_of<DT>(x);
+            auto fold = [&](const uint4 *x, int n) { // the first n of kVecs vectors
+                const float bm = max_of<DT>(x, n);
                 if (bm > st.m) { // the sum so far, relative to the new maximum
                     const float r = row_exp(st.m, bm, p.scale);
                     z = mul2(z, make_float2(r, r));
@@ -358,6 +365,8 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
                 if (st.m == -INFINITY) { // nothing yet but -inf, and perhaps a NaN
 #pragma unroll
                     for (int i = 0; i < kVecs; ++i) {
+                        if (i >= n)
+                            break;
                         float f[VEC];
                         unpack<DT>(x[i], f);
 #pragma unroll
@@ -369,6 +378,8 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
                 const float2 neg = make_float2(-st.m, -st.m);
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
+                    if (i >= n)
+                        break;
                     float2 f[VEC / 2];
                     unpack2<DT>(x[i], f);
 #pragma unroll
@@ -382,18 +393,20 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
                     z = add2(z, f[0]);
                 }
             };
-#pragma unroll 1
-            for (int i = 0; i < kHeld; i += kVecs) {
-                from_held(y, i);
-                fold(y);
-            }
 #pragma unroll
             for (int i = 0; i < kHeld; i += kVecs)
-                fold(x + i);
+                if (i < mine_n)
+                    fold(x + i, mine_n - i);
+            copies_wait();
+#pragma unroll 1
+            for (int i = 0; i < kHeld && kHeld + i < mine_n; i += kVecs) {
+                from_held(y, i);
+                fold(y, mine_n - kHeld - i);
+            }
 #pragma unroll 1
             for (uint32_t b = v0 + kPart; b < v1; b += kVecs * kDThreads) {
                 load(y, b + tid);
-                fold(y);
+                fold(y, kVecs);
             }
             st.z = __fadd_rn(z.x, z.y);
             if (edge)
@@ -442,10 +455,12 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
         const float2 c2 = make_float2(c, c), neg = make_float2(-st.m, -st.m);
         const bool vec_store = (((uintptr_t)grow ^ (uintptr_t)row) & 15) == 0;
         char *gbody = grow + (uint64_t)nh * ES;
-        auto emit = [&](const uint4 *x, uint32_t b) {
+        auto emit = [&](const uint4 *x, uint32_t b, int n) {
             char *q = gbody + (uint64_t)b * 16;
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
+                if (i >= n)
+                    break;
                 uint4 o = make_uint4(0, 0, 0, 0);
                 float2 f[VEC / 2];
                 if (!zero) {
@@ -470,17 +485,18 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
         };
 #pragma unroll
         for (int i = 0; i < kHeld; i += kVecs)
-            emit(x + i, v0 + tid + (kHeld + i) * kDThreads);
+            if (i < mine_n)
+                emit(x + i, v0 + tid + i * kDThreads, mine_n - i);
 #pragma unroll 1
-        for (int i = 0; i < kHeld; i += kVecs) {
+        for (int i = 0; i < kHeld && kHeld + i < mine_n; i += kVecs) {
             from_held(y, i);
-            emit(y, v0 + tid + i * kDThreads);
+            emit(y, v0 + tid + (kHeld + i) * kDThreads, mine_n - kHeld - i);
         }
 #pragma unroll 1
         for (uint32_t b = v0 + kPart; b < v1; b += kVecs * kDThreads) {
             if (!skip)
                 load(y, b + tid);
-            emit(y, b + tid);
+            emit(y, b + tid, kVecs);
         }
         if (edge)
             st_value<DT>(grow, ei, zero ? 0.0f : __fmul_rn(row_exp(xe, st.m, p.scale), c));

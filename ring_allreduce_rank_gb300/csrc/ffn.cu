@@ -73,7 +73,8 @@ struct GemmParams {
     uint16_t *h, *dg, *du;
     float *g, *u;
     uint32_t ldh; // row stride of h, dg and du (g and u: n)
-    int vectors;  // every row that the epilogue touches is 32-byte aligned and whole 16-column vectors
+    int vectors;  // every row that the epilogue touches is 16-byte aligned (fp32: 32) and whole vectors of 8 columns
+    int early;    // the weights may be read before the kernel before this one has ended
 };
 
 // ffn_few_kernel's: the same products with the weights as rows.
@@ -160,6 +161,11 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
             }
         }
     }
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 // A 2-D box of a tensor map into this CTA's shared memory; its bytes are
@@ -311,26 +317,23 @@ __device__ __forceinline__ void activation(int act, float g, float &a, float &da
 // What the epilogue reads of one column: the saved g and u, or the old value.
 template <int EPI> struct Ahead1 {
     float g, u;
-    __device__ __forceinline__ void load(const GemmParams &p, const Problem &q, uint32_t row, uint32_t col)
+    __device__ __forceinline__ void load(const GemmParams &p, const Problem &q, uint64_t at, bool in)
     {
-        const uint64_t at = (uint64_t)row * q.n + col;
-        if (EPI == EPI_BACKWARD && row < q.m && col < q.n) {
+        if (EPI == EPI_BACKWARD && in) {
             g = gload<float>(p.g + at);
             u = gload<float>(p.u + at);
         }
-        if (EPI == EPI_STORE && p.accumulate && row < q.m && col < q.n)
+        if (EPI == EPI_STORE && p.accumulate && in)
             g = ld_value<DT_BF16>(q.out, at);
     }
 };
 
-// One finished sum: v, and for EPI_GATED g = v and u = w.
+// One finished sum: v, and for EPI_GATED g = v and u = w; at: its place in
+// rows of n columns, ath: in rows of ldh.
 template <int EPI>
-__device__ __forceinline__ void finish1(const GemmParams &p, const Problem &q, uint32_t row, uint32_t col,
+__device__ __forceinline__ void finish1(const GemmParams &p, const Problem &q, uint64_t at, uint64_t ath,
                                         const Ahead1<EPI> &ahead, float v, float w)
 {
-    if (row >= q.m || col >= q.n)
-        return;
-    const uint64_t at = (uint64_t)row * q.n + col, ath = (uint64_t)row * p.ldh + col;
     float a, da;
     if (EPI == EPI_GATED) {
         if (p.g) {
@@ -349,13 +352,21 @@ __device__ __forceinline__ void finish1(const GemmParams &p, const Problem &q, u
     }
 }
 
-// Sixteen fp32 values of one row as 32-byte vectors.
+// Sixteen values of one row, eight at a time: `both` says whether the second
+// eight are columns of the matrix.
 struct Vals16 {
     uint4 v[4];
-    __device__ __forceinline__ void load(const float *q)
+    __device__ __forceinline__ void load(const float *q, bool both)
     {
         ld32(q, v[0], v[1]);
-        ld32(q + 8, v[2], v[3]);
+        if (both)
+            ld32(q + 8, v[2], v[3]);
+    }
+    __device__ __forceinline__ void load(const uint16_t *q, bool both)
+    {
+        v[0] = ld16(q);
+        if (both)
+            v[1] = ld16(q + 8);
     }
     __device__ __forceinline__ void get(float *f) const
     {
@@ -365,25 +376,38 @@ struct Vals16 {
     }
 };
 
-__device__ __forceinline__ void store16(float *q, const float *f)
+__device__ __forceinline__ void store16(float *q, const float *f, bool both)
 {
     st32(q, pack<DT_FP32>(f), pack<DT_FP32>(f + 4));
-    st32(q + 8, pack<DT_FP32>(f + 8), pack<DT_FP32>(f + 12));
+    if (both)
+        st32(q + 8, pack<DT_FP32>(f + 8), pack<DT_FP32>(f + 12));
 }
 
-__device__ __forceinline__ void store16(uint16_t *q, const float *f) { st32(q, pack<DT_BF16>(f), pack<DT_BF16>(f + 8)); }
+__device__ __forceinline__ void store16(uint16_t *q, const float *f, bool both)
+{
+    if (both && ((uintptr_t)q & 31) == 0) {
+        st32(q, pack<DT_BF16>(f), pack<DT_BF16>(f + 8));
+    } else {
+        st16(q, pack<DT_BF16>(f));
+        if (both)
+            st16(q + 8, pack<DT_BF16>(f + 8));
+    }
+}
 
 // What the epilogue reads of sixteen columns, asked for before it is needed.
 template <int EPI> struct Ahead16 {
     Vals16 g, u;
     __device__ __forceinline__ void load(const GemmParams &p, const Problem &q, uint32_t row, uint32_t col)
     {
-        if (EPI == EPI_BACKWARD && row < q.m && col < q.n) {
-            g.load(p.g + (uint64_t)row * q.n + col);
-            u.load(p.u + (uint64_t)row * q.n + col);
+        if (row >= q.m || col >= q.n)
+            return;
+        const uint64_t at = (uint64_t)row * q.n + col;
+        if (EPI == EPI_BACKWARD) {
+            g.load(p.g + at, col + 8 < q.n);
+            u.load(p.u + at, col + 8 < q.n);
         }
-        if (EPI == EPI_STORE && p.accumulate && row < q.m && col < q.n)
-            ld32(static_cast<const uint16_t *>(q.out) + (uint64_t)row * q.n + col, g.v[0], g.v[1]);
+        if (EPI == EPI_STORE && p.accumulate)
+            g.load(static_cast<const uint16_t *>(q.out) + at, col + 8 < q.n);
     }
 };
 
@@ -394,18 +418,20 @@ __device__ __forceinline__ void finish16(const GemmParams &p, const Problem &q, 
 {
     if (row >= q.m || col >= q.n)
         return;
+    const bool both = col + 8 < q.n;
+    const uint64_t at = (uint64_t)row * q.n + col, ath = (uint64_t)row * p.ldh + col;
     float a[16], da;
     if (EPI == EPI_GATED) {
         if (p.g) {
-            store16(p.g + (uint64_t)row * q.n + col, v);
-            store16(p.u + (uint64_t)row * q.n + col, w);
+            store16(p.g + at, v, both);
+            store16(p.u + at, w, both);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             activation(p.act, v[i], a[i], da);
             a[i] *= w[i];
         }
-        store16(p.h + (uint64_t)row * p.ldh + col, a);
+        store16(p.h + ath, a, both);
     } else if (EPI == EPI_BACKWARD) {
         float g[16], u[16];
         ahead.g.get(g);
@@ -417,9 +443,9 @@ __device__ __forceinline__ void finish16(const GemmParams &p, const Problem &q, 
             v[i] = v[i] * a[i];      // du
             a[i] = a[i] * u[i];      // h
         }
-        store16(p.h + (uint64_t)row * p.ldh + col, a);
-        store16(p.dg + (uint64_t)row * p.ldh + col, g);
-        store16(p.du + (uint64_t)row * p.ldh + col, v);
+        store16(p.h + ath, a, both);
+        store16(p.dg + ath, g, both);
+        store16(p.du + ath, v, both);
     } else {
         if (p.accumulate) {
             unpack<DT_BF16>(ahead.g.v[0], a);
@@ -428,7 +454,7 @@ __device__ __forceinline__ void finish16(const GemmParams &p, const Problem &q, 
             for (int i = 0; i < 16; ++i)
                 v[i] = __fadd_rn(a[i], v[i]);
         }
-        store16(static_cast<uint16_t *>(q.out) + (uint64_t)row * q.n + col, v);
+        store16(static_cast<uint16_t *>(q.out) + at, v, both);
     }
 }
 
@@ -467,7 +493,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
     const uint32_t stages = (smem_u32(raw) + 1023) & ~1023u;
     const uint32_t full = smem_u32(&bars[0]), empty = smem_u32(&bars[kStages]);
     const uint32_t acc_full = smem_u32(&bars[2 * kStages]), acc_empty = smem_u32(&bars[2 * kStages + 2]);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
@@ -482,6 +508,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
         }
         gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 3 && lane / 4 < p.nprob) {
+        const Problem &q = p.prob[lane / 4];
+        const int i = lane & 1;
+        if (lane & 2 ? i < (EPI == EPI_GATED ? 2 : q.segs) : i < q.segs)
+            prefetch_map(lane & 2 ? &q.b[i] : &q.a[i]);
     }
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot)) : "memory");
@@ -594,7 +626,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
                     float v[16];
                     tc_load16(acc + c, v);
                     if (row < q.m)
-                        store16(out + c, v);
+                        store16(out + c, v, true);
                 }
             } else if (p.vectors) {
 #pragma unroll 2
@@ -627,13 +659,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
                     const uint32_t cc = lane % kWide, col = col0 + c + cc;
                     for (uint32_t r0 = lane / kWide; r0 < 32; r0 += 8 * kRows) { // eight rows' reads in flight
                         Ahead1<EPI> old[8];
+                        const uint64_t at = (uint64_t)(row0 + r0) * q.n + col, ath = (uint64_t)(row0 + r0) * p.ldh + col;
+                        const uint32_t step = kRows * q.n, steph = kRows * p.ldh;
+                        const uint32_t rows = col >= q.n || row0 + r0 >= q.m ? 0 : (q.m - row0 - r0 + kRows - 1) / kRows;
 #pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            old[r].load(p, q, row0 + r0 + r * kRows, col);
+                        for (uint32_t r = 0; r < 8; ++r)
+                            old[r].load(p, q, at + (uint64_t)r * step, r < rows);
 #pragma unroll
-                        for (int r = 0; r < 8; ++r) {
+                        for (uint32_t r = 0; r < 8; ++r) {
                             const float *from = turn + (r0 + r * kRows) * 33 + cc;
-                            finish1<EPI>(p, q, row0 + r0 + r * kRows, col, old[r], from[0], EPI == EPI_GATED ? from[16] : 0.0f);
+                            if (r < rows)
+                                finish1<EPI>(p, q, at + (uint64_t)r * step, ath + (uint64_t)r * steph, old[r], from[0],
+                                             EPI == EPI_GATED ? from[16] : 0.0f);
                         }
                     }
                     __syncwarp();
@@ -676,7 +713,7 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t stage_bytes = 2 * kOperandBytes + fp.npad * 128;
     const uint32_t full = smem_u32(&bars[0]), empty = smem_u32(&bars[kMaxStages]);
     const uint32_t acc_full = smem_u32(&bars[2 * kMaxStages]), acc_empty = smem_u32(&bars[2 * kMaxStages + 2]);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
@@ -690,6 +727,10 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
         gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (warp == 3 && lane < (EPI == EPI_GATED ? 2 : q.segs))
+        prefetch_map(&q.a[lane]);
+    else if (warp == 3 && lane >= 16 && lane - 16 < q.segs)
+        prefetch_map(&q.b[lane - 16]);
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -698,11 +739,34 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = tmem_slot;
-    chain_entry();
+    if (!p.early)
+        chain_entry();
 
     if (warp == 0 && lane == 0) {
         uint32_t s = 0, phase = 0;
         bool ok = true;
+        // a: the weights (EPI_GATED: Wg and Wu; else one per segment); b: the tokens
+        auto load_a = [&](const Unit &u, uint32_t kb, uint32_t stage) {
+            mbar_expect(full + 8 * stage, stage_bytes);
+            const uint32_t seg = kb >= q.kblocks ? 1 : 0, at = stages + stage * stage_bytes;
+            const int k = (int)((kb - seg * q.kblocks) * kTileK);
+            const int r0 = EPI == EPI_GATED ? (int)(u.n * 128) : (int)(u.n * 256);
+            load_weights<A_MN>(at, EPI == EPI_GATED ? &q.a[0] : &q.a[seg], r0, k, full + 8 * stage);
+            load_weights<A_MN>(at + kOperandBytes, EPI == EPI_GATED ? &q.a[1] : &q.a[seg], EPI == EPI_GATED ? r0 : r0 + 128, k, full + 8 * stage);
+        };
+        auto load_b = [&](uint32_t kb, uint32_t stage) {
+            const uint32_t seg = kb >= q.kblocks ? 1 : 0;
+            tma_load_own(stages + stage * stage_bytes + 2 * kOperandBytes, &q.b[seg], (int)((kb - seg * q.kblocks) * kTileK), 0, full + 8 * stage);
+        };
+        // the first stages' weights before the tokens' values are ready
+        uint32_t ahead = 0;
+        if (p.early) {
+            const Unit u = unit_at(p, blockIdx.x);
+            ahead = min(fp.stages, u.kb1 - u.kb0);
+            for (uint32_t i = 0; i < ahead; ++i)
+                load_a(u, u.kb0 + i, i);
+            chain_entry();
+        }
         auto next = [&] {
             if (++s == fp.stages) {
                 s = 0;
@@ -712,17 +776,14 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
         for (uint32_t i = blockIdx.x; ok && i < q.units; i += gridDim.x) {
             const Unit u = unit_at(p, i);
             for (uint32_t kb = u.kb0; kb < u.kb1; ++kb) {
-                if (!(ok = mbar_wait(empty + 8 * s, phase ^ 1, &gave_up)))
-                    break;
-                mbar_expect(full + 8 * s, stage_bytes);
-                const uint32_t seg = kb >= q.kblocks ? 1 : 0;
-                const int k = (int)((kb - seg * q.kblocks) * kTileK);
-                const uint32_t at = stages + s * stage_bytes;
-                // a: the weights (EPI_GATED: Wg and Wu; else one per segment); b: the tokens
-                const int r0 = EPI == EPI_GATED ? (int)(u.n * 128) : (int)(u.n * 256);
-                load_weights<A_MN>(at, EPI == EPI_GATED ? &q.a[0] : &q.a[seg], r0, k, full + 8 * s);
-                load_weights<A_MN>(at + kOperandBytes, EPI == EPI_GATED ? &q.a[1] : &q.a[seg], EPI == EPI_GATED ? r0 : r0 + 128, k, full + 8 * s);
-                tma_load_own(at + 2 * kOperandBytes, &q.b[seg], k, 0, full + 8 * s);
+                if (ahead) {
+                    --ahead; // the ring's first round: this stage is free and its weights are on the way
+                } else {
+                    if (!(ok = mbar_wait(empty + 8 * s, phase ^ 1, &gave_up)))
+                        break;
+                    load_a(u, kb, s);
+                }
+                load_b(kb, s);
                 next();
             }
         }
@@ -762,6 +823,8 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
                 tc_commit_own(acc_full + 8 * buf);
         }
     } else if (warp >= 4) {
+        if (p.early)
+            chain_entry();
         // a lane is a weight row, so that a warp's accesses run along a token's
         // row.  EPI_GATED: the two halves of the warps take the tokens in turn,
         // else one block of rows each.
@@ -781,23 +844,26 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
                 tc_load16(acc + (EPI == EPI_GATED ? 0 : half * fp.npad) + c, v);
                 if (EPI == EPI_GATED)
                     tc_load16(acc + fp.npad + c, w);
-                Ahead1<EPI> old[16];
-                if (p.splits == 1)
+                const uint32_t rows = min(16u, q.m - min(q.m, c)); // tokens of these columns
+                if (p.splits > 1) {
+                    float *out = q.partial + ((uint64_t)u.split * q.m + c) * width + u.n * kTileN + (EPI == EPI_GATED ? 0 : half * 128) + lanes + lane;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        old[j].load(p, q, c + j, col);
+                    for (uint32_t j = 0; j < 16; ++j, out += width)
+                        if (j < rows) {
+                            gstore<float>(out, v[j]);
+                            if (EPI == EPI_GATED)
+                                gstore<float>(out + 128, w[j]);
+                        }
+                } else if (col < q.n) {
+                    uint64_t at = (uint64_t)c * q.n + col, ath = (uint64_t)c * p.ldh + col;
+                    Ahead1<EPI> old[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    if (c + j >= q.m)
-                        break;
-                    if (p.splits > 1) {
-                        float *out = q.partial + ((uint64_t)u.split * q.m + c + j) * width + u.n * kTileN + lanes + lane;
-                        gstore<float>(out + (EPI == EPI_GATED ? 0 : half * 128), v[j]);
-                        if (EPI == EPI_GATED)
-                            gstore<float>(out + 128, w[j]);
-                    } else {
-                        finish1<EPI>(p, q, c + j, col, old[j], v[j], EPI == EPI_GATED ? w[j] : 0.0f);
-                    }
+                    for (uint32_t j = 0; j < 16; ++j)
+                        old[j].load(p, q, at + (uint64_t)j * q.n, j < rows);
+#pragma unroll
+                    for (uint32_t j = 0; j < 16; ++j, at += q.n, ath += p.ldh)
+                        if (j < rows)
+                            finish1<EPI>(p, q, at, ath, old[j], v[j], EPI == EPI_GATED ? w[j] : 0.0f);
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -835,7 +901,8 @@ template <int EPI> __global__ void __launch_bounds__(256) ffn_join_kernel(const 
             const float *at = q.partial + row * width + (EPI == EPI_GATED ? col / 128 * 256 + col % 128 : col);
             float v = 0.0f, w = 0.0f, f[4], h[4];
             Ahead1<EPI> old;
-            old.load(p, q, row, col);
+            const uint64_t place = (uint64_t)row * q.n + col;
+            old.load(p, q, place, true);
             for (uint32_t s0 = 0; s0 < p.splits; s0 += 4) { // four loads in flight
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
@@ -852,7 +919,7 @@ template <int EPI> __global__ void __launch_bounds__(256) ffn_join_kernel(const 
                             w = __fadd_rn(w, h[s]);
                     }
             }
-            finish1<EPI>(p, q, row, col, old, v, w);
+            finish1<EPI>(p, q, place, (uint64_t)row * p.ldh + col, old, v, w);
         }
     }
 }
@@ -950,7 +1017,7 @@ constexpr uint32_t kMaxSplits = 16;
 // part's products and a unit's epilogue, which overlap, plus the join.  A block
 // of K takes a pair about 0.35 us; a CTA with few tokens reads its 32 KiB of
 // weights in 0.5 us alone, and at the memory's rate with the others.  An
-// epilogue takes a pair about 3 us, or 15 us on rows that no 32-byte vector
+// epilogue takes a pair about 3 us, or 15 us on rows that no 16-byte vector
 // divides, and a CTA with few tokens 0.5 us; a join about 3 us and its bytes
 // at 6 TB/s.  Without it a product of few tiles (few tokens, narrow layers)
 // would leave most SMs idle.
@@ -981,7 +1048,7 @@ struct Shape {
 struct Launch {
     Shape s[kMaxProblems];
     int n;
-    bool gated, few, odd; // few: by ffn_few_kernel; odd: the epilogue's rows are no 32-byte vectors
+    bool gated, few, odd; // few: by ffn_few_kernel; odd: the epilogue's rows are no 16-byte vectors
     uint32_t splits;
     size_t partial; // bytes of all splits
     void plan()
@@ -1018,7 +1085,7 @@ bool make_plan(size_t t, size_t d, size_t f, bool backward, bool aligned, FfnPla
     p->dp = (d + 7) / 8 * 8;
     p->fp = (f + 15) / 16 * 16; // h, dg and du in rows of whole 32-byte vectors
     const bool pd = p->dp != d || !aligned, pf = f % 8 || !aligned, few = t <= kFewTokens,
-               od = d % 16 != 0, of = f % 16 != 0;
+               od = d % 8 != 0, of = f % 8 != 0;
     p->up_ = Launch{{{t, f, d, 1}}, 1, true, few, of, 1, 0};
     p->down = Launch{{{t, d, f, 1}}, 1, false, few, od, 1, 0};
     p->dh = Launch{{{t, f, d, 1}}, 1, false, few, of, 1, 0};
@@ -1046,7 +1113,7 @@ bool make_plan(size_t t, size_t d, size_t f, bool backward, bool aligned, FfnPla
         p->wd = take(d * p->fp * 2);
     for (Launch *l : {&p->up_, &p->down, &p->dh, &p->dx, &p->dw}) {
         l->plan();
-        if (backward == (l != &p->up_ && l != &p->down))
+        if (backward || l == &p->up_ || l == &p->down) // a backward pass's buffer serves the forward too
             partial = std::max(partial, l->partial);
     }
     p->partial = take(partial);
@@ -1266,12 +1333,13 @@ ccl_status_t gated_ffn_impl(const FfnArgs &a, void *out, cudaStream_t stream)
     p.u = a.saved ? a.saved + a.t * a.f : nullptr;
     p.ldh = (uint32_t)pl.fp;
     char *partial = work + pl.partial;
-    p.vectors = a.f % 16 == 0 && (uintptr_t)a.saved % 32 == 0;
+    p.vectors = a.f % 8 == 0 && (uintptr_t)a.saved % 32 == 0;
     Problem &q = p.prob[0];
     if (pl.up_.few) {
         if (ccl_status_t st = launch_few<EPI_GATED, false>(p, pl.up_, w2, &x, partial, stream))
             return st;
         q.out = out;
+        p.early = wd.ptr == a.wd; // not a copy made within this call
         return launch_few<EPI_STORE, false>(p, pl.down, &wd, &h, partial, stream);
     }
     if (!encode(&q.a[0], x, false) || !encode(&q.b[0], w2[0], false) || !encode(&q.b[1], w2[1], false))
@@ -1279,7 +1347,7 @@ ccl_status_t gated_ffn_impl(const FfnArgs &a, void *out, cudaStream_t stream)
     if (cudaError_t e = launch_gemm<EPI_GATED, false, false>(p, pl.up_, partial, stream))
         return from_cuda(e);
     q.out = out;
-    p.vectors = a.d % 16 == 0 && (uintptr_t)out % 32 == 0;
+    p.vectors = a.d % 8 == 0 && (uintptr_t)out % 16 == 0;
     if (!encode(&q.a[0], h, false) || !encode(&q.b[0], wd, false))
         return CCL_ERR_CUDA;
     return from_cuda(launch_gemm<EPI_STORE, false, false>(p, pl.down, partial, stream));
@@ -1341,7 +1409,7 @@ ccl_status_t gated_ffn_grad_impl(const FfnArgs &a, const void *dy, void *dx, voi
     p.u = a.saved + a.t * a.f;
     p.ldh = (uint32_t)pl.fp;
     char *partial = work + pl.partial;
-    p.vectors = a.f % 16 == 0 && (uintptr_t)a.saved % 32 == 0;
+    p.vectors = a.f % 8 == 0 && (uintptr_t)a.saved % 32 == 0;
     Problem &q = p.prob[0];
     if (pl.dh.few) {
         if (ccl_status_t st = launch_few<EPI_BACKWARD, true>(p, pl.dh, &wd, &y, partial, stream))
@@ -1354,8 +1422,9 @@ ccl_status_t gated_ffn_grad_impl(const FfnArgs &a, const void *dy, void *dx, voi
     }
     if (dx) {
         q.out = dx;
-        p.vectors = a.d % 16 == 0 && (uintptr_t)dx % 32 == 0;
+        p.vectors = a.d % 8 == 0 && (uintptr_t)dx % 16 == 0;
         if (pl.dx.few) {
+            p.early = w2[0].ptr == a.wg && w2[1].ptr == a.wu; // not copies made within this call
             if (ccl_status_t st = launch_few<EPI_STORE, true>(p, pl.dx, w2, d2, partial, stream))
                 return st;
         } else {
@@ -1370,7 +1439,7 @@ ccl_status_t gated_ffn_grad_impl(const FfnArgs &a, const void *dy, void *dx, voi
         return CCL_OK;
     // the weight gradients asked for, in one launch
     p.accumulate = accumulate != 0;
-    p.vectors = a.d % 16 == 0 && a.f % 16 == 0;
+    p.vectors = a.d % 8 == 0 && a.f % 8 == 0;
     Launch l = pl.dw;
     l.n = 0;
     const Matrix *am[3] = {&d2[0], &d2[1], &y}, *bm[3] = {&x, &x, &h};
@@ -1379,7 +1448,7 @@ ccl_status_t gated_ffn_grad_impl(const FfnArgs &a, const void *dy, void *dx, voi
         if (out[i]) {
             l.s[l.n] = pl.dw.s[i];
             p.prob[l.n].out = out[i];
-            p.vectors = p.vectors && (uintptr_t)out[i] % 32 == 0;
+            p.vectors = p.vectors && (uintptr_t)out[i] % 16 == 0;
             if (!encode(&p.prob[l.n].a[0], *am[i], true) || !encode(&p.prob[l.n].b[0], *bm[i], true))
                 return CCL_ERR_CUDA;
             ++l.n;

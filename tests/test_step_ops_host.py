@@ -116,6 +116,9 @@ def test_plans():
     assert ccl.ccl_plan_gated_ffn_work_bytes(t, d, f, aligned=False) == t * f * 2 + weights + t * d * 2
     assert ccl.ccl_plan_gated_ffn_work_bytes(t, d, f, backward=True, aligned=False) == 3 * t * f * 2 + weights + 2 * t * d * 2
     assert ccl.ccl_plan_gated_ffn_work_bytes(t, d - 1, f) == t * f * 2 + 2 * d * f * 2 + t * d * 2
+    for t, d, f in ((1, 4096, 11008), (48, 300, 700), (300, 1001, 2733), (5000, 64, 64), (2000, 512, 1376), (200, 8, 20000)):
+        # a backward pass's buffer serves the forward too
+        assert ccl.ccl_plan_gated_ffn_work_bytes(t, d, f, backward=True) >= ccl.ccl_plan_gated_ffn_work_bytes(t, d, f)
 
 
 def test_binding_names_what_is_wrong():
