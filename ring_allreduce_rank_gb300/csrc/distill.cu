@@ -32,7 +32,7 @@ namespace {
 constexpr int kDThreads = 256;
 constexpr int kDWarps = kDThreads / 32;
 constexpr int kDCtas = 4;        // resident CTAs per SM
-constexpr int kVecs = 4;         // 16-byte vectors a thread folds at a time
+constexpr int kVecs = 2;         // 16-byte vectors a thread folds at a time
 constexpr int kHeld = 8;         // vectors a thread keeps in registers, and as many in shared memory
 constexpr uint32_t kPart = 2 * kHeld * kDThreads; // vectors a CTA keeps
 constexpr int kMaxCluster = 8;   // portable cluster size
@@ -119,24 +119,21 @@ template <int DT> __device__ __forceinline__ void unpack2(const uint4 &v, float2
                              : make_float2(__uint_as_float(w[i & 3] << 16), __uint_as_float(w[i & 3] & 0xffff0000u));
 }
 
-// The largest value of the first n of kVecs vectors; a NaN does not count (it reaches the sum).
-template <int DT> __device__ __forceinline__ float max_of(const uint4 *x, int n)
+// The largest value of kVecs vectors; a NaN does not count (it reaches the sum).
+template <int DT> __device__ __forceinline__ float max_of(const uint4 *x)
 {
     if (DT == DT_FP32) {
         float m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i)
-            if (i < n)
-                m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(x[i].x), __uint_as_float(x[i].y)),
-                                   fmaxf(__uint_as_float(x[i].z), __uint_as_float(x[i].w))));
+            m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(x[i].x), __uint_as_float(x[i].y)),
+                               fmaxf(__uint_as_float(x[i].z), __uint_as_float(x[i].w))));
         return m;
     }
     uint32_t m = 0xff80ff80u; // -inf twice
     auto up = [&](uint32_t w) { asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w)); };
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-        if (i >= n)
-            break;
         up(x[i].x);
         up(x[i].y);
         up(x[i].z);
@@ -268,7 +265,7 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
     if (!skip) {
 #pragma unroll
         for (int i = 0; i < kHeld; ++i)
-            if (kHeld + i < mine_n) {
+            if (kHeld + i / kVecs * kVecs < mine_n) {
                 if (v0 + tid + (kHeld + i) * kDThreads < v1)
                     copy16_async(&held[i * kDThreads + tid], body + (uint64_t)(v0 + tid) * 16 + (kHeld + i) * kDThreads * 16);
                 else
@@ -355,8 +352,8 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
         // (m, Z): this thread's vectors, then warp, CTA and cluster
         if (!skip) {
             float2 z = make_float2(0.0f, 0.0f);
-            auto fold = [&](const uint4 *x, int n) { // the first n of kVecs vectors
-                const float bm = max_of<DT>(x, n);
+            auto fold = [&](const uint4 *x) {
+                const float bm = max_of<DT>(x);
                 if (bm > st.m) { // the sum so far, relative to the new maximum
                     const float r = row_exp(st.m, bm, p.scale);
                     z = mul2(z, make_float2(r, r));
@@ -365,8 +362,6 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
                 if (st.m == -INFINITY) { // nothing yet but -inf, and perhaps a NaN
 #pragma unroll
                     for (int i = 0; i < kVecs; ++i) {
-                        if (i >= n)
-                            break;
                         float f[VEC];
                         unpack<DT>(x[i], f);
 #pragma unroll
@@ -378,8 +373,6 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
                 const float2 neg = make_float2(-st.m, -st.m);
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
-                    if (i >= n)
-                        break;
                     float2 f[VEC / 2];
                     unpack2<DT>(x[i], f);
 #pragma unroll
@@ -396,17 +389,17 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
 #pragma unroll
             for (int i = 0; i < kHeld; i += kVecs)
                 if (i < mine_n)
-                    fold(x + i, mine_n - i);
+                    fold(x + i);
             copies_wait();
 #pragma unroll 1
             for (int i = 0; i < kHeld && kHeld + i < mine_n; i += kVecs) {
                 from_held(y, i);
-                fold(y, mine_n - kHeld - i);
+                fold(y);
             }
 #pragma unroll 1
             for (uint32_t b = v0 + kPart; b < v1; b += kVecs * kDThreads) {
                 load(y, b + tid);
-                fold(y, kVecs);
+                fold(y);
             }
             st.z = __fadd_rn(z.x, z.y);
             if (edge)
@@ -455,12 +448,10 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
         const float2 c2 = make_float2(c, c), neg = make_float2(-st.m, -st.m);
         const bool vec_store = (((uintptr_t)grow ^ (uintptr_t)row) & 15) == 0;
         char *gbody = grow + (uint64_t)nh * ES;
-        auto emit = [&](const uint4 *x, uint32_t b, int n) {
+        auto emit = [&](const uint4 *x, uint32_t b) {
             char *q = gbody + (uint64_t)b * 16;
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                if (i >= n)
-                    break;
                 uint4 o = make_uint4(0, 0, 0, 0);
                 float2 f[VEC / 2];
                 if (!zero) {
@@ -486,17 +477,17 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < kHeld; i += kVecs)
             if (i < mine_n)
-                emit(x + i, v0 + tid + i * kDThreads, mine_n - i);
+                emit(x + i, v0 + tid + i * kDThreads);
 #pragma unroll 1
         for (int i = 0; i < kHeld && kHeld + i < mine_n; i += kVecs) {
             from_held(y, i);
-            emit(y, v0 + tid + (kHeld + i) * kDThreads, mine_n - kHeld - i);
+            emit(y, v0 + tid + (kHeld + i) * kDThreads);
         }
 #pragma unroll 1
         for (uint32_t b = v0 + kPart; b < v1; b += kVecs * kDThreads) {
             if (!skip)
                 load(y, b + tid);
-            emit(y, b + tid, kVecs);
+            emit(y, b + tid);
         }
         if (edge)
             st_value<DT>(grow, ei, zero ? 0.0f : __fmul_rn(row_exp(xe, st.m, p.scale), c));

@@ -8,11 +8,13 @@
 // Gradient: dE[v] = round([dE[v] +] scale * sum over {t: id_t = v} of dY[t]),
 // the sum in fp32.  Launches, chained so that each starts under the one before:
 //   0. embed_zero_kernel (dense gradient): zeros to the rows that no token
-//      names, which need no sort to be found.
-//   1. embed_sort_kernel, beside it: the tokens' (row, position) pairs sorted
-//      by row, stably, by a radix sort that one cluster of eight CTAs runs (the
-//      digits' counts cross the cluster through distributed shared memory).
-//   2. embed_sum_kernel: the sorted tokens in pieces of 8 to 64, each summed in
+//      names, which need no sort to be found; one CTA of it also ranks the
+//      tokens where they are at most 1024.
+//   1. embed_sort_kernel, for more, beside it: the tokens' (row, position)
+//      pairs sorted by row, stably, by a radix sort that one cluster of eight
+//      CTAs runs (the digits' counts cross the cluster through distributed
+//      shared memory).
+//   2. embed_sum_kernel: the sorted tokens in pieces of 8 to 32, each summed in
 //      order; a row whose tokens lie in one piece is finished here, a row that
 //      crosses pieces leaves one fp32 partial sum per piece.
 //   3. embed_join_kernel: those partial sums, added in order.
@@ -35,9 +37,10 @@ constexpr int kSortCtas = 8;       // one portable cluster
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigits = 256;       // bins of one radix pass
-constexpr int kZeroThreads = 256;
-constexpr int kMaxPiece = 64;      // sorted tokens summed by one warp, at most
-constexpr int kAhead = 8;          // rows' loads a warp has in flight
+constexpr int kZeroThreads = 512;
+constexpr int kMinPiece = 8, kMaxPiece = 32; // sorted tokens summed by one warp
+constexpr int kAhead = 8;          // rows' loads a warp has in flight; pieces are multiples of it
+constexpr int kFewIds = 1024;      // so many tokens are ranked by one CTA instead of sorted
 constexpr int kSumThreads = 128;
 
 // ------------------------------------------------------------------ lookup
@@ -115,6 +118,7 @@ struct SortParams {
     char *grad; // the dense gradient, for its zero rows
     uint64_t pitch, row_bytes;
     int elem;
+    uint32_t zero_ctas, rank; // embed_zero_kernel's CTAs that zero, and whether a further one ranks
 };
 
 __device__ __forceinline__ uint32_t row_key(const SortParams &p, uint64_t t)
@@ -144,27 +148,46 @@ __device__ __forceinline__ void warp_zero(char *q, uint64_t n, int elem, int lan
 }
 
 // A range of rows per CTA: the rows that tokens name marked from all the ids,
-// the others zeroed.
-__global__ void __launch_bounds__(kZeroThreads, 4) embed_zero_kernel(const __grid_constant__ SortParams p)
+// the others zeroed.  With p.rank a further CTA makes the sorted list of at most
+// kFewIds tokens.
+__global__ void __launch_bounds__(kZeroThreads, 2) embed_zero_kernel(const __grid_constant__ SortParams p)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); // the sort does not wait for the zeros
     constexpr uint32_t kBits = 65536;
+    constexpr int kIds = 16;
     __shared__ uint32_t mark[kBits / 32];
+    __shared__ uint64_t pairs[kFewIds];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t per = (p.rows + gridDim.x - 1) / gridDim.x;
+    if (p.rank && blockIdx.x == p.zero_ctas) {
+        // a pair's place is the number of smaller pairs, (row, position) all distinct
+        const uint32_t n = (uint32_t)p.ntokens;
+        for (uint32_t t = tid; t < n; t += kZeroThreads)
+            pairs[t] = (uint64_t)row_key(p, t) << 32 | t;
+        __syncthreads();
+        for (uint32_t t = tid; t < n; t += kZeroThreads) {
+            const uint64_t own = pairs[t];
+            uint32_t place = 0;
+#pragma unroll 8
+            for (uint32_t i = 0; i < n; ++i)
+                place += pairs[i] < own;
+            gstore<uint2>(p.buf[0] + place, make_uint2((uint32_t)(own >> 32), t));
+        }
+        return;
+    }
+    const uint32_t per = (p.rows + p.zero_ctas - 1) / p.zero_ctas;
     const uint64_t end = umin64(p.rows, (uint64_t)(blockIdx.x + 1) * per);
     for (uint64_t lo = (uint64_t)blockIdx.x * per; lo < end; lo += kBits) {
         const uint32_t n = (uint32_t)umin64(kBits, end - lo);
         for (uint32_t i = tid; i < (n + 31) / 32; i += kZeroThreads)
             mark[i] = 0;
         __syncthreads();
-        for (uint64_t t0 = tid; t0 < p.ntokens; t0 += 8 * kZeroThreads) {
-            uint32_t key[8]; // eight loads in flight
+        for (uint64_t t0 = tid; t0 < p.ntokens; t0 += kIds * kZeroThreads) {
+            uint32_t key[kIds]; // as many loads in flight
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < kIds; ++j)
                 key[j] = t0 + j * kZeroThreads < p.ntokens ? row_key(p, t0 + j * kZeroThreads) : 0xffffffffu;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < kIds; ++j) {
                 const uint64_t r = (uint64_t)key[j] - lo;
                 if (r < n)
                     atomicOr(&mark[r >> 5], 1u << (r & 31));
@@ -191,29 +214,6 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
     const uint64_t lo = ((uint64_t)blockIdx.x * kSortWarps + warp) * slice;
     const uint64_t hi = umin64(p.ntokens, lo + slice);
     const uint32_t below = (1u << lane) - 1;
-
-    if (p.ntokens <= kSortThreads) {
-        // one CTA ranks the few pairs by counting, without passes
-        if (blockIdx.x == 0) {
-            uint64_t *key = reinterpret_cast<uint64_t *>(&cnt[0][0]);
-            const uint32_t n = (uint32_t)p.ntokens;
-            const uint32_t row = tid < (int)n ? row_key(p, tid) : 0;
-            const uint64_t own = (uint64_t)row << 32 | (uint32_t)tid;
-            if (tid < (int)n)
-                key[tid] = own;
-            __syncthreads();
-            if (tid < (int)n) {
-                uint32_t rank = 0;
-#pragma unroll 8
-                for (uint32_t i = 0; i < n; ++i)
-                    rank += key[i] < own;
-                gstore<uint2>(p.buf[(p.passes - 1) & 1] + rank, make_uint2(row, (uint32_t)tid));
-            }
-        }
-        // the sums come after this kernel, and with it after the zeros
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        return; // the same for the whole cluster: no other CTA waits
-    }
 
     for (int pass = 0; pass < p.passes; ++pass) {
         const int shift = pass * p.bits;
@@ -530,12 +530,12 @@ bool aligned16(const void *p, size_t pitch, size_t row_bytes)
     return ((uintptr_t)p | pitch | row_bytes) % 16 == 0;
 }
 
-// Tokens a piece: eight, one batch of loads, doubled up to 64 while that
+// Tokens a piece: eight, doubled up to 32 while that
 // still leaves more warps than the GPU holds about half full (152 SMs x 32
 // warps; a warp covers at least 128 columns).
 uint32_t piece_of(size_t ntokens, size_t dim)
 {
-    uint32_t n = kAhead;
+    uint32_t n = kMinPiece;
     while (n < kMaxPiece && (ntokens / n) * ((dim + 127) / 128) > 152 * 32)
         n *= 2;
     return n;
@@ -664,34 +664,40 @@ ccl_status_t embedding_grad_impl(const void *grad_out, size_t grad_out_stride, c
     s.elem = (int)es;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
+    s.rank = ntokens && ntokens <= kFewIds;
     if (!accumulate) {
         int sms = 0, dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return CCL_ERR_CUDA;
-        cfg.gridDim = dim3((unsigned)std::min<size_t>(rows, 4 * (size_t)sms)); // all resident
+        s.zero_ctas = (uint32_t)std::min<size_t>(rows, 2 * (size_t)sms); // all resident
+    }
+    if (s.zero_ctas + s.rank) {
+        cfg.gridDim = dim3(s.zero_ctas + s.rank);
         cfg.blockDim = dim3(kZeroThreads);
         if (cudaError_t e = cudaLaunchKernelEx(&cfg, embed_zero_kernel, s))
             return from_cuda(e);
         count_launches(1);
-        if (ntokens == 0)
-            return CCL_OK;
     }
-    cfg.gridDim = dim3(kSortCtas);
-    cfg.blockDim = dim3(kSortThreads);
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kSortCtas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = accumulate ? 1 : 2; // beside the zeros, when there are any
-    if (cudaError_t e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, s))
-        return from_cuda(e);
-    count_launches(1);
+    if (ntokens == 0)
+        return CCL_OK;
+    if (!s.rank) {
+        cfg.gridDim = dim3(kSortCtas);
+        cfg.blockDim = dim3(kSortThreads);
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kSortCtas;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = accumulate ? 1 : 2; // beside the zeros, when there are any
+        if (cudaError_t e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, s))
+            return from_cuda(e);
+        count_launches(1);
+    }
     SumParams p{};
-    p.sorted = s.buf[(s.passes - 1) & 1];
+    p.sorted = s.buf[s.rank ? 0 : (s.passes - 1) & 1];
     p.ntokens = ntokens;
     p.dim = dim;
     p.dim_pad = (dim + 3) / 4 * 4;

@@ -104,10 +104,10 @@ def test_c_entries_refuse_before_launching():
 
 
 def test_plans():
-    # two lists of (row, position) pairs, and two fp32 partial rows for every piece of 8 (few tokens) to 64 once there are two
+    # two lists of (row, position) pairs, and two fp32 partial rows for every piece of 8 (few tokens) to 32 once there are two
     assert ccl.ccl_plan_embedding_grad_work_bytes(8, 1000, 4096) == 2 * 256
     assert ccl.ccl_plan_embedding_grad_work_bytes(64, 1000, 4096) == 2 * 512 + 2 * 8 * 4096 * 4
-    assert ccl.ccl_plan_embedding_grad_work_bytes(1 << 20, 1000, 4096) == 2 * (8 << 20) + 2 * (1 << 14) * 4096 * 4
+    assert ccl.ccl_plan_embedding_grad_work_bytes(1 << 20, 1000, 4096) == 2 * (8 << 20) + 2 * (1 << 15) * 4096 * 4
     # h alone; h, dg and du; padded copies where a width is no multiple of 8 or a base is unaligned
     t, d, f = 4096, 4096, 11008
     assert ccl.ccl_plan_gated_ffn_work_bytes(t, d, f) == t * f * 2
