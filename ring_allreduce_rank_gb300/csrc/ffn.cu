@@ -937,38 +937,36 @@ struct PackParams {
 };
 
 // Rows of `cols` elements to rows `ld` apart (ld a multiple of 8), the rest of
-// a row zero; a thread writes a vector of eight.
+// a row zero; a thread writes a vector of eight, blockIdx.y is the matrix.
 __global__ void __launch_bounds__(256) ffn_pack_kernel(const __grid_constant__ PackParams p)
 {
     chain_entry();
-    for (int k = 0; k < p.n; ++k) {
-        const auto &m = p.m[k];
-        const uint32_t per = m.ld / 8;
-        for (uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x; e < m.vectors; e += (uint64_t)gridDim.x * 256) {
-            const uint64_t r = m.vectors >> 32 ? e / per : (uint32_t)e / per;
-            const uint32_t c = (uint32_t)(e - r * per) * 8;
-            const uint16_t *src = m.src + r * m.cols + c;
-            if (c && c + 9 <= m.cols) {
-                // inside a row: the words around the eight values
-                const uint32_t odd = (uintptr_t)src & 2;
-                const uint16_t *word = src - odd / 2;
-                uint32_t x[5];
+    const auto &m = p.m[blockIdx.y];
+    const uint32_t per = m.ld / 8;
+    for (uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x; e < m.vectors; e += (uint64_t)gridDim.x * 256) {
+        const uint64_t r = m.vectors >> 32 ? e / per : (uint32_t)e / per;
+        const uint32_t c = (uint32_t)(e - r * per) * 8;
+        const uint16_t *src = m.src + r * m.cols + c;
+        if (c && c + 9 <= m.cols) {
+            // inside a row: the words around the eight values
+            const uint32_t odd = (uintptr_t)src & 2;
+            const uint16_t *word = src - odd / 2;
+            uint32_t x[5];
 #pragma unroll
-                for (int i = 0; i < 5; ++i)
-                    x[i] = i < 4 || odd ? gload<uint32_t>(word + 2 * i) : 0;
-                uint32_t o[4];
+            for (int i = 0; i < 5; ++i)
+                x[i] = i < 4 || odd ? gload<uint32_t>(word + 2 * i) : 0;
+            uint32_t o[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[i] = __funnelshift_r(x[i], x[i + 1], odd * 8);
-                st16(m.dst + e * 8, make_uint4(o[0], o[1], o[2], o[3]));
-                continue;
-            }
-            uint32_t h[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                h[i] = c + i < m.cols ? gload<uint16_t>(src + i) : 0;
-            st16(m.dst + e * 8, make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16));
+            for (int i = 0; i < 4; ++i)
+                o[i] = __funnelshift_r(x[i], x[i + 1], odd * 8);
+            st16(m.dst + e * 8, make_uint4(o[0], o[1], o[2], o[3]));
+            continue;
         }
+        uint32_t h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            h[i] = c + i < m.cols ? gload<uint16_t>(src + i) : 0;
+        st16(m.dst + e * 8, make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16));
     }
 }
 
@@ -1144,7 +1142,7 @@ class Operands {
     {
         if (p_.n == 0)
             return cudaSuccess;
-        const cudaError_t e = launch_chained(ffn_pack_kernel, dim3((unsigned)std::min<uint64_t>((most_ + 255) / 256, 8 * kSms)), dim3(256), 0, stream, p_);
+        const cudaError_t e = launch_chained(ffn_pack_kernel, dim3((unsigned)std::min<uint64_t>((most_ + 255) / 256, 8 * kSms), (unsigned)p_.n), dim3(256), 0, stream, p_);
         if (e == cudaSuccess)
             count_launches(1);
         return e;
