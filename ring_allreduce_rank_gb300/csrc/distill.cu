@@ -7,14 +7,19 @@
 //     ds_v  = w / tau * (q_v - sum_{j: i_j = v} p_j).
 // With m the row's maximum and Z = sum_v exp((s_v - m) / tau), both need one
 // pass over the row for (m, Z); the gradient needs the row's values again.
-// Bound by memory bandwidth, which sees one read of the logits and one write
-// of the gradient: a cluster of CTAs takes a row, each CTA asks for its whole
-// part at once (up to 64 KiB: half to shared memory by asynchronous copies,
-// half to registers) and keeps it there between the two uses, and the CTAs
-// join (m, Z) through distributed shared memory.  Four CTAs an SM are at
-// different places of this, so that loads, exponentials and stores overlap.
-// Reading the row a second time from the L2 cache instead missed the cache
-// (608 CTAs' rows of 250 KiB exceed it): 471 us for 4096 rows of 128000 bf16.
+// Bound by memory bandwidth.  The loss alone uses a row once: a CTA streams it
+// through its registers, eight vectors a thread in flight (4096 rows of 128000
+// bf16: 160 us, 0.97 of the measured copy bandwidth).  For loss and gradient
+// in one call memory sees one read of the logits and one write of the gradient:
+// a cluster of CTAs takes a row, each CTA asks for its whole part at once (up to
+// 64 KiB: half to registers, half to shared memory by asynchronous copies) and
+// keeps it there between the two uses, and the CTAs join (m, Z) through
+// distributed shared memory.  Four CTAs an SM are at different places of this,
+// so that loads, exponentials and stores overlap: 406 us for the same rows,
+// 0.76 of the copy bandwidth (reading a row a second time from the L2 cache
+// missed it, 608 CTAs' rows of 250 KiB, and took 471).  The gradient from kept
+// statistics asks for its part in the same way, 350 us (streaming it like the
+// loss, stores between the loads, took 409).
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -29,7 +34,7 @@ namespace cg = cooperative_groups;
 namespace ccl {
 namespace {
 
-constexpr int kDThreads = 256;
+constexpr int kDThreads = 256;   // that hold a row's vectors; a further warp works on the teacher's entries
 constexpr int kDWarps = kDThreads / 32;
 constexpr int kDCtas = 4;        // resident CTAs per SM
 constexpr int kVecs = 2;         // 16-byte vectors a thread folds at a time
@@ -55,6 +60,7 @@ struct DistillParams {
     uint32_t slot_bits;   // the hash table of the listed ids has 2^slot_bits places
     float scale;          // log2(e) / tau
     float inv_tau;
+    uint32_t cluster_bits; // 2^cluster_bits CTAs take a row
 };
 
 __device__ __forceinline__ float exp2_approx(float x)
@@ -155,47 +161,34 @@ __device__ __forceinline__ Stat join(const Stat &a, const Stat &b, float scale)
 
 __device__ __forceinline__ Stat warp_join(Stat s, float scale)
 {
+    float m = s.m;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        Stat t;
-        t.m = __shfl_xor_sync(0xffffffffu, s.m, o);
-        t.z = __shfl_xor_sync(0xffffffffu, s.z, o);
-        s = join(s, t, scale);
-    }
+    for (int o = 16; o; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (s.m != m) // not where both are -inf
+        s.z = __fmul_rn(s.z, row_exp(s.m, m, scale));
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        s.z = __fadd_rn(s.z, __shfl_xor_sync(0xffffffffu, s.z, o));
+    s.m = m;
     return s;
 }
 
-// Sum or maximum over the first `warps` warps, which alone call this; buf
-// holds a value per warp and is used once.
-template <bool MAX> __device__ __forceinline__ float warps_reduce(float v, float *buf, int warps)
+template <bool MAX> __device__ __forceinline__ float warp_reduce(float v)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         const float u = __shfl_xor_sync(0xffffffffu, v, o);
         v = MAX ? fmaxf(v, u) : __fadd_rn(v, u);
     }
-    if (warps == 1) {
-        __syncwarp();
-        return v;
-    }
-    if (lane == 0)
-        buf[warp] = v;
-    asm volatile("bar.sync 1, %0;" ::"r"(warps * 32) : "memory");
-    v = lane < warps ? buf[lane] : (MAX ? -INFINITY : 0.0f);
-#pragma unroll
-    for (int o = kDWarps / 2; o; o >>= 1) {
-        const float u = __shfl_xor_sync(0xffffffffu, v, o);
-        v = MAX ? fmaxf(v, u) : __fadd_rn(v, u);
-    }
-    return __shfl_sync(0xffffffffu, v, 0);
+    return v;
 }
 
 // One cluster per row.  The row's 16-byte vectors are shared out over the
 // cluster's CTAs in contiguous parts; the elements before the first 16-byte
 // boundary and after the last one (fewer than a vector each) are CTA 0's.
 template <int DT, int MODE>
-__global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid_constant__ DistillParams p)
+__global__ void __launch_bounds__(kDThreads + 32, MODE == DISTILL_FUSED ? kDCtas : kDCtas - 1) distill_kernel(const __grid_constant__ DistillParams p)
 {
     constexpr int VEC = DType<DT>::kVec, ES = DType<DT>::kSize;
     constexpr uint32_t kNone = 0xffffffffu, kEntry = 0x7fffffffu;
@@ -204,14 +197,13 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
     __shared__ float prob[kMaxTop];  // p_j, 0 for entries that do not count
     __shared__ float logit[kMaxTop]; // the student's logit at id j
     __shared__ uint32_t slot[MODE == DISTILL_LOSS ? 1 : 2 * kMaxTop]; // an entry of each id, hashed
-    __shared__ float red[3][kDWarps];
     __shared__ int present; // whether the row has a teacher
     __shared__ Stat wstat[kMaxCluster * kDWarps]; // every warp of the cluster's part of the row
     cg::cluster_group cluster = cg::this_cluster();
-    const uint32_t ctas = cluster.num_blocks(), cta = cluster.block_rank();
+    const uint32_t ctas = 1u << p.cluster_bits, cta = blockIdx.x & (ctas - 1); // its rank in the cluster
     if (MODE != DISTILL_GRAD)
         cluster_arrive(); // waited for before the first write to another CTA
-    const uint64_t t = blockIdx.x / ctas;
+    const uint64_t t = blockIdx.x >> p.cluster_bits;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int top = (int)p.top;
 
@@ -220,10 +212,10 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
     char *grow = MODE == DISTILL_LOSS ? nullptr : p.grad + t * p.grad_pitch;
     const uint32_t nh = (uint32_t)umin64(p.vocab, ((16 - ((uintptr_t)row & 15)) & 15) / ES);
     const uint32_t nv = ((uint32_t)p.vocab - nh) / VEC, nt = (uint32_t)p.vocab - nh - nv * VEC;
-    const uint32_t per = (nv + ctas - 1) / ctas, v0 = min(nv, per * cta), v1 = min(nv, v0 + per);
+    const uint32_t per = (nv + ctas - 1) >> p.cluster_bits, v0 = min(nv, per * cta), v1 = min(nv, v0 + per);
     const char *body = row + (uint64_t)nh * ES;
     // an edge element: head, then tail
-    const bool edge = cta == 0 && tid < (int)(nh + nt);
+    const bool edge = cta == 0 && tid < (int)(nh + nt); // (fewer than 16 threads)
     const uint32_t ei = tid < (int)nh ? tid : (uint32_t)p.vocab - nt + (tid - nh);
     // a row whose weight is 0 has loss 0 and gradient 0 whatever it holds
     // (its statistics are still wanted where the caller keeps them)
@@ -234,6 +226,12 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
     const uint4 ninf = make_uint4(kNinf, kNinf, kNinf, kNinf);
     auto load = [&](uint4 *x, uint32_t b) {
         const char *q = body + (uint64_t)b * 16;
+        if (b - tid + kVecs * kDThreads <= v1) { // the whole CTA's vectors
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+                x[i] = ld16(q + i * kDThreads * 16);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             x[i] = ninf;
@@ -249,22 +247,12 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
     // vectors a thread has to work on (some threads one less): registers
     // first, then shared memory, then what does not fit
     const int mine_n = (int)((v1 - v0 + kDThreads - 1) / kDThreads);
-    // the teacher's entries are worked on by as many warps as there are
-    // entries for; the loss is CTA 0's.  Their loads go out before the row's,
-    // which would delay them.
-    const int warps = max(1, min(kDWarps, (top + 31) / 32)), step = warps * 32;
-    const bool listed = !skip && warp < warps && (MODE != DISTILL_LOSS || cta == 0);
-    int64_t first_id = -1;
-    float first_logit = 0.0f, first_student = 0.0f;
-    if (listed && tid < top) {
-        first_id = gload<int64_t>(p.ids + t * p.top + tid);
-        first_logit = gload<float>(p.teacher + t * p.top + tid);
-    }
+    const bool holds = warp < kDWarps; // else the warp of the teacher's entries
     uint4 x[kHeld];
     float xe = 0.0f;
-    if (!skip) {
+    if (!skip && holds) {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i)
+        for (int i = 0; MODE != DISTILL_LOSS && i < kHeld; ++i)
             if (kHeld + i / kVecs * kVecs < mine_n) {
                 if (v0 + tid + (kHeld + i) * kDThreads < v1)
                     copy16_async(&held[i * kDThreads + tid], body + (uint64_t)(v0 + tid) * 16 + (kHeld + i) * kDThreads * 16);
@@ -285,59 +273,77 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
         return v >= v0 && v < v1;
     };
 
-    // the teacher's probabilities
-    if (warp < warps) {
-        float tm = -INFINITY;
+    // The teacher's entries: a warp of their own, beside the sums of the row.
+    // The loss is CTA 0's.
+    const bool listed = !holds && !skip && (MODE != DISTILL_LOSS || cta == 0);
+    float tm = -INFINITY;
+    if (!holds) {
+        constexpr int kBatch = 4;
         if (MODE != DISTILL_LOSS)
-            for (uint32_t i = tid; i < 1u << p.slot_bits; i += step)
+            for (uint32_t i = lane; i < 1u << p.slot_bits; i += 32)
                 slot[i] = kNone;
         if (listed)
-            for (int j = tid; j < top; j += step) {
-                const int64_t i = j == tid ? first_id : gload<int64_t>(p.ids + t * p.top + j);
-                const bool ok = (uint64_t)i < p.vocab;
-                const float l = !ok ? -INFINITY : j == tid ? first_logit : gload<float>(p.teacher + t * p.top + j);
-                id[j] = ok ? (uint32_t)i : kNone;
-                prob[j] = l;
-                // CTA 0 needs every listed logit for the loss, the others
-                // their own; the first one's is waited for only later
-                if (ok && (mine((uint32_t)i) || (MODE != DISTILL_GRAD && cta == 0))) {
-                    if (j == tid)
-                        first_student = ld_value<DT>(row, (uint64_t)i);
-                    else
-                        logit[j] = ld_value<DT>(row, (uint64_t)i);
+            for (int j0 = lane; j0 < top; j0 += 32 * kBatch) {
+                int64_t i[kBatch];
+                float l[kBatch], student[kBatch];
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b)
+                    if (j0 + 32 * b < top) {
+                        i[b] = gload<int64_t>(p.ids + t * p.top + j0 + 32 * b);
+                        l[b] = gload<float>(p.teacher + t * p.top + j0 + 32 * b);
+                    }
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    // CTA 0 needs every listed logit for the loss, the others their own
+                    student[b] = 0.0f;
+                    if (j0 + 32 * b < top && (uint64_t)i[b] < p.vocab && (mine((uint32_t)i[b]) || (MODE != DISTILL_GRAD && cta == 0)))
+                        student[b] = ld_value<DT>(row, (uint64_t)i[b]);
                 }
-                // a NaN counts as present, so that it reaches the result
-                tm = l != l ? INFINITY : fmaxf(tm, l);
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b)
+                    if (j0 + 32 * b < top) {
+                        const bool ok = (uint64_t)i[b] < p.vocab;
+                        const float v = ok ? l[b] : -INFINITY;
+                        id[j0 + 32 * b] = ok ? (uint32_t)i[b] : kNone;
+                        prob[j0 + 32 * b] = v;
+                        logit[j0 + 32 * b] = student[b];
+                        // a NaN counts as present, so that it reaches the result
+                        tm = v != v ? INFINITY : fmaxf(tm, v);
+                    }
             }
-        tm = warps_reduce<true>(tm, red[0], warps);
+        tm = warp_reduce<true>(tm);
+        if (lane == 0)
+            present = tm > -INFINITY;
+    }
+    auto probabilities = [&] {
         float tz = 0.0f;
-        if (tm > -INFINITY)
-            for (int j = tid; j < top; j += step) {
-                const float e = id[j] != kNone ? exp2f(__fmul_rn(__fsub_rn(prob[j], tm), p.scale)) : 0.0f;
-                prob[j] = e;
-                tz = __fadd_rn(tz, e);
-                if (MODE != DISTILL_LOSS && id[j] != kNone) {
-                    // one entry stands for each id in an open hash table at most
-                    // half full; the top bit says that the id has others
-                    const uint32_t mask = (1u << p.slot_bits) - 1;
-                    for (uint32_t h = id[j] * 2654435761u >> (32 - p.slot_bits);; h = (h + 1) & mask) {
-                        const uint32_t was = atomicCAS(&slot[h], kNone, (uint32_t)j);
-                        if (was == kNone)
-                            break;
-                        if (id[was & kEntry] == id[j]) {
-                            atomicOr(&slot[h], ~kEntry);
-                            break;
-                        }
+        if (!(tm > -INFINITY))
+            return;
+        for (int j = lane; j < top; j += 32) {
+            const float e = id[j] != kNone ? exp2f(__fmul_rn(__fsub_rn(prob[j], tm), p.scale)) : 0.0f;
+            prob[j] = e;
+            tz = __fadd_rn(tz, e);
+            if (MODE != DISTILL_LOSS && id[j] != kNone) {
+                // one entry stands for each id in an open hash table at most
+                // half full; the top bit says that the id has others
+                const uint32_t mask = (1u << p.slot_bits) - 1;
+                for (uint32_t h = id[j] * 2654435761u >> (32 - p.slot_bits);; h = (h + 1) & mask) {
+                    const uint32_t was = atomicCAS(&slot[h], kNone, (uint32_t)j);
+                    if (was == kNone)
+                        break;
+                    if (id[was & kEntry] == id[j]) {
+                        atomicOr(&slot[h], ~kEntry);
+                        break;
                     }
                 }
             }
-        tz = warps_reduce<false>(tz, red[1], warps);
-        if (tm > -INFINITY)
-            for (int j = tid; j < top; j += step)
-                prob[j] = __fdiv_rn(prob[j], tz);
-        if (tid == 0)
-            present = tm > -INFINITY;
-    }
+        }
+        tz = warp_reduce<false>(tz);
+        for (int j = lane; j < top; j += 32)
+            prob[j] = __fdiv_rn(prob[j], tz);
+        __syncwarp();
+    };
+
     Stat st{-INFINITY, 0.0f};
     const float2 scale2 = make_float2(p.scale, p.scale);
     uint4 y[kVecs];
@@ -345,12 +351,12 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
         st.m = gload<float>(p.stats + 2 * t);
         st.z = gload<float>(p.stats + 2 * t + 1);
         copies_wait();
-        if (tid < top && tid < step)
-            logit[tid] = first_student;
         __syncthreads();
+        if (!holds)
+            probabilities();
     } else {
         // (m, Z): this thread's vectors, then warp, CTA and cluster
-        if (!skip) {
+        if (!skip && holds) {
             float2 z = make_float2(0.0f, 0.0f);
             auto fold = [&](const uint4 *x) {
                 const float bm = max_of<DT>(x);
@@ -386,34 +392,46 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
                     z = add2(z, f[0]);
                 }
             };
+            if (MODE == DISTILL_LOSS) {
+                // nothing is needed again: the registers take the next vectors
+#pragma unroll 1
+                for (int n = 0; n < mine_n; n += kHeld)
 #pragma unroll
-            for (int i = 0; i < kHeld; i += kVecs)
-                if (i < mine_n)
-                    fold(x + i);
-            copies_wait();
+                    for (int i = 0; i < kHeld; i += kVecs) {
+                        fold(x + i);
+                        load(x + i, v0 + tid + (uint32_t)(n + kHeld + i) * kDThreads);
+                    }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kHeld; i += kVecs)
+                    if (i < mine_n)
+                        fold(x + i);
+                copies_wait();
 #pragma unroll 1
-            for (int i = 0; i < kHeld && kHeld + i < mine_n; i += kVecs) {
-                from_held(y, i);
-                fold(y);
-            }
+                for (int i = 0; i < kHeld && kHeld + i < mine_n; i += kVecs) {
+                    from_held(y, i);
+                    fold(y);
+                }
 #pragma unroll 1
-            for (uint32_t b = v0 + kPart; b < v1; b += kVecs * kDThreads) {
-                load(y, b + tid);
-                fold(y);
+                for (uint32_t b = v0 + kPart; b < v1; b += kVecs * kDThreads) {
+                    load(y, b + tid);
+                    fold(y);
+                }
             }
             st.z = __fadd_rn(z.x, z.y);
             if (edge)
                 st = join(st, Stat{xe, xe == -INFINITY ? 0.0f : row_exp(xe, xe, p.scale)}, p.scale);
         }
-        st = warp_join(st, p.scale);
-        if (tid < top && tid < step)
-            logit[tid] = first_student;
+        if (holds)
+            st = warp_join(st, p.scale);
         cluster_wait(); // every CTA of the cluster has begun
-        if (lane < (int)ctas)
+        if (holds && lane < (int)ctas)
             cluster.map_shared_rank(wstat, lane)[cta * kDWarps + warp] = st;
         // from here on a CTA may overwrite its part of the logits (in place):
         // every read of another CTA's part is above
         cluster_arrive();
+        if (listed)
+            probabilities();
         cluster_wait();
         st = Stat{-INFINITY, 0.0f};
 #pragma unroll
@@ -421,22 +439,22 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
             if (i + lane < (int)ctas * kDWarps)
                 st = join(st, wstat[i + lane], p.scale);
         st = warp_join(st, p.scale);
-        if (cta == 0 && warp < warps) {
-            if (p.stats && tid == 0) {
+        if (cta == 0 && !holds) {
+            if (p.stats && lane == 0) {
                 gstore<float>(p.stats + 2 * t, st.m);
                 gstore<float>(p.stats + 2 * t + 1, st.z);
             }
             float sum = 0.0f;
-            if (present) {
+            if (tm > -INFINITY) {
                 const float lz = logf(st.z);
-                for (int j = tid; j < top; j += step)
+                for (int j = lane; j < top; j += 32)
                     if (!(prob[j] == 0.0f)) {
                         const float logq = __fsub_rn(__fmul_rn(__fsub_rn(logit[j], st.m), p.inv_tau), lz);
                         sum = __fadd_rn(sum, __fmul_rn(prob[j], __fsub_rn(logf(prob[j]), logq)));
                     }
             }
-            sum = warps_reduce<false>(sum, red[2], warps);
-            if (tid == 0)
+            sum = warp_reduce<false>(sum);
+            if (lane == 0)
                 gstore<float>(p.loss + t, w == 0.0f ? 0.0f : __fmul_rn(w, sum));
         }
     }
@@ -450,6 +468,7 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
         char *gbody = grow + (uint64_t)nh * ES;
         auto emit = [&](const uint4 *x, uint32_t b) {
             char *q = gbody + (uint64_t)b * 16;
+            const bool whole = vec_store && b - tid + kVecs * kDThreads <= v1;
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
                 uint4 o = make_uint4(0, 0, 0, 0);
@@ -461,7 +480,9 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
                         f[k] = mul2(row_exp2(f[k], neg, scale2), c2);
                     o = pack<DT>(reinterpret_cast<const float *>(f));
                 }
-                if (b + i * kDThreads < v1) {
+                if (whole) {
+                    st16(q + i * kDThreads * 16, o);
+                } else if (b + i * kDThreads < v1) {
                     if (vec_store) {
                         st16(q + i * kDThreads * 16, o);
                     } else {
@@ -474,26 +495,28 @@ __global__ void __launch_bounds__(kDThreads, kDCtas) distill_kernel(const __grid
                 }
             }
         };
+        if (holds) {
 #pragma unroll
-        for (int i = 0; i < kHeld; i += kVecs)
-            if (i < mine_n)
-                emit(x + i, v0 + tid + i * kDThreads);
+            for (int i = 0; i < kHeld; i += kVecs)
+                if (i < mine_n)
+                    emit(x + i, v0 + tid + i * kDThreads);
 #pragma unroll 1
-        for (int i = 0; i < kHeld && kHeld + i < mine_n; i += kVecs) {
-            from_held(y, i);
-            emit(y, v0 + tid + (kHeld + i) * kDThreads);
-        }
+            for (int i = 0; i < kHeld && kHeld + i < mine_n; i += kVecs) {
+                from_held(y, i);
+                emit(y, v0 + tid + (kHeld + i) * kDThreads);
+            }
 #pragma unroll 1
-        for (uint32_t b = v0 + kPart; b < v1; b += kVecs * kDThreads) {
-            if (!skip)
-                load(y, b + tid);
-            emit(y, b + tid);
+            for (uint32_t b = v0 + kPart; b < v1; b += kVecs * kDThreads) {
+                if (!skip)
+                    load(y, b + tid);
+                emit(y, b + tid);
+            }
         }
         if (edge)
             st_value<DT>(grow, ei, zero ? 0.0f : __fmul_rn(row_exp(xe, st.m, p.scale), c));
         __syncthreads(); // before the listed ids' gradients replace what was written
         if (!zero)
-            for (uint32_t h = tid; h < 1u << p.slot_bits; h += kDThreads) {
+            for (uint32_t h = tid; h < 1u << p.slot_bits; h += kDThreads + 32) {
                 const uint32_t e = slot[h];
                 if (e == kNone)
                     continue;
@@ -520,12 +543,13 @@ cudaError_t launch_distill(const DistillParams &p, uint64_t rows, uint32_t ctas,
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * ctas));
-    cfg.blockDim = dim3(kDThreads);
-    cfg.dynamicSmemBytes = kHeld * kDThreads * 16;
+    cfg.blockDim = dim3(kDThreads + 32);
+    cfg.dynamicSmemBytes = MODE == DISTILL_LOSS ? 0 : kHeld * kDThreads * 16;
     cfg.stream = stream;
     static std::atomic<unsigned long long> ready{0};
-    if (cudaError_t e = large_smem_once(reinterpret_cast<const void *>(distill_kernel<DT, MODE>), (int)cfg.dynamicSmemBytes, ready))
-        return e;
+    if (MODE != DISTILL_LOSS)
+        if (cudaError_t e = large_smem_once(reinterpret_cast<const void *>(distill_kernel<DT, MODE>), (int)cfg.dynamicSmemBytes, ready))
+            return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ctas;
@@ -613,13 +637,17 @@ ccl_status_t distill_impl(int mode, const DistillArgs &a, cudaStream_t stream)
     p.slot_bits = 5;
     while (1u << p.slot_bits < 2 * a.top)
         ++p.slot_bits;
-    // the fewest CTAs that hold a row; more, as long as each thread has a
-    // batch of vectors, while they leave places on the GPU empty
+    // the fewest CTAs that hold a row (for the loss alone: one); more, as long
+    // as each thread has a batch of vectors, while they leave places on the
+    // GPU empty
     const uint64_t bytes = a.vocab * es;
     uint32_t ctas = 1;
-    while (ctas < kMaxCluster && (bytes > (uint64_t)ctas * kPart * 16 ||
-                                  (a.nrows * ctas < 152 * kDCtas && bytes >= (uint64_t)2 * ctas * kVecs * kDThreads * 16)))
+    p.cluster_bits = 0;
+    while (ctas < kMaxCluster && ((mode != DISTILL_LOSS && bytes > (uint64_t)ctas * kPart * 16) ||
+                                  (a.nrows * ctas < 152 * kDCtas && bytes >= (uint64_t)2 * ctas * kVecs * kDThreads * 16))) {
         ctas *= 2;
+        ++p.cluster_bits;
+    }
     const bool f = a.dtype == CCL_FP32;
     cudaError_t e;
     if (mode == DISTILL_LOSS)
