@@ -429,7 +429,8 @@ ccl_status_t ccl_allreduce_host(const void *const *send, void *const *recv, int 
  * enqueued on `stream`, argument errors returned before anything is enqueued,
  * CCL_ERR_OVERLAP where a written buffer overlaps another one of the call
  * (except in the in-place forms noted), nothing allocated, so that every call
- * may be captured in a CUDA graph.  Sums are held in fp32 and each output is
+ * may be captured in a CUDA graph (after one call of its kind on the device,
+ * which sets its kernels up).  Sums are held in fp32 and each output is
  * rounded once to its type.  Strides are in elements, from one row to the
  * next, and at least the row's length; buffers need only their element's
  * alignment (16-byte aligned rows of whole 16-byte vectors run at full
@@ -558,7 +559,8 @@ ccl_status_t ccl_check_read(unsigned long long *mismatches, int reset);
 
 /* Debug builds (libccl_debug.so, compiled with CCL_DEBUG_BOUNDS) check every
  * global load and store of every kernel against the byte ranges of the
- * call's own buffers, library workspace included; an access outside them is
+ * call's own buffers, library workspace included (but not the tensor-map
+ * copies of the gated feed-forward block, which their maps bound); an access outside them is
  * skipped, never performed, and counted.  Waits for the device and returns
  * the count and the first offending address.  Release builds return
  * CCL_ERR_UNSUPPORTED.  Calls whose work overlaps on the GPU share the range

