@@ -8,8 +8,8 @@
 // Gradient: dE[v] = round([dE[v] +] scale * sum over {t: id_t = v} of dY[t]),
 // the sum in fp32.  Launches, chained so that each starts under the one before:
 //   0. embed_zero_kernel (dense gradient): zeros to the rows that no token
-//      names, which need no sort to be found; one CTA of it also ranks the
-//      tokens where they are at most 1024.
+//      names, which need no sort to be found; a few further CTAs of it rank
+//      the tokens where they are at most 4096.
 //   1. embed_sort_kernel, for more, beside it: the tokens' (row, position)
 //      pairs sorted by row, stably, by a radix sort that one cluster of eight
 //      CTAs runs (the digits' counts cross the cluster through distributed
@@ -44,7 +44,8 @@ constexpr int kDigits = 256;       // bins of one radix pass
 constexpr int kZeroThreads = 512;
 constexpr int kMinPiece = 8, kMaxPiece = 32; // sorted tokens summed by one warp
 constexpr int kAhead = 8;          // rows' loads a warp has in flight; pieces are multiples of it
-constexpr int kFewIds = 1024;      // so many tokens are ranked by one CTA instead of sorted
+constexpr int kFewIds = 4096;      // so many tokens are ranked by counting instead of sorted
+constexpr int kRanked = 128;       // tokens that a CTA ranks
 constexpr int kSumThreads = 128;
 
 // ------------------------------------------------------------------ lookup
@@ -122,7 +123,7 @@ struct SortParams {
     char *grad; // the dense gradient, for its zero rows
     uint64_t pitch, row_bytes;
     int elem;
-    uint32_t zero_ctas, rank; // embed_zero_kernel's CTAs that zero, and whether a further one ranks
+    uint32_t zero_ctas, rank_ctas; // embed_zero_kernel's CTAs that zero, and those before them that rank
 };
 
 __device__ __forceinline__ uint32_t row_key(const SortParams &p, uint64_t t)
@@ -152,35 +153,45 @@ __device__ __forceinline__ void warp_zero(char *q, uint64_t n, int elem, int lan
 }
 
 // A range of rows per CTA: the rows that tokens name marked from all the ids,
-// the others zeroed.  With p.rank a further CTA makes the sorted list of at most
-// kFewIds tokens.
+// the others zeroed.  The first p.rank_ctas CTAs make the sorted list of at
+// most kFewIds tokens.
 __global__ void __launch_bounds__(kZeroThreads, 2) embed_zero_kernel(const __grid_constant__ SortParams p)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); // the sort does not wait for the zeros
     constexpr uint32_t kBits = 65536;
     constexpr int kIds = 16;
     __shared__ uint32_t mark[kBits / 32];
-    __shared__ uint64_t pairs[kFewIds];
+    __shared__ uint32_t row[kFewIds];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (p.rank && blockIdx.x == p.zero_ctas) {
-        // a pair's place is the number of smaller pairs, (row, position) all distinct
+    if (blockIdx.x < p.rank_ctas) {
+        // a token's place is the number of tokens of smaller rows and of
+        // earlier ones of its own; four threads count for each, in segments of
+        // odd length so that they read different banks
         const uint32_t n = (uint32_t)p.ntokens;
-        for (uint32_t t = tid; t < n; t += kZeroThreads)
-            pairs[t] = (uint64_t)row_key(p, t) << 32 | t;
-        __syncthreads();
-        for (uint32_t t = tid; t < n; t += kZeroThreads) {
-            const uint64_t own = pairs[t];
-            uint32_t place = 0;
 #pragma unroll 8
-            for (uint32_t i = 0; i < n; ++i)
-                place += pairs[i] < own;
-            gstore<uint2>(p.buf[0] + place, make_uint2((uint32_t)(own >> 32), t));
-        }
+        for (uint32_t t = tid; t < n; t += kZeroThreads)
+            row[t] = row_key(p, t);
+        __syncthreads();
+        const uint32_t t = blockIdx.x * kRanked + tid / 4, seg = (n + 3) / 4 | 1;
+        const uint32_t lo = min(n, (tid & 3) * seg), hi = min(n, lo + seg);
+        const uint32_t own = t < n ? row[t] : 0, mid = max(lo, min(hi, t));
+        uint32_t place = 0;
+#pragma unroll 8
+        for (uint32_t i = lo; i < mid; ++i)
+            place += row[i] <= own;
+#pragma unroll 8
+        for (uint32_t i = mid; i < hi; ++i)
+            place += row[i] < own;
+        place += __shfl_xor_sync(0xffffffffu, place, 1);
+        place += __shfl_xor_sync(0xffffffffu, place, 2);
+        if (t < n && (tid & 3) == 0)
+            gstore<uint2>(p.buf[0] + place, make_uint2(own, t));
         return;
     }
+    const uint32_t zero_cta = blockIdx.x - p.rank_ctas;
     const uint32_t per = (p.rows + p.zero_ctas - 1) / p.zero_ctas;
-    const uint64_t end = umin64(p.rows, (uint64_t)(blockIdx.x + 1) * per);
-    for (uint64_t lo = (uint64_t)blockIdx.x * per; lo < end; lo += kBits) {
+    const uint64_t end = umin64(p.rows, (uint64_t)(zero_cta + 1) * per);
+    for (uint64_t lo = (uint64_t)zero_cta * per; lo < end; lo += kBits) {
         const uint32_t n = (uint32_t)umin64(kBits, end - lo);
         for (uint32_t i = tid; i < (n + 31) / 32; i += kZeroThreads)
             mark[i] = 0;
@@ -668,7 +679,7 @@ ccl_status_t embedding_grad_impl(const void *grad_out, size_t grad_out_stride, c
     s.elem = (int)es;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
-    s.rank = ntokens && ntokens <= kFewIds;
+    s.rank_ctas = ntokens <= kFewIds ? (uint32_t)((ntokens + kRanked - 1) / kRanked) : 0;
     if (!accumulate) {
         int sms = 0, dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -676,8 +687,8 @@ ccl_status_t embedding_grad_impl(const void *grad_out, size_t grad_out_stride, c
             return CCL_ERR_CUDA;
         s.zero_ctas = (uint32_t)std::min<size_t>(rows, 2 * (size_t)sms); // all resident
     }
-    if (s.zero_ctas + s.rank) {
-        cfg.gridDim = dim3(s.zero_ctas + s.rank);
+    if (s.zero_ctas + s.rank_ctas) {
+        cfg.gridDim = dim3(s.zero_ctas + s.rank_ctas);
         cfg.blockDim = dim3(kZeroThreads);
         if (cudaError_t e = cudaLaunchKernelEx(&cfg, embed_zero_kernel, s))
             return from_cuda(e);
@@ -685,7 +696,7 @@ ccl_status_t embedding_grad_impl(const void *grad_out, size_t grad_out_stride, c
     }
     if (ntokens == 0)
         return CCL_OK;
-    if (!s.rank) {
+    if (!s.rank_ctas) {
         cfg.gridDim = dim3(kSortCtas);
         cfg.blockDim = dim3(kSortThreads);
         cudaLaunchAttribute attr[2];
@@ -701,7 +712,7 @@ ccl_status_t embedding_grad_impl(const void *grad_out, size_t grad_out_stride, c
         count_launches(1);
     }
     SumParams p{};
-    p.sorted = s.buf[s.rank ? 0 : (s.passes - 1) & 1];
+    p.sorted = s.buf[s.rank_ctas ? 0 : (s.passes - 1) & 1];
     p.ntokens = ntokens;
     p.dim = dim;
     p.dim_pad = (dim + 3) / 4 * 4;

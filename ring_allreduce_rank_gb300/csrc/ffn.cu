@@ -48,7 +48,14 @@ constexpr int kOperandBytes = 128 * kTileK * 2;        // one CTA's part of A or
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kStages = 6;
 constexpr int kMaxStages = 6; // ffn_few_kernel's
-constexpr int kFewTokens = 256;
+// Products that ffn_few_kernel takes: few tokens.  Forward in us, this kernel
+// against CTA pairs' 256-row tiles: 488 x 2584 with 48 tokens 16.8 against 17.3,
+// with 64 equal, with 128 22.0 against 19.7; 4096 x 11008 with 64 tokens 61
+// against 73, with 128 69 against 79, with 198 84 against 82.  Backward to the
+// inputs, 1000 x 3000: with 64 tokens 19.5 against 31.4, with 128 24.4 against
+// 34.4, with 198 54.5 against 34.5.
+constexpr uint64_t kFewTokens = 64, kFewTokensMost = 128; // the latter for many weights, and backward
+constexpr uint64_t kManyWeights = 1 << 24;
 constexpr int kFewBytes = 200 * 1024; // its stages', at most
 constexpr int kGemmThreads = 384; // producer, issuer, tensor memory, one idle warp, eight epilogue warps
 constexpr int kEpiWarps = 8;
@@ -89,7 +96,6 @@ struct FewParams {
     GemmParams p;
     uint32_t npad;   // tokens, rounded up to 16
     uint32_t stages; // of 32 KiB of weights and npad * 128 bytes of activations
-    uint32_t bufs;   // accumulators in turn: 2, or 1 for more than 128 tokens
 };
 
 __device__ unsigned long long g_ffn_timeouts;
@@ -703,7 +709,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
 
 // ------------------------------------------------------------------ few tokens
 
-// The same products for at most 256 tokens, with the weights as the
+// The same products for at most 128 tokens, with the weights as the
 // accumulator's rows and the tokens as its columns, so that the tensor cores
 // work on the tokens there are and not on a 256-row tile of them: one CTA a
 // unit of two 128-row blocks of weights (EPI_GATED: the same rows of Wg and
@@ -809,8 +815,8 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
         bool ok = true;
         for (uint32_t i = blockIdx.x; ok && i < q.units; i += gridDim.x, ++t) {
             const Unit u = unit_at(p, i);
-            const uint32_t buf = t % fp.bufs, round = t / fp.bufs;
-            if (!(ok = mbar_wait(acc_empty + 8 * buf, (round & 1) ^ 1, &gave_up)))
+            const uint32_t buf = t & 1;
+            if (!(ok = mbar_wait(acc_empty + 8 * buf, ((t >> 1) & 1) ^ 1, &gave_up)))
                 break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             for (uint32_t kb = u.kb0; kb < u.kb1; ++kb) {
@@ -843,8 +849,8 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
         uint32_t t = 0;
         for (uint32_t i = blockIdx.x; i < q.units; i += gridDim.x, ++t) {
             const Unit u = unit_at(p, i);
-            const uint32_t buf = t % fp.bufs, round = t / fp.bufs;
-            if (!__all_sync(0xffffffffu, mbar_wait(acc_full + 8 * buf, round & 1, &gave_up)))
+            const uint32_t buf = t & 1;
+            if (!__all_sync(0xffffffffu, mbar_wait(acc_full + 8 * buf, (t >> 1) & 1, &gave_up)))
                 break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tmem + buf * 2 * fp.npad + (lanes << 16);
@@ -1093,12 +1099,13 @@ bool make_plan(size_t t, size_t d, size_t f, bool backward, bool aligned, FfnPla
     p->f = f;
     p->dp = (d + 7) / 8 * 8;
     p->fp = (f + 15) / 16 * 16; // h, dg and du in rows of whole 32-byte vectors
-    const bool pd = p->dp != d || !aligned, pf = f % 8 || !aligned, few = t <= kFewTokens,
+    const bool pd = p->dp != d || !aligned, pf = f % 8 || !aligned, few = t <= kFewTokens || (t <= kFewTokensMost && (uint64_t)d * f >= kManyWeights),
+               few_b = t <= kFewTokensMost,
                od = d % 8 != 0, of = f % 8 != 0;
     p->up_ = Launch{{{t, f, d, 1}}, 1, true, few, of, 1, 0};
     p->down = Launch{{{t, d, f, 1}}, 1, false, few, od, 1, 0};
-    p->dh = Launch{{{t, f, d, 1}}, 1, false, few, of, 1, 0};
-    p->dx = Launch{{{t, d, f, 2}}, 1, false, few, od, 1, 0};
+    p->dh = Launch{{{t, f, d, 1}}, 1, false, few_b, of, 1, 0};
+    p->dx = Launch{{{t, d, f, 2}}, 1, false, few_b, od, 1, 0};
     p->dw = Launch{{{f, d, t, 1}, {f, d, t, 1}, {d, f, t, 1}}, 3, false, false, od || of, 1, 0};
     size_t at = 0, partial = 0;
     auto take = [&](size_t n) {
@@ -1239,7 +1246,6 @@ ccl_status_t launch_few(GemmParams &p, const Launch &l, const Matrix *w, const M
     FewParams fp;
     fp.npad = (uint32_t)(l.s[0].m + 15) / 16 * 16;
     fp.stages = std::min<uint32_t>(kMaxStages, kFewBytes / (2 * kOperandBytes + fp.npad * 128));
-    fp.bufs = fp.npad > 128 ? 1 : 2;
     uint64_t units;
     cudaError_t e = set_problems(p, l, partial, &units);
     static std::atomic<unsigned long long> ready{0};
