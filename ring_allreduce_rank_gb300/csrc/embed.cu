@@ -158,30 +158,50 @@ __device__ __forceinline__ void warp_zero(char *q, uint64_t n, int elem, int lan
 __global__ void __launch_bounds__(kZeroThreads, 2) embed_zero_kernel(const __grid_constant__ SortParams p)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); // the sort does not wait for the zeros
-    constexpr uint32_t kBits = 65536;
+    constexpr uint32_t kRows = 16384; // marked at a time
     constexpr int kIds = 16;
-    __shared__ uint32_t mark[kBits / 32];
-    __shared__ uint32_t row[kFewIds];
+    // a byte a row, set by plain stores of one value: an atomic per token of a
+    // frequent row took longer than the zeros
+    __shared__ uint32_t mark_words[kRows / 4];
+    uint8_t *mark = reinterpret_cast<uint8_t *>(mark_words);
+    __shared__ uint4 row4[kFewIds / 4]; // rows of the tokens
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (blockIdx.x < p.rank_ctas) {
         // a token's place is the number of tokens of smaller rows and of
         // earlier ones of its own; four threads count for each, in segments of
-        // odd length so that they read different banks
-        const uint32_t n = (uint32_t)p.ntokens;
-#pragma unroll 8
-        for (uint32_t t = tid; t < n; t += kZeroThreads)
-            row[t] = row_key(p, t);
+        // an odd number of vectors so that they read different banks
+        uint32_t *row = reinterpret_cast<uint32_t *>(row4);
+        const uint32_t n = (uint32_t)p.ntokens, n4 = (n + 3) / 4, seg = (n4 + 3) / 4 | 1;
+        uint32_t key[kFewIds / kZeroThreads]; // all the loads in flight
+#pragma unroll
+        for (int j = 0; j < kFewIds / kZeroThreads; ++j)
+            key[j] = tid + j * kZeroThreads < n ? row_key(p, tid + j * kZeroThreads) : 0xffffffffu;
+#pragma unroll
+        for (int j = 0; j < kFewIds / kZeroThreads; ++j)
+            row[tid + j * kZeroThreads] = key[j]; // past the end: larger than any row
         __syncthreads();
-        const uint32_t t = blockIdx.x * kRanked + tid / 4, seg = (n + 3) / 4 | 1;
-        const uint32_t lo = min(n, (tid & 3) * seg), hi = min(n, lo + seg);
-        const uint32_t own = t < n ? row[t] : 0, mid = max(lo, min(hi, t));
+        const uint32_t t = blockIdx.x * kRanked + tid / 4;
+        const uint32_t lo = min(n4, (tid & 3) * seg), hi = min(n4, lo + seg);
+        const uint32_t own = t < n ? row[t] : 0;
         uint32_t place = 0;
+        // all lanes walk the segment in step: before the warp's tokens (<=), the
+        // vectors around them (both), after them (<)
+        const uint32_t first4 = (t & ~7u) / 4, last4 = first4 + 2; // a warp's eight tokens
+        uint32_t v = lo;
+        const uint32_t a = max(lo, min(hi, first4)), b = max(lo, min(hi, last4));
 #pragma unroll 8
-        for (uint32_t i = lo; i < mid; ++i)
-            place += row[i] <= own;
+        for (; v < a; ++v) {
+            const uint4 r = row4[v];
+            place += (r.x <= own) + (r.y <= own) + (r.z <= own) + (r.w <= own);
+        }
+        for (; v < b; ++v)
+            for (uint32_t i = 4 * v; i < 4 * v + 4; ++i)
+                place += row[i] < own || (row[i] == own && i < t);
 #pragma unroll 8
-        for (uint32_t i = mid; i < hi; ++i)
-            place += row[i] < own;
+        for (; v < hi; ++v) {
+            const uint4 r = row4[v];
+            place += (r.x < own) + (r.y < own) + (r.z < own) + (r.w < own);
+        }
         place += __shfl_xor_sync(0xffffffffu, place, 1);
         place += __shfl_xor_sync(0xffffffffu, place, 2);
         if (t < n && (tid & 3) == 0)
@@ -191,10 +211,10 @@ __global__ void __launch_bounds__(kZeroThreads, 2) embed_zero_kernel(const __gri
     const uint32_t zero_cta = blockIdx.x - p.rank_ctas;
     const uint32_t per = (p.rows + p.zero_ctas - 1) / p.zero_ctas;
     const uint64_t end = umin64(p.rows, (uint64_t)(zero_cta + 1) * per);
-    for (uint64_t lo = (uint64_t)zero_cta * per; lo < end; lo += kBits) {
-        const uint32_t n = (uint32_t)umin64(kBits, end - lo);
-        for (uint32_t i = tid; i < (n + 31) / 32; i += kZeroThreads)
-            mark[i] = 0;
+    for (uint64_t lo = (uint64_t)zero_cta * per; lo < end; lo += kRows) {
+        const uint32_t n = (uint32_t)umin64(kRows, end - lo);
+        for (uint32_t i = tid; i < (n + 3) / 4; i += kZeroThreads)
+            mark_words[i] = 0;
         __syncthreads();
         for (uint64_t t0 = tid; t0 < p.ntokens; t0 += kIds * kZeroThreads) {
             uint32_t key[kIds]; // as many loads in flight
@@ -205,12 +225,12 @@ __global__ void __launch_bounds__(kZeroThreads, 2) embed_zero_kernel(const __gri
             for (int j = 0; j < kIds; ++j) {
                 const uint64_t r = (uint64_t)key[j] - lo;
                 if (r < n)
-                    atomicOr(&mark[r >> 5], 1u << (r & 31));
+                    mark[r] = 1;
             }
         }
         __syncthreads();
         for (uint32_t r = warp; r < n; r += kZeroThreads / 32)
-            if (!(mark[r >> 5] >> (r & 31) & 1))
+            if (!mark[r])
                 warp_zero(p.grad + (lo + r) * p.pitch, p.row_bytes, p.elem, lane);
         __syncthreads();
     }
