@@ -147,6 +147,32 @@ def test_gradient_accumulates_in_place_and_keeps_what_is_between(d, stride, lead
     assert torch.equal(whole, before)
 
 
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("kind", ["uniform", "one"])
+@pytest.mark.parametrize("n", [127, 128, 129, 4095, 4096, 4097])
+def test_gradient_where_ranking_by_counting_ends(n, kind, accumulate):
+    rng = np.random.default_rng(n)
+    rows, d = 700, 12
+    dy, dy64, _ = _matrix(rng, n, d, torch.float32)
+    grad, old64, _ = _matrix(rng, rows, d, torch.float32)
+    ids = _ids(rng, n, rows, kind).to(DEV)
+    ccl.ccl_embedding_grad(dy, ids, grad, scale=0.75, accumulate=accumulate)
+    _check_grad(dy64, ids, 0, rows, 0.75, grad, old64 if accumulate else None, torch.float32)
+
+
+@pytest.mark.parametrize("n", [500, 5000])
+def test_gradient_of_more_rows_than_are_marked_at_a_time(n):
+    # 16384 rows a CTA and two CTAs an SM at a time; here each marks a second range
+    rows = 2 * torch.cuda.get_device_properties(0).multi_processor_count * 16500 + 7
+    rng = np.random.default_rng(n)
+    dy, dy64, _ = _matrix(rng, n, 2, torch.float32)
+    ids = _ids(rng, n, rows, "uniform").to(DEV)
+    grad = torch.full((rows, 2), 3.0, device=DEV)
+    ccl.ccl_embedding_grad(dy, ids, grad)
+    cnt = _check_grad(dy64, ids, 0, rows, 1.0, grad, None, torch.float32)
+    assert bool((grad.cpu()[cnt == 0] == 0).all())
+
+
 def test_no_tokens_and_no_rows():
     grad = torch.full((5, 8), 2.0, device=DEV)
     none = torch.empty(0, dtype=torch.int64, device=DEV)

@@ -108,6 +108,14 @@ def test_few_tokens_without_saving(T):
     check({"out": out}, {"out": reference(*args, "silu")["out"]})
 
 
+# either side of each product's choice of tile: 64 and 128 tokens, 2^24 weights
+@pytest.mark.parametrize("T,D,F", [(64, 260, 520), (65, 260, 520), (128, 260, 520), (129, 260, 520), (64, 2048, 8192), (65, 2048, 8191),
+                                   (65, 2048, 8192), (128, 2048, 8192), (129, 2048, 8192)])
+def test_forward_and_backward_where_the_tile_changes(T, D, F):
+    args = inputs(T, D, F, T + D + F)
+    check(forward_backward(*args, "silu"), reference(*args, "silu"))
+
+
 @pytest.mark.parametrize("lead", [1, 4])
 def test_buffers_with_their_elements_alignment_only(lead):
     args = inputs(70, 96, 136, lead, lead)
