@@ -541,15 +541,27 @@ def _on_gpu(*ts: Optional[torch.Tensor]) -> int:
     return dev
 
 
-# the current stream's handle without a Stream object around it, which costs
-# more than a small kernel's launch
+# the current device and the current stream's handle without the objects and
+# checks around them, which cost more than a small kernel's launch
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_on(stream, device: int):
     if stream is None and _raw_stream is not None:
         return _raw_stream(device)
     return _stream(stream)
+
+
+def _launch(name: str, device: int, stream, *args) -> None:
+    """Calls an operator's entry, which launches on the current device, with
+    the tensors' device current and on that device's stream."""
+    entry = getattr(lib(), name)
+    if _current_device() == device:
+        _check(entry(*args, _stream_on(stream, device)), name)
+    else:
+        with torch.cuda.device(device):
+            _check(entry(*args, _stream_on(stream, device)), name)
 
 
 def _work(work: Optional[torch.Tensor], nbytes: int, like: torch.Tensor, stream):
@@ -560,7 +572,7 @@ def _work(work: Optional[torch.Tensor], nbytes: int, like: torch.Tensor, stream)
             stream = torch.cuda.ExternalStream(int(stream), device=like.device)
         with torch.cuda.stream(stream):
             work = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    elif not work.is_cuda or not work.is_contiguous():
+    elif not work.is_contiguous():
         raise ValueError("work must be a contiguous CUDA tensor")
     return work, work.numel() * work.element_size()
 
@@ -573,8 +585,8 @@ def ccl_embedding(table: torch.Tensor, ids: torch.Tensor, out: torch.Tensor, sca
     tp, rows, dim, ts = _rows(table, "table")
     op, n, _, os_ = _rows(out, "out", dim, table.dtype)
     ip = _flat(ids, "ids", (n,), torch.int64)
-    _check(lib().ccl_embedding(tp, rows, dim, ts, _dtype(table), ip, n, int(first_row), float(scale), op, os_,
-                               _stream_on(stream, dev)), "ccl_embedding")
+    _launch("ccl_embedding", dev, stream, tp, rows, dim, ts, _dtype(table), ip, n, int(first_row), float(scale), op,
+            os_)
 
 
 def ccl_embedding_grad(grad_out: torch.Tensor, ids: torch.Tensor, grad_table: torch.Tensor, scale: float = 1.0,
@@ -583,15 +595,14 @@ def ccl_embedding_grad(grad_out: torch.Tensor, ids: torch.Tensor, grad_table: to
     """grad_table[v] = [grad_table[v] +] scale * the sum of grad_out[t] over
     the tokens with ids[t] == first_row + v.  work: a device buffer of at least
     ccl_plan_embedding_grad_work_bytes bytes (allocated here when omitted)."""
-    dev = _on_gpu(grad_out, ids, grad_table)
+    dev = _on_gpu(grad_out, ids, grad_table, work)
     gp, n, dim, gs = _rows(grad_out, "grad_out")
     tp, rows, _, ts = _rows(grad_table, "grad_table", dim, grad_out.dtype)
     ip = _flat(ids, "ids", (n,), torch.int64)
     work, nbytes = _work(work, 0 if work is not None else ccl_plan_embedding_grad_work_bytes(n, rows, dim), grad_out,
                          stream)
-    _check(lib().ccl_embedding_grad(gp, gs, ip, n, int(first_row), rows, dim, _dtype(grad_out), float(scale),
-                                    int(bool(accumulate)), tp, ts, work.data_ptr(), nbytes, _stream_on(stream, dev)),
-           "ccl_embedding_grad")
+    _launch("ccl_embedding_grad", dev, stream, gp, gs, ip, n, int(first_row), rows, dim, _dtype(grad_out),
+            float(scale), int(bool(accumulate)), tp, ts, work.data_ptr(), nbytes)
 
 
 def ccl_plan_embedding_grad_work_bytes(ntokens: int, rows: int, dim: int) -> int:
@@ -622,14 +633,13 @@ def ccl_gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_d
     [ffn, dim], w_down [dim, ffn].  saved ([2, tokens, ffn], float32): kept for
     ccl_gated_ffn_grad.  work: a device buffer of at least
     ccl_plan_gated_ffn_work_bytes bytes (allocated here when omitted)."""
-    dev = _on_gpu(x, w_gate, w_up, w_down, out, saved)
+    dev = _on_gpu(x, w_gate, w_up, w_down, out, saved, work)
     ptrs, (n, dim, ffn) = _ffn_shapes(x, w_gate, w_up, w_down)
     op = _flat(out, "out", (n, dim), x.dtype)
     sp = _flat(saved, "saved", (2, n, ffn), torch.float32)
     work, nbytes = _work(work, 0 if work is not None else
                          ccl_plan_gated_ffn_work_bytes(n, dim, ffn, False, all(q % 16 == 0 for q in ptrs)), x, stream)
-    _check(lib().ccl_gated_ffn(*ptrs, n, dim, ffn, _dtype(x), _act(act), op, sp, work.data_ptr(), nbytes,
-                               _stream_on(stream, dev)), "ccl_gated_ffn")
+    _launch("ccl_gated_ffn", dev, stream, *ptrs, n, dim, ffn, _dtype(x), _act(act), op, sp, work.data_ptr(), nbytes)
 
 
 def ccl_gated_ffn_grad(grad_out: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
@@ -639,7 +649,7 @@ def ccl_gated_ffn_grad(grad_out: torch.Tensor, x: torch.Tensor, w_gate: torch.Te
                        work: Optional[torch.Tensor] = None, stream=None) -> None:
     """The block's gradients (those given), from the saved pre-activations;
     accumulate adds to the weights' gradients."""
-    dev = _on_gpu(grad_out, x, w_gate, w_up, w_down, saved, grad_x, grad_w_gate, grad_w_up, grad_w_down)
+    dev = _on_gpu(grad_out, x, w_gate, w_up, w_down, saved, grad_x, grad_w_gate, grad_w_up, grad_w_down, work)
     ptrs, (n, dim, ffn) = _ffn_shapes(x, w_gate, w_up, w_down)
     dt = x.dtype
     yp = _flat(grad_out, "grad_out", (n, dim), dt)
@@ -649,8 +659,8 @@ def ccl_gated_ffn_grad(grad_out: torch.Tensor, x: torch.Tensor, w_gate: torch.Te
     work, nbytes = _work(work, 0 if work is not None else
                          ccl_plan_gated_ffn_work_bytes(n, dim, ffn, True, all(q % 16 == 0 for q in (yp, *ptrs))), x,
                          stream)
-    _check(lib().ccl_gated_ffn_grad(yp, *ptrs, sp, n, dim, ffn, _dtype(x), _act(act), int(bool(accumulate)), *grads,
-                                    work.data_ptr(), nbytes, _stream_on(stream, dev)), "ccl_gated_ffn_grad")
+    _launch("ccl_gated_ffn_grad", dev, stream, yp, *ptrs, sp, n, dim, ffn, _dtype(x), _act(act),
+            int(bool(accumulate)), *grads, work.data_ptr(), nbytes)
 
 
 def ccl_plan_gated_ffn_work_bytes(ntokens: int, dim: int, ffn: int, backward: bool = False, aligned: bool = True) -> int:
@@ -682,11 +692,11 @@ def ccl_distill_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_lo
         if gn != n:
             raise ValueError("grad has %d rows, expected %d" % (gn, n))
     top = teacher_ids.shape[-1]
-    _check(lib().ccl_distill_loss(lp, n, vocab, ls, _dtype(logits), _flat(teacher_ids, "teacher_ids", (n, top), torch.int64),
-                                  _flat(teacher_logits, "teacher_logits", (n, top), torch.float32), top,
-                                  float(temperature), _flat(weights, "weights", (n,), torch.float32),
-                                  _flat(loss, "loss", (n,), torch.float32), _flat(stats, "stats", (n, 2), torch.float32),
-                                  gp, gs, _stream_on(stream, dev)), "ccl_distill_loss")
+    _launch("ccl_distill_loss", dev, stream, lp, n, vocab, ls, _dtype(logits),
+            _flat(teacher_ids, "teacher_ids", (n, top), torch.int64),
+            _flat(teacher_logits, "teacher_logits", (n, top), torch.float32), top, float(temperature),
+            _flat(weights, "weights", (n,), torch.float32), _flat(loss, "loss", (n,), torch.float32),
+            _flat(stats, "stats", (n, 2), torch.float32), gp, gs)
 
 
 def ccl_distill_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
@@ -700,11 +710,10 @@ def ccl_distill_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_lo
     if gn != n:
         raise ValueError("grad has %d rows, expected %d" % (gn, n))
     top = teacher_ids.shape[-1]
-    _check(lib().ccl_distill_grad(lp, n, vocab, ls, _dtype(logits), _flat(teacher_ids, "teacher_ids", (n, top), torch.int64),
-                                  _flat(teacher_logits, "teacher_logits", (n, top), torch.float32), top,
-                                  float(temperature), _flat(weights, "weights", (n,), torch.float32),
-                                  _flat(stats, "stats", (n, 2), torch.float32), gp, gs, _stream_on(stream, dev)),
-           "ccl_distill_grad")
+    _launch("ccl_distill_grad", dev, stream, lp, n, vocab, ls, _dtype(logits),
+            _flat(teacher_ids, "teacher_ids", (n, top), torch.int64),
+            _flat(teacher_logits, "teacher_logits", (n, top), torch.float32), top, float(temperature),
+            _flat(weights, "weights", (n,), torch.float32), _flat(stats, "stats", (n, 2), torch.float32), gp, gs)
 
 
 # ------------------------------------------------------------------ planner
