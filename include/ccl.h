@@ -433,8 +433,8 @@ ccl_status_t ccl_allreduce_host(const void *const *send, void *const *recv, int 
  * which sets its kernels up).  Sums are held in fp32 and each output is
  * rounded once to its type.  Strides are in elements, from one row to the
  * next, and at least the row's length; buffers need only their element's
- * alignment (16-byte aligned rows of whole 16-byte vectors run at full
- * bandwidth).  No value is added by an atomic: the same inputs give the same
+ * alignment (without it: CCL_ERR_INVALID_ARG; 16-byte aligned rows of whole
+ * 16-byte vectors run at full bandwidth).  No value is added by an atomic: the same inputs give the same
  * bits. */
 
 /* Embedding lookup: out[t] = round(scale * table[ids[t] - first_row]), t <

@@ -593,7 +593,9 @@ ccl_status_t distill_impl(int mode, const DistillArgs &a, cudaStream_t stream)
     if (a.nrows == 0)
         return CCL_OK;
     if ((a.vocab && !a.logits) || (a.top && (!a.ids || !a.teacher)) || (mode != DISTILL_GRAD && !a.loss) ||
-        (mode == DISTILL_GRAD && !a.stats) || (mode != DISTILL_LOSS && a.vocab && !a.grad))
+        (mode == DISTILL_GRAD && !a.stats) || (mode != DISTILL_LOSS && a.vocab && !a.grad) ||
+        !element_aligned(es, {a.logits, a.grad}) || !element_aligned(8, {a.ids}) ||
+        !element_aligned(4, {a.teacher, a.weights, a.loss, a.stats}))
         return CCL_ERR_INVALID_ARG;
     // in place: the gradient may take the logits' place, row by row
     const bool in_place = a.grad == a.logits && a.grad_stride == a.stride;

@@ -611,7 +611,7 @@ ccl_status_t embedding_impl(const void *table, size_t rows, size_t dim, size_t t
         return CCL_ERR_INVALID_ARG;
     if (ntokens == 0 || dim == 0)
         return CCL_OK;
-    if ((!table && rows) || !ids || !out)
+    if ((!table && rows) || !ids || !out || !element_aligned(es, {table, out}) || !element_aligned(8, {ids}))
         return CCL_ERR_INVALID_ARG;
     const std::vector<Range> w{range_of(out, ob, 0)}, r{range_of(table, tb, 0), range_of(ids, ntokens * 8, 0)};
     if (ccl_status_t st = check_overlaps(w, r, [](const Range &, const Range &) { return false; }))
@@ -668,6 +668,8 @@ ccl_status_t embedding_grad_impl(const void *grad_out, size_t grad_out_stride, c
     if (rows == 0 || dim == 0 || (ntokens == 0 && accumulate))
         return CCL_OK;
     if (!grad_table || (ntokens && (!grad_out || !ids || !work || (uintptr_t)work % 16 || work_bytes < gw.bytes)))
+        return CCL_ERR_INVALID_ARG;
+    if (!element_aligned(es, {grad_out, grad_table}) || !element_aligned(8, {ids}))
         return CCL_ERR_INVALID_ARG;
     std::vector<Range> w{range_of(grad_table, gb, 0)}, r;
     if (ntokens) {

@@ -1320,7 +1320,8 @@ ccl_status_t gated_ffn_impl(const FfnArgs &a, void *out, cudaStream_t stream)
         return st;
     if (a.t == 0 || a.d == 0)
         return CCL_OK;
-    if (!a.x || !out || (a.f && (!a.wg || !a.wu || !a.wd)) || (a.saved && (uintptr_t)a.saved % 4))
+    if (!a.x || !out || (a.f && (!a.wg || !a.wu || !a.wd)) || !element_aligned(2, {a.x, a.wg, a.wu, a.wd, out}) ||
+        !element_aligned(4, {a.saved}))
         return CCL_ERR_INVALID_ARG;
     if (a.f == 0)
         return from_cuda(cudaMemsetAsync(out, 0, a.t * a.d * 2, stream));
@@ -1377,7 +1378,8 @@ ccl_status_t gated_ffn_grad_impl(const FfnArgs &a, const void *dy, void *dx, voi
     if (a.d == 0 || (a.t == 0 && accumulate))
         return CCL_OK;
     const size_t tb = a.t * a.d * 2, wb = a.f * a.d * 2;
-    if ((a.t && (!a.x || !dy || (a.f && (!a.wg || !a.wu || !a.wd || !a.saved)))) || (uintptr_t)a.saved % 4)
+    if ((a.t && (!a.x || !dy || (a.f && (!a.wg || !a.wu || !a.wd || !a.saved)))) ||
+        !element_aligned(2, {a.x, a.wg, a.wu, a.wd, dy, dx, dwg, dwu, dwd}) || !element_aligned(4, {a.saved}))
         return CCL_ERR_INVALID_ARG;
     const bool empty = a.t == 0 || a.f == 0;
     if (!empty && (!a.work || (uintptr_t)a.work % 256 || a.work_bytes < pl.bytes))

@@ -4,6 +4,7 @@
 #pragma once
 
 #include <atomic>
+#include <initializer_list>
 #include <new>
 
 #include "ccl_internal.h"
@@ -111,6 +112,16 @@ inline cudaError_t large_smem_once(const void *kernel, int bytes, std::atomic<un
 
 constexpr size_t kAlign = 256;
 inline size_t up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
+
+// Whether every pointer is a multiple of `size` bytes (NULL is): the kernels
+// read elements with loads of their own size, which fault elsewhere.
+inline bool element_aligned(size_t size, std::initializer_list<const void *> ps)
+{
+    for (const void *p : ps)
+        if ((uintptr_t)p % size)
+            return false;
+    return true;
+}
 
 // Bytes from the first to past the last of n rows of `dim` elements, `stride`
 // apart; false where that overflows.
