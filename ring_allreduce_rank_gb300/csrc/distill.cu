@@ -454,8 +454,8 @@ __global__ void __launch_bounds__(kDThreads + 32, MODE == DISTILL_FUSED ? kDCtas
                     }
             }
             sum = warp_reduce<false>(sum);
-            if (lane == 0)
-                gstore<float>(p.loss + t, w == 0.0f ? 0.0f : __fmul_rn(w, sum));
+            if (lane == 0) // without a teacher 0 whatever the weight is
+                gstore<float>(p.loss + t, w == 0.0f || !(tm > -INFINITY) ? 0.0f : __fmul_rn(w, sum));
         }
     }
 
