@@ -63,7 +63,8 @@ class Rank:
 
 def train(ranks: int = 4, steps: int = 20, tokens: int = 256, vocab: int = 4000, dim: int = 256, ffn: int = 704, top: int = 16,
           temperature: float = 1.0, rate: float = 0.5, device="cuda:0"):
-    """The mean loss of every step; raises if the ranks' weights ever differ."""
+    """The mean loss of every step; raises if the ranks' weights ever differ,
+    or if a kernel gave up waiting (its results are then NaN)."""
     torch.cuda.set_device(device)
     world = [Rank(tokens, vocab, dim, ffn, device) for _ in range(ranks)]
     gen = torch.Generator(device=device).manual_seed(1)
@@ -84,6 +85,8 @@ def train(ranks: int = 4, steps: int = 20, tokens: int = 256, vocab: int = 4000,
                 w.sub_(g, alpha=rate)
         for k in range(4):
             ccl.ccl_check_identical([r.weights[k] for r in world], mismatches)
+    if ccl.ccl_gated_ffn_timeouts():
+        raise RuntimeError("a feed-forward kernel gave up waiting %d times" % ccl.ccl_gated_ffn_timeouts())
     if mismatches.item():
         raise RuntimeError("%d weights differ between ranks" % mismatches.item())
     return [v.item() for v in losses]

@@ -497,10 +497,15 @@ ccl_status_t ccl_gated_ffn_grad(const void *grad_out, const void *x, const void 
  * enough for ccl_gated_ffn of the same sizes. */
 ccl_status_t ccl_plan_gated_ffn_work_bytes(size_t ntokens, size_t dim, size_t ffn, int backward, int aligned, size_t *bytes);
 
-/* How often a gated feed-forward kernel on the current device gave up waiting
- * for its own copies or products (after 4 s; its results are then missing):
- * 0 on a sound machine.  Waits for the device. */
+/* How often a wait of a gated feed-forward kernel on the current device for
+ * its own copies or products ran out: 0 on a sound machine.  What such a kernel
+ * could not compute it writes as NaN, and so is every output that depends on
+ * it.  Waits for the device. */
 ccl_status_t ccl_gated_ffn_timeouts(unsigned long long *count);
+/* The longest such wait, in ns, of calls made from now on (4 s by default).  0
+ * gives up at once, without a copy or product that another one waits for: every
+ * output is NaN, so that a program can try what it does then. */
+ccl_status_t ccl_set_gated_ffn_wait_limit(unsigned long long ns);
 
 /* Distillation loss from a teacher's top logits.  Row t's teacher
  * distribution p is the softmax of teacher_logits[t][0..top) / temperature

@@ -95,6 +95,7 @@ def lib() -> ctypes.CDLL:
                 "ccl_gated_ffn": [vp, vp, vp, vp, sz, sz, sz, i32, i32, vp, vp, vp, sz, vp],
                 "ccl_gated_ffn_grad": [vp, vp, vp, vp, vp, vp, sz, sz, sz, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp],
                 "ccl_plan_gated_ffn_work_bytes": [sz, sz, sz, i32, i32, psz],
+                "ccl_set_gated_ffn_wait_limit": [ctypes.c_ulonglong],
                 "ccl_gated_ffn_timeouts": [ctypes.POINTER(ctypes.c_ulonglong)],
                 "ccl_distill_loss": [vp, sz, sz, sz, i32, vp, vp, sz, f32, vp, vp, vp, vp, sz, vp],
                 "ccl_distill_grad": [vp, sz, sz, sz, i32, vp, vp, sz, f32, vp, vp, vp, sz, vp],
@@ -671,10 +672,16 @@ def ccl_plan_gated_ffn_work_bytes(ntokens: int, dim: int, ffn: int, backward: bo
 
 
 def ccl_gated_ffn_timeouts() -> int:
-    """Kernels of the block that gave up waiting (0 on a sound machine); waits for the device."""
+    """The block's waits that ran out (0 on a sound machine); what they left
+    uncomputed is NaN.  Waits for the device."""
     n = ctypes.c_ulonglong()
     _check(lib().ccl_gated_ffn_timeouts(ctypes.byref(n)), "ccl_gated_ffn_timeouts")
     return int(n.value)
+
+
+def ccl_set_gated_ffn_wait_limit(ns: int) -> None:
+    """The longest wait within the block's kernels, in ns, from now on (0: they give up at once)."""
+    _check(lib().ccl_set_gated_ffn_wait_limit(int(ns)), "ccl_set_gated_ffn_wait_limit")
 
 
 def ccl_distill_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, loss: torch.Tensor,

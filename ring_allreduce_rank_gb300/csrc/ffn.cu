@@ -63,7 +63,7 @@ constexpr int kTurnFloats = 32 * 33; // an epilogue warp's 32 x 32 values, rows 
 constexpr int kGemmSmem = kStages * kStageBytes + 1024 /* alignment */ + kEpiWarps * kTurnFloats * 4;
 constexpr int kGroupM = 8; // row tiles walked before the next column tile
 constexpr int kMaxProblems = 3;
-constexpr unsigned long long kWaitLimitNs = 4000000000ull;
+std::atomic<unsigned long long> g_wait_ns{4000000000ull}; // the bounded waits' limit, for calls made from now on
 
 enum Epilogue { EPI_GATED = 0, EPI_STORE = 1, EPI_BACKWARD = 2 };
 
@@ -89,6 +89,7 @@ struct GemmParams {
     uint32_t ldh; // row stride of h, dg and du (g and u: n)
     int vectors;  // every row that the epilogue touches is 16-byte aligned (fp32: 32) and whole vectors of 8 columns
     int early;    // the weights may be read before the kernel before this one has ended
+    unsigned long long wait_ns; // how long a role waits for another; 0: no role begins
 };
 
 // ffn_few_kernel's: the same products with the weights as rows.
@@ -147,8 +148,8 @@ __device__ __forceinline__ unsigned long long now_ns()
 }
 
 // Waits for the phase of the given parity; false (and the CTA's flag set, and
-// the device's counter raised) after kWaitLimitNs, or once another role gave up.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up)
+// the device's counter raised) after `limit` ns, or once another role gave up.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up, unsigned long long limit)
 {
     unsigned long long t0 = 0;
     for (uint32_t n = 0;; ++n) {
@@ -167,7 +168,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
             const unsigned long long t = now_ns();
             if (!t0) {
                 t0 = t;
-            } else if (t - t0 > kWaitLimitNs) {
+            } else if (t - t0 > limit) {
                 *gave_up = 1;
                 atomicAdd(&g_ffn_timeouts, 1ull);
                 return false;
@@ -365,6 +366,17 @@ __device__ __forceinline__ void finish1(const GemmParams &p, const Problem &q, u
     }
 }
 
+// The result of one column of one row whose products never came, as NaN: a
+// kernel that gave up leaves nothing that could pass for a result.
+template <int EPI> __device__ __forceinline__ void finish_nan(const GemmParams &p, const Problem &q, uint32_t row, uint32_t col)
+{
+    const float nan = __uint_as_float(0x7fffffffu);
+    const uint64_t at = (uint64_t)row * q.n + col;
+    Ahead1<EPI> old;
+    old.load(p, q, at, true);
+    finish1<EPI>(p, q, at, (uint64_t)row * p.ldh + col, old, nan, nan);
+}
+
 // Sixteen values of one row, eight at a time: `both` says whether the second
 // eight are columns of the matrix.
 struct Vals16 {
@@ -519,7 +531,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
             mbar_init(acc_full + 8 * i, 1);
             mbar_init(acc_empty + 8 * i, 2 * kEpiWarps);
         }
-        gave_up = 0;
+        if ((gave_up = p.wait_ns == 0))
+            atomicAdd(&g_ffn_timeouts, 1ull);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 3 && lane / 4 < p.nprob) {
@@ -547,14 +560,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
         // producer: this CTA's halves of A and B, stage by stage
         const uint32_t leader_full = in_cta(full, 0);
         uint32_t s = 0, phase = 0;
-        bool ok = true;
+        bool ok = p.wait_ns != 0;
         for (uint32_t i = pair; ok && i < total; i += pairs) {
             const Unit u = unit_at(p, i);
             const Problem &q = p.prob[u.prob];
             const int am = (int)(u.m * kTileM + rank * 128);
             const int bn = EPI == EPI_GATED ? (int)(u.n * 128) : (int)(u.n * kTileN + rank * 128);
             for (uint32_t kb = u.kb0; kb < u.kb1; ++kb) {
-                if (!(ok = mbar_wait(empty + 8 * s, phase ^ 1, &gave_up)))
+                if (!(ok = mbar_wait(empty + 8 * s, phase ^ 1, &gave_up, p.wait_ns)))
                     break;
                 if (rank == 0)
                     mbar_expect(full + 8 * s, 2 * kStageBytes);
@@ -572,7 +585,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
         }
         // the issuer's last arrivals reach both CTAs while they are here
         for (int i = 0; ok && i < kStages; ++i) {
-            ok = mbar_wait(empty + 8 * s, phase ^ 1, &gave_up);
+            ok = mbar_wait(empty + 8 * s, phase ^ 1, &gave_up, p.wait_ns);
             if (++s == kStages) {
                 s = 0;
                 phase ^= 1;
@@ -583,15 +596,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
         const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (A_MN ? 1u << 15 : 0) | (B_MN ? 1u << 16 : 0) |
                                (kTileN >> 3) << 17 | (kTileM >> 4) << 24;
         uint32_t s = 0, phase = 0, t = 0;
-        bool ok = true;
+        bool ok = p.wait_ns != 0;
         for (uint32_t i = pair; ok && i < total; i += pairs, ++t) {
             const Unit u = unit_at(p, i);
             const uint32_t buf = t & 1;
-            if (!(ok = mbar_wait(acc_empty + 8 * buf, ((t >> 1) & 1) ^ 1, &gave_up)))
+            if (!(ok = mbar_wait(acc_empty + 8 * buf, ((t >> 1) & 1) ^ 1, &gave_up, p.wait_ns)))
                 break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             for (uint32_t kb = u.kb0; kb < u.kb1; ++kb) {
-                if (!(ok = mbar_wait(full + 8 * s, phase, &gave_up)))
+                if (!(ok = mbar_wait(full + 8 * s, phase, &gave_up, p.wait_ns)))
                     break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t at = stages + s * kStageBytes;
@@ -617,18 +630,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
         const uint32_t lanes = (uint32_t)(warp & 3) * 32;
         const uint32_t leader_empty = in_cta(acc_empty, 0);
         float *turn = reinterpret_cast<float *>(raw + (stages - smem_u32(raw)) + kStages * kStageBytes) + (warp - 4) * kTurnFloats;
-        uint32_t t = 0;
-        for (uint32_t i = pair; i < total; i += pairs, ++t) {
+        constexpr uint32_t kCols = EPI == EPI_GATED ? 64 : 128;
+        uint32_t t = 0, i = pair;
+        for (; p.wait_ns && i < total; i += pairs, ++t) {
             const Unit u = unit_at(p, i);
             const Problem &q = p.prob[u.prob];
             const uint32_t buf = t & 1;
             const uint32_t row0 = u.m * kTileM + rank * 128 + lanes, row = row0 + lane;
-            constexpr uint32_t kCols = EPI == EPI_GATED ? 64 : 128;
             const uint32_t c0 = half * kCols, col0 = u.n * (2 * kCols) + c0;
             Ahead16<EPI> ahead;
             if (p.vectors && p.splits == 1)
                 ahead.load(p, q, row, col0);
-            if (!__all_sync(0xffffffffu, mbar_wait(acc_full + 8 * buf, (t >> 1) & 1, &gave_up)))
+            if (!__all_sync(0xffffffffu, mbar_wait(acc_full + 8 * buf, (t >> 1) & 1, &gave_up, p.wait_ns)))
                 break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tmem + buf * kTileN + (lanes << 16);
@@ -694,6 +707,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
             if (lane == 0)
                 mbar_arrive_cluster(leader_empty + 8 * buf);
         }
+        for (; i < total; i += pairs) { // after a wait that gave up
+            const Unit u = unit_at(p, i);
+            const Problem &q = p.prob[u.prob];
+            const uint32_t row0 = u.m * kTileM + rank * 128 + lanes, col0 = u.n * (2 * kCols) + half * kCols;
+            for (uint32_t row = row0; row < min(row0 + 32, q.m); ++row)
+                if (p.splits > 1) {
+                    float *out = q.partial + ((uint64_t)u.split * q.m + row) * q.nt * kTileN + u.n * kTileN + half * 128;
+                    for (uint32_t c = lane; c < 128; c += 32)
+                        gstore<float>(out + c, __uint_as_float(0x7fffffffu));
+                } else {
+                    for (uint32_t col = col0 + lane; col < min(col0 + kCols, q.n); col += 32)
+                        finish_nan<EPI>(p, q, row, col);
+                }
+        }
     }
     __syncwarp();
     if (gave_up) // copies still in flight land before the CTA's memory is given back
@@ -741,7 +768,8 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
             mbar_init(acc_full + 8 * i, 1);
             mbar_init(acc_empty + 8 * i, kEpiWarps);
         }
-        gave_up = 0;
+        if ((gave_up = p.wait_ns == 0))
+            atomicAdd(&g_ffn_timeouts, 1ull);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 3 && lane < (EPI == EPI_GATED ? 2 : q.segs))
@@ -761,7 +789,7 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
 
     if (warp == 0 && lane == 0) {
         uint32_t s = 0, phase = 0;
-        bool ok = true;
+        bool ok = p.wait_ns != 0;
         // a: the weights (EPI_GATED: Wg and Wu; else one per segment); b: the tokens
         auto load_a = [&](const Unit &u, uint32_t kb, uint32_t stage) {
             mbar_expect(full + 8 * stage, stage_bytes);
@@ -779,7 +807,7 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
         uint32_t ahead = 0;
         if (p.early) {
             const Unit u = unit_at(p, blockIdx.x);
-            ahead = min(fp.stages, u.kb1 - u.kb0);
+            ahead = ok ? min(fp.stages, u.kb1 - u.kb0) : 0;
             for (uint32_t i = 0; i < ahead; ++i)
                 load_a(u, u.kb0 + i, i);
             chain_entry();
@@ -796,7 +824,7 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
                 if (ahead) {
                     --ahead; // the ring's first round: this stage is free and its weights are on the way
                 } else {
-                    if (!(ok = mbar_wait(empty + 8 * s, phase ^ 1, &gave_up)))
+                    if (!(ok = mbar_wait(empty + 8 * s, phase ^ 1, &gave_up, p.wait_ns)))
                         break;
                     load_a(u, kb, s);
                 }
@@ -806,21 +834,21 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         // the issuer's last arrivals come while the CTA is here
         for (uint32_t i = 0; ok && i < fp.stages; ++i) {
-            ok = mbar_wait(empty + 8 * s, phase ^ 1, &gave_up);
+            ok = mbar_wait(empty + 8 * s, phase ^ 1, &gave_up, p.wait_ns);
             next();
         }
     } else if (warp == 1 && lane == 0) {
         const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (A_MN ? 1u << 15 : 0) | (fp.npad >> 3) << 17 | (128u >> 4) << 24;
         uint32_t s = 0, phase = 0, t = 0;
-        bool ok = true;
+        bool ok = p.wait_ns != 0;
         for (uint32_t i = blockIdx.x; ok && i < q.units; i += gridDim.x, ++t) {
             const Unit u = unit_at(p, i);
             const uint32_t buf = t & 1;
-            if (!(ok = mbar_wait(acc_empty + 8 * buf, ((t >> 1) & 1) ^ 1, &gave_up)))
+            if (!(ok = mbar_wait(acc_empty + 8 * buf, ((t >> 1) & 1) ^ 1, &gave_up, p.wait_ns)))
                 break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             for (uint32_t kb = u.kb0; kb < u.kb1; ++kb) {
-                if (!(ok = mbar_wait(full + 8 * s, phase, &gave_up)))
+                if (!(ok = mbar_wait(full + 8 * s, phase, &gave_up, p.wait_ns)))
                     break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t at = stages + s * stage_bytes;
@@ -846,11 +874,11 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
         // row.  EPI_GATED: the two halves of the warps take the tokens in turn,
         // else one block of rows each.
         const uint32_t half = (warp - 4) / 4, lanes = (uint32_t)(warp & 3) * 32;
-        uint32_t t = 0;
-        for (uint32_t i = blockIdx.x; i < q.units; i += gridDim.x, ++t) {
+        uint32_t t = 0, i = blockIdx.x;
+        for (; p.wait_ns && i < q.units; i += gridDim.x, ++t) {
             const Unit u = unit_at(p, i);
             const uint32_t buf = t & 1;
-            if (!__all_sync(0xffffffffu, mbar_wait(acc_full + 8 * buf, (t >> 1) & 1, &gave_up)))
+            if (!__all_sync(0xffffffffu, mbar_wait(acc_full + 8 * buf, (t >> 1) & 1, &gave_up, p.wait_ns)))
                 break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tmem + buf * 2 * fp.npad + (lanes << 16);
@@ -887,6 +915,22 @@ template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(acc_empty + 8 * buf);
+        }
+        for (; i < q.units; i += gridDim.x) { // after a wait that gave up
+            const Unit u = unit_at(p, i);
+            const uint32_t c0 = (EPI == EPI_GATED ? 0 : half * 128) + lanes + lane, col = u.n * (EPI == EPI_GATED ? 128 : 256) + c0;
+            for (uint32_t row = 0; row < q.m; ++row) {
+                if (EPI == EPI_GATED && (row / 16 & 1) != half)
+                    continue; // the other half's token
+                if (p.splits > 1) {
+                    float *out = q.partial + ((uint64_t)u.split * q.m + row) * q.nt * kTileN + u.n * kTileN + c0;
+                    gstore<float>(out, __uint_as_float(0x7fffffffu));
+                    if (EPI == EPI_GATED)
+                        gstore<float>(out + 128, __uint_as_float(0x7fffffffu));
+                } else if (col < q.n) {
+                    finish_nan<EPI>(p, q, row, col);
+                }
+            }
         }
     }
     __syncwarp();
@@ -1344,6 +1388,7 @@ ccl_status_t gated_ffn_impl(const FfnArgs &a, void *out, cudaStream_t stream)
         return from_cuda(e);
     GemmParams p{};
     p.act = (int)a.act;
+    p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     p.h = reinterpret_cast<uint16_t *>(work + pl.h);
     p.g = a.saved;
     p.u = a.saved ? a.saved + a.t * a.f : nullptr;
@@ -1419,6 +1464,7 @@ ccl_status_t gated_ffn_grad_impl(const FfnArgs &a, const void *dy, void *dx, voi
         return from_cuda(e);
     GemmParams p{};
     p.act = (int)a.act;
+    p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     p.h = reinterpret_cast<uint16_t *>(work + pl.h);
     p.dg = reinterpret_cast<uint16_t *>(work + pl.dg);
     p.du = reinterpret_cast<uint16_t *>(work + pl.du);
@@ -1511,6 +1557,12 @@ ccl_status_t ccl_gated_ffn_grad(const void *grad_out, const void *x, const void 
                                            const_cast<float *>(saved), work, work_bytes},
                                    grad_out, grad_x, grad_w_gate, grad_w_up, grad_w_down, accumulate, stream);
     }));
+}
+
+ccl_status_t ccl_set_gated_ffn_wait_limit(unsigned long long ns)
+{
+    g_wait_ns.store(ns, std::memory_order_relaxed);
+    return CCL_OK;
 }
 
 ccl_status_t ccl_gated_ffn_timeouts(unsigned long long *count)
