@@ -457,7 +457,7 @@ ccl_status_t ccl_embedding(const void *table, size_t rows, size_t dim, size_t ta
  * ccl_plan_embedding_grad_work_bytes bytes, 16-byte aligned, not shared with
  * a concurrent call; its contents need no initialisation.  Launches: the zero
  * rows (accumulate = 0), the sort (one launch for both up to 4096 tokens), the
- * sums, and the join when there are over 8 tokens. */
+ * sums, and the join when the tokens fill more than one run (of 8 to 32). */
 ccl_status_t ccl_embedding_grad(const void *grad_out, size_t grad_out_stride, const int64_t *ids, size_t ntokens,
                                 int64_t first_row, size_t rows, size_t dim, ccl_dtype_t dtype, float scale,
                                 int accumulate, void *grad_table, size_t grad_table_stride, void *work,

@@ -452,10 +452,9 @@ template <int DT, bool VECTOR> __global__ void __launch_bounds__(kSumThreads) em
     constexpr int N = Columns<DT, VECTOR>::N;
     const uint64_t first = (uint64_t)blockIdx.x * p.piece;
     const int n = (int)umin64(p.piece, p.ntokens - first);
-    // lane l holds tokens l and l + 32 of the piece
-    const uint2 none = make_uint2(0xffffffffu, 0);
-    const uint2 a = lane < n ? gload<uint2>(p.sorted + first + lane) : none;
-    const uint2 b = lane + 32 < n ? gload<uint2>(p.sorted + first + lane + 32) : none;
+    // lane l holds token l of the piece
+    static_assert(kMaxPiece <= 32, "a lane holds one token");
+    const uint2 a = lane < n ? gload<uint2>(p.sorted + first + lane) : make_uint2(0xffffffffu, 0);
     const uint32_t prev = first ? row_at(p, first - 1) : 0xffffffffu;
     const uint32_t next = row_at(p, first + n);
     float acc[N];
@@ -469,12 +468,8 @@ template <int DT, bool VECTOR> __global__ void __launch_bounds__(kSumThreads) em
         uint4 v[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const uint32_t ra = __shfl_sync(0xffffffffu, a.x, (i0 + i) & 31);
-            const uint32_t rb = __shfl_sync(0xffffffffu, b.x, (i0 + i) & 31);
-            const uint32_t ta = __shfl_sync(0xffffffffu, a.y, (i0 + i) & 31);
-            const uint32_t tb = __shfl_sync(0xffffffffu, b.y, (i0 + i) & 31);
-            r[i] = i0 + i < 32 ? ra : rb;
-            const uint32_t t = i0 + i < 32 ? ta : tb;
+            r[i] = __shfl_sync(0xffffffffu, a.x, i0 + i);
+            const uint32_t t = __shfl_sync(0xffffffffu, a.y, i0 + i);
             if (r[i] < p.rows)
                 v[i] = cols.fetch(p.dy + (uint64_t)t * p.dy_pitch);
         }
