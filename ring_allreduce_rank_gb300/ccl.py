@@ -529,21 +529,25 @@ def _flat(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype):
 
 def _on_gpu(*ts: Optional[torch.Tensor]) -> int:
     """The one device that all the tensors are on."""
-    dev = -1
+    dev = None
     for t in ts:
-        if t is None:
-            continue
-        d = t.get_device()
-        if d < 0:
-            raise ValueError("the operators take CUDA tensors")
-        if dev >= 0 and d != dev:
-            raise ValueError("the tensors are on different devices")
-        dev = d
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if d < 0:
+                    raise ValueError("the operators take CUDA tensors")
+                if dev is not None:
+                    raise ValueError("the tensors are on different devices")
+                dev = d
+    if dev is None:
+        raise ValueError("the operators take CUDA tensors")
     return dev
 
 
 # the current device and the current stream's handle without the objects and
-# checks around them, which cost more than a small kernel's launch
+# checks around them, which cost more than a small kernel's launch.  The C
+# entries launch on the current device: an operator whose tensors are on another
+# one runs with that one current.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
@@ -552,17 +556,6 @@ def _stream_on(stream, device: int):
     if stream is None and _raw_stream is not None:
         return _raw_stream(device)
     return _stream(stream)
-
-
-def _launch(name: str, device: int, stream, *args) -> None:
-    """Calls an operator's entry, which launches on the current device, with
-    the tensors' device current and on that device's stream."""
-    entry = getattr(lib(), name)
-    if _current_device() == device:
-        _check(entry(*args, _stream_on(stream, device)), name)
-    else:
-        with torch.cuda.device(device):
-            _check(entry(*args, _stream_on(stream, device)), name)
 
 
 def _work(work: Optional[torch.Tensor], nbytes: int, like: torch.Tensor, stream):
@@ -583,11 +576,14 @@ def ccl_embedding(table: torch.Tensor, ids: torch.Tensor, out: torch.Tensor, sca
     """out[t] = scale * table[ids[t] - first_row]; zeros for an id outside the
     table's rows (padding, or another rank's shard of the vocabulary)."""
     dev = _on_gpu(table, ids, out)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return ccl_embedding(table, ids, out, scale, first_row, stream)
     tp, rows, dim, ts = _rows(table, "table")
     op, n, _, os_ = _rows(out, "out", dim, table.dtype)
     ip = _flat(ids, "ids", (n,), torch.int64)
-    _launch("ccl_embedding", dev, stream, tp, rows, dim, ts, _dtype(table), ip, n, int(first_row), float(scale), op,
-            os_)
+    _check(lib().ccl_embedding(tp, rows, dim, ts, _dtype(table), ip, n, int(first_row), float(scale), op, os_,
+                               _stream_on(stream, dev)), "ccl_embedding")
 
 
 def ccl_embedding_grad(grad_out: torch.Tensor, ids: torch.Tensor, grad_table: torch.Tensor, scale: float = 1.0,
@@ -597,13 +593,17 @@ def ccl_embedding_grad(grad_out: torch.Tensor, ids: torch.Tensor, grad_table: to
     the tokens with ids[t] == first_row + v.  work: a device buffer of at least
     ccl_plan_embedding_grad_work_bytes bytes (allocated here when omitted)."""
     dev = _on_gpu(grad_out, ids, grad_table, work)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return ccl_embedding_grad(grad_out, ids, grad_table, scale, first_row, accumulate, work, stream)
     gp, n, dim, gs = _rows(grad_out, "grad_out")
     tp, rows, _, ts = _rows(grad_table, "grad_table", dim, grad_out.dtype)
     ip = _flat(ids, "ids", (n,), torch.int64)
     work, nbytes = _work(work, 0 if work is not None else ccl_plan_embedding_grad_work_bytes(n, rows, dim), grad_out,
                          stream)
-    _launch("ccl_embedding_grad", dev, stream, gp, gs, ip, n, int(first_row), rows, dim, _dtype(grad_out),
-            float(scale), int(bool(accumulate)), tp, ts, work.data_ptr(), nbytes)
+    _check(lib().ccl_embedding_grad(gp, gs, ip, n, int(first_row), rows, dim, _dtype(grad_out), float(scale),
+                                    int(bool(accumulate)), tp, ts, work.data_ptr(), nbytes, _stream_on(stream, dev)),
+           "ccl_embedding_grad")
 
 
 def ccl_plan_embedding_grad_work_bytes(ntokens: int, rows: int, dim: int) -> int:
@@ -635,12 +635,16 @@ def ccl_gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_d
     ccl_gated_ffn_grad.  work: a device buffer of at least
     ccl_plan_gated_ffn_work_bytes bytes (allocated here when omitted)."""
     dev = _on_gpu(x, w_gate, w_up, w_down, out, saved, work)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return ccl_gated_ffn(x, w_gate, w_up, w_down, out, act, saved, work, stream)
     ptrs, (n, dim, ffn) = _ffn_shapes(x, w_gate, w_up, w_down)
     op = _flat(out, "out", (n, dim), x.dtype)
     sp = _flat(saved, "saved", (2, n, ffn), torch.float32)
     work, nbytes = _work(work, 0 if work is not None else
                          ccl_plan_gated_ffn_work_bytes(n, dim, ffn, False, all(q % 16 == 0 for q in ptrs)), x, stream)
-    _launch("ccl_gated_ffn", dev, stream, *ptrs, n, dim, ffn, _dtype(x), _act(act), op, sp, work.data_ptr(), nbytes)
+    _check(lib().ccl_gated_ffn(*ptrs, n, dim, ffn, _dtype(x), _act(act), op, sp, work.data_ptr(), nbytes,
+                               _stream_on(stream, dev)), "ccl_gated_ffn")
 
 
 def ccl_gated_ffn_grad(grad_out: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
@@ -651,6 +655,10 @@ def ccl_gated_ffn_grad(grad_out: torch.Tensor, x: torch.Tensor, w_gate: torch.Te
     """The block's gradients (those given), from the saved pre-activations;
     accumulate adds to the weights' gradients."""
     dev = _on_gpu(grad_out, x, w_gate, w_up, w_down, saved, grad_x, grad_w_gate, grad_w_up, grad_w_down, work)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return ccl_gated_ffn_grad(grad_out, x, w_gate, w_up, w_down, saved, grad_x, grad_w_gate, grad_w_up,
+                                      grad_w_down, act, accumulate, work, stream)
     ptrs, (n, dim, ffn) = _ffn_shapes(x, w_gate, w_up, w_down)
     dt = x.dtype
     yp = _flat(grad_out, "grad_out", (n, dim), dt)
@@ -660,8 +668,8 @@ def ccl_gated_ffn_grad(grad_out: torch.Tensor, x: torch.Tensor, w_gate: torch.Te
     work, nbytes = _work(work, 0 if work is not None else
                          ccl_plan_gated_ffn_work_bytes(n, dim, ffn, True, all(q % 16 == 0 for q in (yp, *ptrs))), x,
                          stream)
-    _launch("ccl_gated_ffn_grad", dev, stream, yp, *ptrs, sp, n, dim, ffn, _dtype(x), _act(act),
-            int(bool(accumulate)), *grads, work.data_ptr(), nbytes)
+    _check(lib().ccl_gated_ffn_grad(yp, *ptrs, sp, n, dim, ffn, _dtype(x), _act(act), int(bool(accumulate)), *grads,
+                                    work.data_ptr(), nbytes, _stream_on(stream, dev)), "ccl_gated_ffn_grad")
 
 
 def ccl_plan_gated_ffn_work_bytes(ntokens: int, dim: int, ffn: int, backward: bool = False, aligned: bool = True) -> int:
@@ -692,6 +700,10 @@ def ccl_distill_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_lo
     ccl_distill_grad.  grad: the gradient by the logits, in the same pass (may
     be `logits` itself)."""
     dev = _on_gpu(logits, teacher_ids, teacher_logits, loss, stats, grad, weights)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return ccl_distill_loss(logits, teacher_ids, teacher_logits, loss, stats, grad, weights, temperature,
+                                    stream)
     lp, n, vocab, ls = _rows(logits, "logits")
     gp, gs = None, vocab
     if grad is not None:
@@ -699,11 +711,11 @@ def ccl_distill_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_lo
         if gn != n:
             raise ValueError("grad has %d rows, expected %d" % (gn, n))
     top = teacher_ids.shape[-1]
-    _launch("ccl_distill_loss", dev, stream, lp, n, vocab, ls, _dtype(logits),
-            _flat(teacher_ids, "teacher_ids", (n, top), torch.int64),
-            _flat(teacher_logits, "teacher_logits", (n, top), torch.float32), top, float(temperature),
-            _flat(weights, "weights", (n,), torch.float32), _flat(loss, "loss", (n,), torch.float32),
-            _flat(stats, "stats", (n, 2), torch.float32), gp, gs)
+    _check(lib().ccl_distill_loss(lp, n, vocab, ls, _dtype(logits), _flat(teacher_ids, "teacher_ids", (n, top), torch.int64),
+                                  _flat(teacher_logits, "teacher_logits", (n, top), torch.float32), top,
+                                  float(temperature), _flat(weights, "weights", (n,), torch.float32),
+                                  _flat(loss, "loss", (n,), torch.float32), _flat(stats, "stats", (n, 2), torch.float32),
+                                  gp, gs, _stream_on(stream, dev)), "ccl_distill_loss")
 
 
 def ccl_distill_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
@@ -712,15 +724,19 @@ def ccl_distill_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_lo
     """The gradient of the sum of ccl_distill_loss's losses by the logits, from
     the stats it kept; grad may be `logits` itself."""
     dev = _on_gpu(logits, teacher_ids, teacher_logits, stats, grad, weights)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return ccl_distill_grad(logits, teacher_ids, teacher_logits, stats, grad, weights, temperature, stream)
     lp, n, vocab, ls = _rows(logits, "logits")
     gp, gn, _, gs = _rows(grad, "grad", vocab, logits.dtype)
     if gn != n:
         raise ValueError("grad has %d rows, expected %d" % (gn, n))
     top = teacher_ids.shape[-1]
-    _launch("ccl_distill_grad", dev, stream, lp, n, vocab, ls, _dtype(logits),
-            _flat(teacher_ids, "teacher_ids", (n, top), torch.int64),
-            _flat(teacher_logits, "teacher_logits", (n, top), torch.float32), top, float(temperature),
-            _flat(weights, "weights", (n,), torch.float32), _flat(stats, "stats", (n, 2), torch.float32), gp, gs)
+    _check(lib().ccl_distill_grad(lp, n, vocab, ls, _dtype(logits), _flat(teacher_ids, "teacher_ids", (n, top), torch.int64),
+                                  _flat(teacher_logits, "teacher_logits", (n, top), torch.float32), top,
+                                  float(temperature), _flat(weights, "weights", (n,), torch.float32),
+                                  _flat(stats, "stats", (n, 2), torch.float32), gp, gs, _stream_on(stream, dev)),
+           "ccl_distill_grad")
 
 
 # ------------------------------------------------------------------ planner

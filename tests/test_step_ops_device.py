@@ -103,3 +103,7 @@ def test_tensors_on_two_devices_are_refused():
         C._on_gpu(On(1), On(0))
     with pytest.raises(ValueError, match="CUDA"):
         C._on_gpu(On(1), On(-1))
+    with pytest.raises(ValueError, match="CUDA"):
+        C._on_gpu(On(-1), On(1))
+    with pytest.raises(ValueError, match="CUDA"):
+        ccl.ccl_embedding(None, None, None)
