@@ -9,7 +9,7 @@
 // pass over the row for (m, Z); the gradient needs the row's values again.
 // Bound by memory bandwidth.  The loss alone uses a row once: a CTA streams it
 // through its registers, eight vectors a thread in flight (4096 rows of 128000
-// bf16: 160 us, 0.97 of the measured copy bandwidth).  For loss and gradient
+// bf16: 161-163 us, 0.95-0.96 of the measured copy bandwidth).  For loss and gradient
 // in one call memory sees one read of the logits and one write of the gradient:
 // a cluster of CTAs takes a row, each CTA asks for its whole part at once (up to
 // 64 KiB: half to registers, half to shared memory by asynchronous copies) and
@@ -17,9 +17,10 @@
 // distributed shared memory.  Four CTAs an SM are at different places of this,
 // so that loads, exponentials and stores overlap: 406 us for the same rows,
 // 0.76 of the copy bandwidth (reading a row a second time from the L2 cache
-// missed it, 608 CTAs' rows of 250 KiB, and took 471).  The gradient from kept
-// statistics asks for its part in the same way, 350 us (streaming it like the
-// loss, stores between the loads, took 409).
+// missed it, 608 CTAs' rows of 250 KiB, and took 471).  Four CTAs leave a thread
+// 56 registers and 100-160 bytes of spills; three, without spills, took 427.
+// The gradient from kept statistics asks for its part in the same way, 345 us,
+// 0.90 (streaming it like the loss, stores between the loads, took 409).
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -36,7 +37,7 @@ namespace {
 
 constexpr int kDThreads = 256;   // that hold a row's vectors; a further warp works on the teacher's entries
 constexpr int kDWarps = kDThreads / 32;
-constexpr int kDCtas = 4;        // resident CTAs per SM
+constexpr int kDCtas = 4;        // resident CTAs per SM, for loss and gradient in one call; one less for either alone
 constexpr int kVecs = 2;         // 16-byte vectors a thread folds at a time
 constexpr int kHeld = 8;         // vectors a thread keeps in registers, and as many in shared memory
 constexpr uint32_t kPart = 2 * kHeld * kDThreads; // vectors a CTA keeps
@@ -641,7 +642,8 @@ ccl_status_t distill_impl(int mode, const DistillArgs &a, cudaStream_t stream)
         ++p.slot_bits;
     // the fewest CTAs that hold a row (for the loss alone: one); more, as long
     // as each thread has a batch of vectors, while they leave places on the
-    // GPU empty
+    // GPU empty (counted as loss and gradient in one call have them; the other
+    // two have 456 of these 608: 333 rows of 50257 fp32 take 1.5 and 2.9 rounds)
     const uint64_t bytes = a.vocab * es;
     uint32_t ctas = 1;
     p.cluster_bits = 0;

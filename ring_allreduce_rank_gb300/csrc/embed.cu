@@ -10,10 +10,11 @@
 //   0. embed_zero_kernel (dense gradient): zeros to the rows that no token
 //      names, which need no sort to be found; a few further CTAs of it rank
 //      the tokens where they are at most 4096.
-//   1. embed_sort_kernel, for more, beside it: the tokens' (row, position)
-//      pairs sorted by row, stably, by a radix sort that one cluster of eight
-//      CTAs runs (the digits' counts cross the cluster through distributed
-//      shared memory).
+//   1. embed_sort_kernel, for more: the tokens' (row, position) pairs sorted by
+//      row, stably, by a radix sort that one cluster of eight CTAs runs (the
+//      digits' counts cross the cluster through distributed shared memory).  It
+//      need not wait for the zeros, but its CTAs take all the registers of an
+//      SM each, so it begins once eight SMs have finished theirs.
 //   2. embed_sum_kernel: the sorted tokens in pieces of 8 to 32, each summed in
 //      order; a row whose tokens lie in one piece is finished here, a row that
 //      crosses pieces leaves one fp32 partial sum per piece.
@@ -21,9 +22,10 @@
 // No value is added by an atomic, so the same ids give the same bits each
 // time, and a row that takes every token is still summed by all SMs.
 // 16384 Zipf-distributed tokens of 4096 bf16 values over 32000 rows: lookup
-// 31 us (the repeated rows come from the L2 cache), dense gradient 87 us
-// against 58 us for its bytes at the copy bandwidth: zeros 40 us, which cover
-// the sort's 16, sums 33, join 8 (each alone).
+// 31 us (the repeated rows come from the L2 cache), dense gradient 84 us
+// against 58 us for its bytes at the copy bandwidth: zeros 40 us, sort 16,
+// sums 30, join 12 (each alone); 94 us where the sort begins after the last
+// zero.  Added to a table that is there (no zeros, old rows read): 73 us.
 #include <cooperative_groups.h>
 
 #include <vector>
@@ -157,7 +159,7 @@ __device__ __forceinline__ void warp_zero(char *q, uint64_t n, int elem, int lan
 // most kFewIds tokens.
 __global__ void __launch_bounds__(kZeroThreads, 2) embed_zero_kernel(const __grid_constant__ SortParams p)
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); // the sort does not wait for the zeros
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); // the sort needs no zeros, only room
     constexpr uint32_t kRows = 16384; // marked at a time
     constexpr int kIds = 16;
     // a byte a row, set by plain stores of one value: an atomic per token of a
@@ -723,7 +725,7 @@ ccl_status_t embedding_grad_impl(const void *grad_out, size_t grad_out_stride, c
         attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = accumulate ? 1 : 2; // beside the zeros, when there are any
+        cfg.numAttrs = accumulate ? 1 : 2; // under the zeros' tail, when there are any
         if (cudaError_t e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, s))
             return from_cuda(e);
         count_launches(1);

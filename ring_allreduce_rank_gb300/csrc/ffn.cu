@@ -22,10 +22,10 @@
 // add a rounding to every factor of every gradient.
 //
 // Bound by the tensor cores for many tokens, by reading the weights for few.
-// At 4096 x 11008: forward of 4096 tokens 664-680 us (1.63-1.67 PFLOP/s; cuBLAS
+// At 4096 x 11008: forward of 4096 tokens 678-692 us (1.60-1.63 PFLOP/s; cuBLAS
 // sustains 1.71 on plain products at this card's power limit), forward and
-// backward of 2048 tokens 1067-1098 us (1.51-1.56 PFLOP/s), forward of one
-// token 52 us (5.2 TB/s of weights, 0.76 of the copy bandwidth), of 48 59 us.
+// backward of 2048 tokens 1077-1103 us (1.51-1.54 PFLOP/s), forward of one
+// token 53 us (5.1 TB/s of weights, 0.75 of the copy bandwidth), of 48 60 us.
 // Cutting the last, partly filled round of tiles along K to fill it made each
 // product shorter alone and the whole longer: at the power limit a fuller GPU
 // runs at a lower clock, and the partial sums' join is not free.
@@ -51,7 +51,8 @@ constexpr int kMaxStages = 6; // ffn_few_kernel's
 // Products that ffn_few_kernel takes: few tokens.  Forward in us, this kernel
 // against CTA pairs' 256-row tiles: 488 x 2584 with 48 tokens 16.8 against 17.3,
 // with 64 equal, with 128 22.0 against 19.7; 4096 x 11008 with 64 tokens 61
-// against 73, with 128 69 against 79, with 198 84 against 82.  Backward to the
+// against 73, with 128 69 against 79, with 198 84 against 82 (kManyWeights lies
+// between the two widths, where nothing was measured).  Backward to the
 // inputs, 1000 x 3000: with 64 tokens 19.5 against 31.4, with 128 24.4 against
 // 34.4, with 198 54.5 against 34.5.
 constexpr uint64_t kFewTokens = 64, kFewTokensMost = 128; // the latter for many weights, and backward
@@ -741,10 +742,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
 // work on the tokens there are and not on a 256-row tile of them: one CTA a
 // unit of two 128-row blocks of weights (EPI_GATED: the same rows of Wg and
 // Wu), which share the tokens' stage.  Bound by reading the weights: one
-// token's g and u at 4096 x 11008 take 32 us (5.6 TB/s); on the 256-row tile
-// they took 52, half of a tensor core's time spent on absent tokens.  Cutting
-// K further to spread the 86 units over all SMs gave nothing at one token
-// (52.2-52.5 us for the call) and cost 4-7 us at 48, whose partial sums weigh.
+// token's g and u at 4096 x 11008 take 34 us (5.3 TB/s); on the 256-row tile
+// they took 52, half of a tensor core's time spent on absent tokens.  Its 86
+// units are cut in 7 along K, 602 on 152 CTAs; other cuts, into 2 to 14, made
+// the call 52-61 us.  With 48 tokens they stay whole, on 86 CTAs: cutting them
+// cost 4-7 us, because the partial sums weigh.
 template <int EPI, bool A_MN> __global__ void __launch_bounds__(kGemmThreads, 1) ffn_few_kernel(const __grid_constant__ FewParams fp)
 {
     extern __shared__ uint8_t raw[];
