@@ -208,7 +208,7 @@ def _run_own(s):
                       normalize=s["normalize"], valid=s["valid"], work=s["work"])
         out = {k: s[k] for k in ("ids", "weights", "counts", "load", "importance", "loss")}
         if s["form"] == "train":
-            ccl.ccl_route_grad(s["logits"], s["ids"], s["weights"], s["lse"], s["counts"], s["load"], s["grad_weights"], s["grad_logits"],
+            ccl.ccl_route_grad(s["logits"], s["ids"], s["lse"], s["counts"], s["load"], s["grad_weights"], s["grad_logits"],
                                normalize=s["normalize"], balance=BALANCE, z=ZLOSS)
             out["grad_logits"] = s["grad_logits"]
         return out
