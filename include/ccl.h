@@ -539,6 +539,144 @@ ccl_status_t ccl_distill_grad(const void *logits, size_t nrows, size_t vocab, si
                               cudaStream_t stream);
 
 /* ------------------------------------------------------------------ */
+/* Operators of an expert-parallel step                                */
+/* ------------------------------------------------------------------ */
+
+/* What a rank computes around ccl_alltoallv when a layer's feed-forward block
+ * is a mixture of experts: the router with its balance loss, the tokens in
+ * expert order (the exchange's send buffer and, from the offsets, its counts),
+ * the experts' blocks over them, the weighted sum back, and the gradients, with
+ * the activations kept in 8 bits in between.  The conventions of the operators
+ * of a training step hold.  experts <= CCL_MAX_EXPERTS, choices of one token
+ * (top) <= CCL_MAX_EXPERT_TOP, tokens * top < 2^31. */
+#define CCL_MAX_EXPERTS 1024
+#define CCL_MAX_EXPERT_TOP 32
+
+/* Router.  Over each token's logits z (1 <= top <= experts of them are chosen):
+ *   p = softmax(z); ids[t][0..top) = the experts of the largest logits, largest
+ *   first, ties to the lower expert; weights[t][s] = p at ids[t][s], divided by
+ *   the sum of the chosen ones when normalize != 0; lse[t] = log sum exp z
+ *   counts[e] = tokens that chose e, counts[experts] = n, the tokens routed
+ *   load[e] = counts[e] / all choices, importance[e] = (sum over tokens of p_e) / n
+ *   losses[0] = experts * sum_e load[e] importance[e] (the balance loss: 1 when
+ *   both are even), losses[1] = (sum over tokens of lse^2) / n (the z loss)
+ * A logit of -inf is an expert that the token cannot choose; a slot left without
+ * an expert has id -1 and weight 0.  A token with valid[t] == 0 (valid == NULL:
+ * none), or without any expert, is not routed: ids -1, weights 0, lse 0, and it
+ * counts nowhere.  A NaN or +inf makes its token's weights NaN (the ids stay in
+ * range, NaN being the largest).  work: ccl_plan_route_work_bytes bytes, 256-byte
+ * aligned, not shared with a concurrent call, contents irrelevant (0 bytes for
+ * few tokens).  One launch, or two. */
+ccl_status_t ccl_route(const void *logits, size_t ntokens, size_t experts, size_t logits_stride, ccl_dtype_t dtype,
+                       const uint8_t *valid, size_t top, int normalize, int32_t *ids, float *weights, float *lse,
+                       int32_t *counts, float *load, float *importance, float *losses, void *work, size_t work_bytes,
+                       cudaStream_t stream);
+ccl_status_t ccl_plan_route_work_bytes(size_t ntokens, size_t experts, size_t *bytes);
+
+/* Its gradient by the logits, of sum grad_weights * weights + balance *
+ * losses[0] + z * losses[1] (the choices and load are constants):
+ *   grad[t][j] = p_j (G_j - sum_i G_i p_i + 2 z lse[t] / n),
+ *   G_j = balance * experts * load[j] / n + [j chosen] (by its weight)
+ * from what ccl_route left in ids, lse, counts (only counts[experts] is read) and
+ * load, which may have been averaged over the ranks by ccl_allreduce in between.
+ * grad_weights where the id is -1 does not count, whatever it holds.  Tokens that
+ * are not routed have gradient 0.  In place: grad_logits == logits with the same
+ * stride. */
+ccl_status_t ccl_route_grad(const void *logits, size_t ntokens, size_t experts, size_t logits_stride, ccl_dtype_t dtype,
+                            const int32_t *ids, size_t top, int normalize, const float *lse, const int32_t *counts,
+                            const float *load, const float *grad_weights, float balance, float z, void *grad_logits,
+                            size_t grad_stride, cudaStream_t stream);
+
+/* The tokens' copies in expert order: place[t][s] = the row of token t's s-th
+ * choice, rows being ordered by expert, then token, then choice; expert
+ * first_expert + e has rows [offsets[e], offsets[e + 1]), offsets[0] = 0.  An id outside [first_expert, first_expert + experts)
+ * (-1, or an expert of another rank) has place -1.  work:
+ * ccl_plan_expert_order_work_bytes bytes, 256-byte aligned, not shared with a
+ * concurrent call (0 bytes up to 4096 choices).  One launch, or three. */
+ccl_status_t ccl_expert_order(const int32_t *ids, size_t ntokens, size_t top, int32_t first_expert, size_t experts,
+                              int32_t *offsets, int32_t *place, void *work, size_t work_bytes, cudaStream_t stream);
+ccl_status_t ccl_plan_expert_order_work_bytes(size_t ntokens, size_t top, size_t experts, size_t *bytes);
+
+/* rows[place[t][s]] = x[t].  A place outside [0, nrows) is skipped; rows that no
+ * place names are left as they were.  No two places may name the same row.  Its
+ * gradient is ccl_combine without weights. */
+ccl_status_t ccl_dispatch(const void *x, size_t ntokens, size_t dim, size_t x_stride, ccl_dtype_t dtype,
+                          const int32_t *place, size_t top, void *rows, size_t nrows, size_t rows_stride,
+                          cudaStream_t stream);
+
+/* out[t] = round(sum over s of weights[t][s] rows[place[t][s]]), the sum in fp32
+ * in the order of s.  A place outside [0, nrows) adds nothing, whatever its
+ * weight; a token without any gives zeros.  weights == NULL means 1. */
+ccl_status_t ccl_combine(const void *rows, size_t nrows, size_t dim, size_t rows_stride, ccl_dtype_t dtype,
+                         const int32_t *place, const float *weights, size_t ntokens, size_t top, void *out,
+                         size_t out_stride, cudaStream_t stream);
+
+/* Its gradients: grad_rows[place[t][s]] = round(weights[t][s] grad_out[t]) and
+ * grad_weights[t][s] = <grad_out[t], rows[place[t][s]]> in fp32, 0 where there is
+ * no row.  A NULL gradient is not computed, and rows is read for grad_weights
+ * only.  Rows that no place names are left as they were; no two places may name
+ * the same row.  In place: grad_rows == rows with the same stride. */
+ccl_status_t ccl_combine_grad(const void *grad_out, size_t grad_out_stride, const void *rows, size_t nrows, size_t dim,
+                              size_t rows_stride, ccl_dtype_t dtype, const int32_t *place, const float *weights,
+                              size_t ntokens, size_t top, void *grad_rows, size_t grad_rows_stride, float *grad_weights,
+                              cudaStream_t stream);
+
+/* Activations in 8 bits, kept for the backward pass.  Each row is cut into blocks
+ * of 32 values (the last one may be shorter); a block's step is 2^e, the least
+ * power of two with |x| <= 127 * 2^e (e >= -126, and at most 121, where larger
+ * values become 127 * 2^121), and
+ *   codes[r][c] = x / 2^e rounded to the nearest integer, ties to even
+ *   scales[r][c / 32] = e + 127; 255 for a block that holds an infinity or a NaN,
+ *   which comes back as NaN
+ * so that a value comes back to within 2^(e-1), and as a bf16 number.  codes:
+ * [rows][width], 32-byte aligned, width = the columns rounded up to a multiple of
+ * 32 (ccl_plan_act8_width), its last columns 0; scales: [rows][width / 32].
+ * rows < 2^31, cols <= 2^24. */
+ccl_status_t ccl_act8_pack(const void *x, size_t rows, size_t cols, size_t x_stride, ccl_dtype_t dtype, int8_t *codes,
+                           uint8_t *scales, cudaStream_t stream);
+ccl_status_t ccl_act8_unpack(const int8_t *codes, const uint8_t *scales, size_t rows, size_t cols, ccl_dtype_t dtype,
+                             void *x, size_t x_stride, cudaStream_t stream);
+ccl_status_t ccl_plan_act8_width(size_t cols, size_t *width);
+
+/* The experts' gated feed-forward blocks (as ccl_gated_ffn) over rows in expert
+ * order: rows [offsets[e], offsets[e + 1]) of x go through expert e's weights,
+ * w_gate, w_up [experts][ffn][dim] and w_down [experts][dim][ffn], all contiguous
+ * and bf16.  offsets is DEVICE memory, [experts + 1], as ccl_expert_order leaves
+ * it (any part of it will do): the call needs no count on the host.  Offsets that
+ * fall, or lie outside [0, nrows], are taken as the largest before them within
+ * [0, nrows].  Rows of out before offsets[0] and from offsets[experts] on are left
+ * as they were.  saved_codes, saved_scales != NULL keep g and u for the backward
+ * pass in 8 bits as ccl_act8_pack keeps them, [2][nrows][width(ffn)] and
+ * [2][nrows][width(ffn) / 32] (the rows of experts).  ffn >= 1.  work: ccl_plan_expert_ffn_work_bytes bytes,
+ * 256-byte aligned, not shared with a concurrent call, contents irrelevant. */
+ccl_status_t ccl_expert_ffn(const void *x, const int32_t *offsets, const void *w_gate, const void *w_up,
+                            const void *w_down, size_t nrows, size_t experts, size_t dim, size_t ffn, ccl_dtype_t dtype,
+                            ccl_act_t act, void *out, int8_t *saved_codes, uint8_t *saved_scales, void *work,
+                            size_t work_bytes, cudaStream_t stream);
+
+/* Its gradients, from grad_out, the saved g and u, and x, which is given either
+ * as it was (x) or in 8 bits (x == NULL: x_codes, x_scales, as ccl_act8_pack left
+ * it):
+ *   dh = grad_out w_down, du = dh * act(g), dg = dh * u * act'(g), h = act(g) * u
+ *   grad_x = dg w_gate + du w_up, grad_w_gate = dg^T x, grad_w_up = du^T x,
+ *   grad_w_down = grad_out^T h
+ * expert by expert, h, dg and du rounded to bf16 once.  A NULL gradient is not
+ * computed.  An expert without rows has weight gradients 0.  accumulate != 0 adds
+ * to the weight gradients: round(old + sum), one rounding.  work: planned with
+ * backward = 1.  Waits that run out are counted by ccl_gated_ffn_timeouts, and
+ * ccl_set_gated_ffn_wait_limit sets their limit. */
+ccl_status_t ccl_expert_ffn_grad(const void *grad_out, const void *x, const int8_t *x_codes, const uint8_t *x_scales,
+                                 const int32_t *offsets, const void *w_gate, const void *w_up, const void *w_down,
+                                 const int8_t *saved_codes, const uint8_t *saved_scales, size_t nrows, size_t experts,
+                                 size_t dim, size_t ffn, ccl_dtype_t dtype, ccl_act_t act, int accumulate, void *grad_x,
+                                 void *grad_w_gate, void *grad_w_up, void *grad_w_down, void *work, size_t work_bytes,
+                                 cudaStream_t stream);
+
+/* Bytes of the work buffer; aligned and backward as for ccl_plan_gated_ffn_work_bytes. */
+ccl_status_t ccl_plan_expert_ffn_work_bytes(size_t nrows, size_t experts, size_t dim, size_t ffn, int backward,
+                                            int aligned, size_t *bytes);
+
+/* ------------------------------------------------------------------ */
 /* Result checks and tracing                                           */
 /* ------------------------------------------------------------------ */
 

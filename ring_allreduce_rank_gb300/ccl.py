@@ -27,6 +27,8 @@ COMPRESSORS = {"int8_block": 0, "threshold": 1, "topk": 2}
 STATUS = {0: "CCL_OK", 1: "CCL_ERR_INVALID_ARG", 2: "CCL_ERR_UNSUPPORTED", 3: "CCL_ERR_OVERLAP",
           4: "CCL_ERR_CUDA", 5: "CCL_ERR_NO_MEMORY", 6: "CCL_ERR_TIMEOUT", 7: "CCL_ERR_CHECK_FAILED"}
 MAX_RANKS = 1024
+MAX_EXPERTS, MAX_EXPERT_TOP = 1024, 32
+ACT8_BLOCK = 32
 DEFAULT_BUCKET_BYTES = 25 * 1024 * 1024
 HOST_WORK_BYTES_DEFAULT = 192 * 1024 * 1024
 
@@ -97,6 +99,21 @@ def lib() -> ctypes.CDLL:
                 "ccl_plan_gated_ffn_work_bytes": [sz, sz, sz, i32, i32, psz],
                 "ccl_set_gated_ffn_wait_limit": [ctypes.c_ulonglong],
                 "ccl_gated_ffn_timeouts": [ctypes.POINTER(ctypes.c_ulonglong)],
+                "ccl_route": [vp, sz, sz, sz, i32, vp, sz, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+                "ccl_plan_route_work_bytes": [sz, sz, psz],
+                "ccl_route_grad": [vp, sz, sz, sz, i32, vp, sz, i32, vp, vp, vp, vp, f32, f32, vp, sz, vp],
+                "ccl_expert_order": [vp, sz, sz, ctypes.c_int32, sz, vp, vp, vp, sz, vp],
+                "ccl_plan_expert_order_work_bytes": [sz, sz, sz, psz],
+                "ccl_dispatch": [vp, sz, sz, sz, i32, vp, sz, vp, sz, sz, vp],
+                "ccl_combine": [vp, sz, sz, sz, i32, vp, vp, sz, sz, vp, sz, vp],
+                "ccl_combine_grad": [vp, sz, vp, sz, sz, sz, i32, vp, vp, sz, sz, vp, sz, vp, vp],
+                "ccl_act8_pack": [vp, sz, sz, sz, i32, vp, vp, vp],
+                "ccl_act8_unpack": [vp, vp, sz, sz, i32, vp, sz, vp],
+                "ccl_plan_act8_width": [sz, psz],
+                "ccl_expert_ffn": [vp, vp, vp, vp, vp, sz, sz, sz, sz, i32, i32, vp, vp, vp, vp, sz, vp],
+                "ccl_expert_ffn_grad": [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, sz, sz, sz, i32, i32, i32, vp, vp, vp, vp, vp,
+                                        sz, vp],
+                "ccl_plan_expert_ffn_work_bytes": [sz, sz, sz, sz, i32, i32, psz],
                 "ccl_distill_loss": [vp, sz, sz, sz, i32, vp, vp, sz, f32, vp, vp, vp, vp, sz, vp],
                 "ccl_distill_grad": [vp, sz, sz, sz, i32, vp, vp, sz, f32, vp, vp, vp, sz, vp],
             }
@@ -737,6 +754,265 @@ def ccl_distill_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_lo
                                   float(temperature), _flat(weights, "weights", (n,), torch.float32),
                                   _flat(stats, "stats", (n, 2), torch.float32), gp, gs, _stream_on(stream, dev)),
            "ccl_distill_grad")
+
+
+# ------------------------------------------------------------------ operators of an expert-parallel step
+
+def _planned(name: str, *args) -> int:
+    out = ctypes.c_size_t()
+    _check(getattr(lib(), name)(*(int(a) for a in args), ctypes.byref(out)), name)
+    return out.value
+
+
+def ccl_plan_route_work_bytes(ntokens: int, experts: int) -> int:
+    return _planned("ccl_plan_route_work_bytes", ntokens, experts)
+
+
+def ccl_plan_expert_order_work_bytes(ntokens: int, top: int, experts: int) -> int:
+    return _planned("ccl_plan_expert_order_work_bytes", ntokens, top, experts)
+
+
+def ccl_plan_act8_width(cols: int) -> int:
+    """Columns of the codes of rows of `cols` values: rounded up to a multiple of 32."""
+    return _planned("ccl_plan_act8_width", cols)
+
+
+def ccl_plan_expert_ffn_work_bytes(nrows: int, experts: int, dim: int, ffn: int, backward: bool = False, aligned: bool = True) -> int:
+    return _planned("ccl_plan_expert_ffn_work_bytes", nrows, experts, dim, ffn, bool(backward), bool(aligned))
+
+
+def _choices(t: torch.Tensor, name: str):
+    """(pointer, tokens, top) of a contiguous [tokens, top] int32 tensor."""
+    if t.dim() != 2:
+        raise ValueError("%s must be a tensor of shape [tokens, top]" % name)
+    return (_flat(t, name, t.shape, torch.int32), *t.shape)
+
+
+def ccl_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, lse: torch.Tensor, counts: torch.Tensor,
+              load: torch.Tensor, importance: torch.Tensor, losses: torch.Tensor, normalize: bool = True,
+              valid: Optional[torch.Tensor] = None, work: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The top choices of every token's softmax over the experts, with the
+    balance and z losses.  logits [tokens, experts]; written: ids (int32) and
+    weights [tokens, top], lse [tokens], counts [experts + 1] (int32; the last
+    one the tokens routed), load and importance [experts], losses [2].  valid
+    ([tokens], bool or uint8): tokens to route.  work: a device buffer of at
+    least ccl_plan_route_work_bytes bytes (allocated here when omitted)."""
+    dev = _on_gpu(logits, ids, weights, lse, counts, load, importance, losses, valid, work)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return ccl_route(logits, ids, weights, lse, counts, load, importance, losses, normalize, valid, work, stream)
+    lp, n, experts, ls = _rows(logits, "logits")
+    ip, tokens, top = _choices(ids, "ids")
+    if tokens != n:
+        raise ValueError("ids has %d tokens, expected %d" % (tokens, n))
+    f32 = torch.float32
+    ptrs = (ip, _flat(weights, "weights", (n, top), f32), _flat(lse, "lse", (n,), f32),
+            _flat(counts, "counts", (experts + 1,), torch.int32), _flat(load, "load", (experts,), f32),
+            _flat(importance, "importance", (experts,), f32), _flat(losses, "losses", (2,), f32))
+    vp = None if valid is None else _flat(valid, "valid", (n,), valid.dtype if valid.dtype == torch.bool else torch.uint8)
+    work, nbytes = _work(work, 0 if work is not None else ccl_plan_route_work_bytes(n, experts), logits, stream)
+    _check(lib().ccl_route(lp, n, experts, ls, _dtype(logits), vp, top, int(bool(normalize)), *ptrs, work.data_ptr(), nbytes,
+                           _stream_on(stream, dev)), "ccl_route")
+
+
+def ccl_route_grad(logits: torch.Tensor, ids: torch.Tensor, lse: torch.Tensor, counts: torch.Tensor, load: torch.Tensor,
+                   grad_weights: torch.Tensor, grad_logits: torch.Tensor, normalize: bool = True, balance: float = 0.0,
+                   z: float = 0.0, stream=None) -> None:
+    """The gradient by the logits of sum grad_weights * weights + balance *
+    losses[0] + z * losses[1], from what ccl_route left (load may have been
+    averaged over the ranks); grad_logits may be `logits` itself."""
+    dev = _on_gpu(logits, ids, lse, counts, load, grad_weights, grad_logits)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return ccl_route_grad(logits, ids, lse, counts, load, grad_weights, grad_logits, normalize, balance, z, stream)
+    lp, n, experts, ls = _rows(logits, "logits")
+    gp, gn, _, gs = _rows(grad_logits, "grad_logits", experts, logits.dtype)
+    ip, tokens, top = _choices(ids, "ids")
+    if tokens != n or gn != n:
+        raise ValueError("ids and grad_logits must have the logits' %d tokens" % n)
+    f32 = torch.float32
+    _check(lib().ccl_route_grad(lp, n, experts, ls, _dtype(logits), ip, top, int(bool(normalize)), _flat(lse, "lse", (n,), f32),
+                                _flat(counts, "counts", (experts + 1,), torch.int32), _flat(load, "load", (experts,), f32),
+                                _flat(grad_weights, "grad_weights", (n, top), f32), float(balance), float(z), gp, gs,
+                                _stream_on(stream, dev)), "ccl_route_grad")
+
+
+def ccl_expert_order(ids: torch.Tensor, offsets: torch.Tensor, place: torch.Tensor, first_expert: int = 0,
+                     work: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The tokens' copies in expert order: place [tokens, top] (int32), the row
+    of each choice, -1 for an id outside [first_expert, first_expert + experts);
+    offsets [experts + 1] (int32), the experts' first rows.  work: a device
+    buffer of at least ccl_plan_expert_order_work_bytes bytes (allocated here
+    when omitted)."""
+    dev = _on_gpu(ids, offsets, place, work)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return ccl_expert_order(ids, offsets, place, first_expert, work, stream)
+    ip, n, top = _choices(ids, "ids")
+    if offsets.dim() != 1 or offsets.numel() < 1:
+        raise ValueError("offsets must be a tensor of shape [experts + 1]")
+    experts = offsets.numel() - 1
+    op, pp = _flat(offsets, "offsets", (experts + 1,), torch.int32), _flat(place, "place", (n, top), torch.int32)
+    work, nbytes = _work(work, 0 if work is not None else ccl_plan_expert_order_work_bytes(n, top, experts), ids, stream)
+    _check(lib().ccl_expert_order(ip, n, top, int(first_expert), experts, op, pp, work.data_ptr(), nbytes,
+                                  _stream_on(stream, dev)), "ccl_expert_order")
+
+
+def ccl_dispatch(x: torch.Tensor, place: torch.Tensor, rows: torch.Tensor, stream=None) -> None:
+    """rows[place[t, s]] = x[t]; rows that no place names stay as they are.  Its
+    gradient is ccl_combine without weights."""
+    dev = _on_gpu(x, place, rows)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return ccl_dispatch(x, place, rows, stream)
+    xp, n, dim, xs = _rows(x, "x")
+    rp, nrows, _, rs = _rows(rows, "rows", dim, x.dtype)
+    pp, tokens, top = _choices(place, "place")
+    if tokens != n:
+        raise ValueError("place has %d tokens, expected %d" % (tokens, n))
+    _check(lib().ccl_dispatch(xp, n, dim, xs, _dtype(x), pp, top, rp, nrows, rs, _stream_on(stream, dev)), "ccl_dispatch")
+
+
+def ccl_combine(rows: torch.Tensor, place: torch.Tensor, out: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                stream=None) -> None:
+    """out[t] = the sum over s of weights[t, s] * rows[place[t, s]] (weights
+    None: 1)."""
+    dev = _on_gpu(rows, place, out, weights)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return ccl_combine(rows, place, out, weights, stream)
+    rp, nrows, dim, rs = _rows(rows, "rows")
+    op, n, _, os_ = _rows(out, "out", dim, rows.dtype)
+    pp, tokens, top = _choices(place, "place")
+    if tokens != n:
+        raise ValueError("place has %d tokens, expected %d" % (tokens, n))
+    _check(lib().ccl_combine(rp, nrows, dim, rs, _dtype(rows), pp, _flat(weights, "weights", (n, top), torch.float32), n, top, op,
+                             os_, _stream_on(stream, dev)), "ccl_combine")
+
+
+def ccl_combine_grad(grad_out: torch.Tensor, place: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                     weights: Optional[torch.Tensor] = None, grad_rows: Optional[torch.Tensor] = None,
+                     grad_weights: Optional[torch.Tensor] = None, stream=None) -> None:
+    """ccl_combine's gradients (those given): grad_rows[place[t, s]] =
+    weights[t, s] * grad_out[t], grad_weights[t, s] = <grad_out[t],
+    rows[place[t, s]]>.  grad_rows may be `rows` itself."""
+    dev = _on_gpu(grad_out, place, rows, weights, grad_rows, grad_weights)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return ccl_combine_grad(grad_out, place, rows, weights, grad_rows, grad_weights, stream)
+    yp, n, dim, ys = _rows(grad_out, "grad_out")
+    pp, tokens, top = _choices(place, "place")
+    if tokens != n:
+        raise ValueError("place has %d tokens, expected %d" % (tokens, n))
+    rp, nrows, rs, gp, gs = None, 0, dim, None, dim
+    if grad_weights is not None and rows is None:
+        raise ValueError("grad_weights needs the rows")
+    if rows is not None:
+        rp, nrows, _, rs = _rows(rows, "rows", dim, grad_out.dtype)
+    if grad_rows is not None:
+        gp, gn, _, gs = _rows(grad_rows, "grad_rows", dim, grad_out.dtype)
+        if rows is not None and gn != nrows:
+            raise ValueError("grad_rows has %d rows, expected %d" % (gn, nrows))
+        nrows = gn
+    _check(lib().ccl_combine_grad(yp, ys, rp, nrows, dim, rs, _dtype(grad_out), pp,
+                                  _flat(weights, "weights", (n, top), torch.float32), n, top, gp, gs,
+                                  _flat(grad_weights, "grad_weights", (n, top), torch.float32), _stream_on(stream, dev)),
+           "ccl_combine_grad")
+
+
+def _act8(pair, name: str, lead, cols: int):
+    """Pointers of (codes, scales) of rows of `cols` values."""
+    width = -(-cols // ACT8_BLOCK) * ACT8_BLOCK
+    codes, scales = pair
+    return (_flat(codes, name + "'s codes", (*lead, width), torch.int8),
+            _flat(scales, name + "'s scales", (*lead, width // ACT8_BLOCK), torch.uint8))
+
+
+def ccl_act8_pack(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    """x's rows in 8 bits: codes [rows, ccl_plan_act8_width(cols)] (int8),
+    scales [rows, width / 32] (uint8), a power of two for each 32 values."""
+    dev = _on_gpu(x, codes, scales)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return ccl_act8_pack(x, codes, scales, stream)
+    xp, n, cols, xs = _rows(x, "x")
+    _check(lib().ccl_act8_pack(xp, n, cols, xs, _dtype(x), *_act8((codes, scales), "x", (n,), cols), _stream_on(stream, dev)),
+           "ccl_act8_pack")
+
+
+def ccl_act8_unpack(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, stream=None) -> None:
+    """The values that ccl_act8_pack kept."""
+    dev = _on_gpu(codes, scales, x)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return ccl_act8_unpack(codes, scales, x, stream)
+    xp, n, cols, xs = _rows(x, "x")
+    _check(lib().ccl_act8_unpack(*_act8((codes, scales), "x", (n,), cols), n, cols, _dtype(x), xp, xs, _stream_on(stream, dev)),
+           "ccl_act8_unpack")
+
+
+def _expert_shapes(rows, offsets, w_gate, w_up, w_down):
+    """Pointers of the offsets and the weights, and the sizes (rows, experts, dim, ffn)."""
+    if rows.dim() != 2 or w_gate.dim() != 3:
+        raise ValueError("the rows are a matrix and the weights are [experts, ., .]")
+    (n, dim), (experts, ffn, _) = rows.shape, w_gate.shape
+    dt = rows.dtype
+    return (_flat(offsets, "offsets", (experts + 1,), torch.int32), _flat(w_gate, "w_gate", (experts, ffn, dim), dt),
+            _flat(w_up, "w_up", (experts, ffn, dim), dt), _flat(w_down, "w_down", (experts, dim, ffn), dt)), (n, experts, dim, ffn)
+
+
+def ccl_expert_ffn(x: torch.Tensor, offsets: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
+                   out: torch.Tensor, act="silu", saved=None, work: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The experts' gated feed-forward blocks: rows [offsets[e], offsets[e + 1])
+    of x through w_gate[e], w_up[e] ([experts, ffn, dim]) and w_down[e]
+    ([experts, dim, ffn]), bfloat16.  offsets ([experts + 1], int32) stays on the
+    device.  saved: (codes [2, rows, ccl_plan_act8_width(ffn)] int8, scales [2,
+    rows, width / 32] uint8), g and u kept in 8 bits for ccl_expert_ffn_grad.
+    work: a device buffer of at least ccl_plan_expert_ffn_work_bytes bytes
+    (allocated here when omitted)."""
+    codes, scales = saved if saved is not None else (None, None)
+    dev = _on_gpu(x, offsets, w_gate, w_up, w_down, out, codes, scales, work)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return ccl_expert_ffn(x, offsets, w_gate, w_up, w_down, out, act, saved, work, stream)
+    (fp, *weights), (n, experts, dim, ffn) = _expert_shapes(x, offsets, w_gate, w_up, w_down)
+    xp, op = _flat(x, "x", (n, dim), x.dtype), _flat(out, "out", (n, dim), x.dtype)
+    sp = (None, None) if saved is None else _act8(saved, "saved", (2, n), ffn)
+    work, nbytes = _work(work, 0 if work is not None else
+                         ccl_plan_expert_ffn_work_bytes(n, experts, dim, ffn, False, all(q % 16 == 0 for q in (xp, *weights))), x,
+                         stream)
+    _check(lib().ccl_expert_ffn(xp, fp, *weights, n, experts, dim, ffn, _dtype(x), _act(act), op, *sp, work.data_ptr(), nbytes,
+                                _stream_on(stream, dev)), "ccl_expert_ffn")
+
+
+def ccl_expert_ffn_grad(grad_out: torch.Tensor, x, offsets: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                        w_down: torch.Tensor, saved, grad_x: Optional[torch.Tensor] = None,
+                        grad_w_gate: Optional[torch.Tensor] = None, grad_w_up: Optional[torch.Tensor] = None,
+                        grad_w_down: Optional[torch.Tensor] = None, act="silu", accumulate: bool = False,
+                        work: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The blocks' gradients (those given), from the saved pre-activations and
+    x: the tensor, or (codes, scales) as ccl_act8_pack keeps it; accumulate adds
+    to the weights' gradients."""
+    eight = not isinstance(x, torch.Tensor)
+    dev = _on_gpu(grad_out, *(x if eight else (x,)), offsets, w_gate, w_up, w_down, *saved, grad_x, grad_w_gate, grad_w_up,
+                  grad_w_down, work)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return ccl_expert_ffn_grad(grad_out, x, offsets, w_gate, w_up, w_down, saved, grad_x, grad_w_gate, grad_w_up,
+                                       grad_w_down, act, accumulate, work, stream)
+    (fp, *weights), (n, experts, dim, ffn) = _expert_shapes(grad_out, offsets, w_gate, w_up, w_down)
+    dt = grad_out.dtype
+    yp = _flat(grad_out, "grad_out", (n, dim), dt)
+    xp = (None, *_act8(x, "x", (n,), dim)) if eight else (_flat(x, "x", (n, dim), dt), None, None)
+    grads = (_flat(grad_x, "grad_x", (n, dim), dt), _flat(grad_w_gate, "grad_w_gate", (experts, ffn, dim), dt),
+             _flat(grad_w_up, "grad_w_up", (experts, ffn, dim), dt), _flat(grad_w_down, "grad_w_down", (experts, dim, ffn), dt))
+    sp = _act8(saved, "saved", (2, n), ffn)
+    work, nbytes = _work(work, 0 if work is not None else
+                         ccl_plan_expert_ffn_work_bytes(n, experts, dim, ffn, True, all(q % 16 == 0 for q in weights)), grad_out,
+                         stream)
+    _check(lib().ccl_expert_ffn_grad(yp, *xp, fp, *weights, *sp, n, experts, dim, ffn, _dtype(grad_out), _act(act),
+                                     int(bool(accumulate)), *grads, work.data_ptr(), nbytes, _stream_on(stream, dev)),
+           "ccl_expert_ffn_grad")
 
 
 # ------------------------------------------------------------------ planner

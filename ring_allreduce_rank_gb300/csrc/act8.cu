@@ -1,0 +1,203 @@
+// act8.cu -- activations kept in 8 bits for the backward pass, and brought back.
+//
+// 9 bits for 8.25 of every 16 or 32: codes [rows][width], a byte a value, and
+// bytes [rows][width / 32], a power of two a block (act8.cuh), width being the
+// columns rounded up to 32, so that every row of codes is whole 32-byte
+// vectors.  Bound by memory bandwidth: each value is read once and written
+// once.  A thread takes a whole block, so that no value crosses lanes; where
+// the source's rows are no whole vectors a warp takes a block, a lane a value,
+// so that its loads still run along the row.
+#include <vector>
+
+#include "../../include/ccl.h"
+#include "act8.cuh"
+#include "ccl_internal.h"
+#include "step_ops.cuh"
+
+namespace ccl {
+namespace {
+
+constexpr uint32_t kActThreads = 256;
+
+struct Act8Params {
+    char *x; // the values' rows, read or written
+    uint8_t *codes, *bytes;
+    uint64_t pitch, blocks; // bytes from row to row; blocks of all rows
+    uint32_t cols, per;     // columns, blocks a row
+};
+
+__device__ __forceinline__ uint64_t row_of(const Act8Params &p, uint64_t i)
+{
+    return p.blocks >> 32 ? i / p.per : (uint32_t)i / p.per;
+}
+
+// 32 consecutive values of a row, 16-byte aligned; those past the row are 0.
+template <int DT> __device__ __forceinline__ void load_block(const char *src, uint32_t n, float *f)
+{
+    constexpr int V = DType<DT>::kVec;
+#pragma unroll
+    for (int i = 0; i < 32 / V; ++i)
+        unpack<DT>((uint32_t)(i * V) < n ? ld16(src + i * 16) : make_uint4(0, 0, 0, 0), f + i * V);
+}
+
+template <int DT, bool VECTOR> __global__ void __launch_bounds__(kActThreads) act8_pack_kernel(Act8Params p)
+{
+    chain_entry();
+    constexpr int es = DType<DT>::kSize;
+    if (VECTOR) {
+        const uint64_t i = (uint64_t)blockIdx.x * kActThreads + threadIdx.x;
+        if (i >= p.blocks)
+            return;
+        const uint64_t r = row_of(p, i);
+        const uint32_t c = (uint32_t)(i - r * p.per) * kActBlock;
+        const char *src = p.x + r * p.pitch + (uint64_t)c * es;
+        float f[32];
+        uint4 lo, hi;
+        load_block<DT>(src, p.cols - c, f);
+        const uint32_t byte = act8_encode(f, lo, hi);
+        st32(p.codes + i * kActBlock, lo, hi);
+        gstore<uint8_t>(p.bytes + i, (uint8_t)byte);
+    } else {
+        const uint32_t lane = threadIdx.x & 31;
+        const uint64_t warps = (uint64_t)gridDim.x * (kActThreads / 32);
+        constexpr int AHEAD = 4;
+        for (uint64_t i0 = (uint64_t)blockIdx.x * (kActThreads / 32) + threadIdx.x / 32; i0 < p.blocks; i0 += AHEAD * warps) {
+            float f[AHEAD];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const uint64_t i = i0 + j * warps;
+                f[j] = 0.0f;
+                if (i < p.blocks) {
+                    const uint64_t r = row_of(p, i);
+                    const uint32_t c = (uint32_t)(i - r * p.per) * kActBlock + lane;
+                    if (c < p.cols)
+                        f[j] = ld_value<DT>(p.x + r * p.pitch, c);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const uint64_t i = i0 + j * warps;
+                const uint32_t byte = act8_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(f[j]) & 0x7fffffffu));
+                if (i < p.blocks) {
+                    gstore<uint8_t>(p.codes + i * kActBlock + lane, byte == kActNan ? 0 : (uint8_t)act8_code(f[j], act8_inverse(byte)));
+                    if (lane == 0)
+                        gstore<uint8_t>(p.bytes + i, (uint8_t)byte);
+                }
+            }
+        }
+    }
+}
+
+template <int DT, bool VECTOR> __global__ void __launch_bounds__(kActThreads) act8_unpack_kernel(Act8Params p)
+{
+    chain_entry();
+    constexpr int es = DType<DT>::kSize, V = DType<DT>::kVec;
+    if (VECTOR) {
+        const uint64_t i = (uint64_t)blockIdx.x * kActThreads + threadIdx.x;
+        if (i >= p.blocks)
+            return;
+        const uint64_t r = row_of(p, i);
+        const uint32_t c = (uint32_t)(i - r * p.per) * kActBlock;
+        char *dst = p.x + r * p.pitch + (uint64_t)c * es;
+        uint4 lo, hi;
+        ld32(p.codes + i * kActBlock, lo, hi);
+        float f[32];
+        act8_decode(lo, hi, act8_step(gload<uint8_t>(p.bytes + i)), f);
+#pragma unroll
+        for (int j = 0; j < 32 / V; ++j)
+            if ((uint32_t)(j * V) < p.cols - c)
+                st16(dst + j * 16, pack<DT>(f + j * V));
+    } else {
+        const uint32_t lane = threadIdx.x & 31;
+        const uint64_t warps = (uint64_t)gridDim.x * (kActThreads / 32);
+        for (uint64_t i = (uint64_t)blockIdx.x * (kActThreads / 32) + threadIdx.x / 32; i < p.blocks; i += warps) {
+            const uint64_t r = row_of(p, i);
+            const uint32_t c = (uint32_t)(i - r * p.per) * kActBlock + lane;
+            const float q = (float)(int8_t)gload<uint8_t>(p.codes + i * kActBlock + lane);
+            if (c < p.cols)
+                st_value<DT>(p.x + r * p.pitch, c, __fmul_rn(q, act8_step(gload<uint8_t>(p.bytes + i))));
+        }
+    }
+}
+
+constexpr size_t kMaxRows = 0x7fffffff, kMaxCols = (size_t)1 << 24;
+
+ccl_status_t act8_impl(bool pack, const void *x, size_t rows, size_t cols, size_t stride, ccl_dtype_t dtype, const void *codes, const void *bytes,
+                       cudaStream_t stream)
+{
+    if (!valid_dtype(dtype) || stride < cols || rows > kMaxRows || cols > kMaxCols)
+        return CCL_ERR_INVALID_ARG;
+    const size_t es = elem_size(dtype), per = (cols + kActBlock - 1) / kActBlock;
+    size_t xb;
+    if (!extent(rows, cols, stride, es, &xb))
+        return CCL_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0)
+        return CCL_OK;
+    if (!x || !codes || !bytes || !element_aligned(es, {x}) || !element_aligned(32, {codes}))
+        return CCL_ERR_INVALID_ARG;
+    const Range a = range_of(x, xb, 0), b = range_of(codes, rows * per * kActBlock, 0), c = range_of(bytes, rows * per, 0);
+    const std::vector<Range> w = pack ? std::vector<Range>{b, c} : std::vector<Range>{a}, r = pack ? std::vector<Range>{a} : std::vector<Range>{b, c};
+    if (ccl_status_t st = check_overlaps(w, r, [](const Range &, const Range &) { return false; }))
+        return st;
+#ifdef CCL_DEBUG_BOUNDS
+    if (cudaError_t e = dbg_set_ranges({{x, xb}, {codes, rows * per * kActBlock}, {bytes, rows * per}}, stream))
+        return from_cuda(e);
+#endif
+    Act8Params p{};
+    p.x = static_cast<char *>(const_cast<void *>(x));
+    p.codes = static_cast<uint8_t *>(const_cast<void *>(codes));
+    p.bytes = static_cast<uint8_t *>(const_cast<void *>(bytes));
+    p.pitch = stride * es;
+    p.blocks = (uint64_t)rows * per;
+    p.cols = (uint32_t)cols;
+    p.per = (uint32_t)per;
+    const bool vec = ((uintptr_t)x | p.pitch | cols * es) % 16 == 0;
+    // a thread a block: the grid's 2^31 CTAs hold 2^39 of them, and 2^31 rows of 2^24 columns have 2^50
+    if (vec && p.blocks > (uint64_t)0x7fffffff * kActThreads)
+        return CCL_ERR_INVALID_ARG;
+    const uint64_t per_cta = vec ? kActThreads : kActThreads / 32;
+    const uint64_t ctas = (p.blocks + per_cta - 1) / per_cta;
+    const dim3 grid((unsigned)(vec ? ctas : std::min<uint64_t>(ctas, 8 * 152))), block(kActThreads);
+    void (*k)(Act8Params);
+    if (pack)
+        k = dtype == CCL_FP32 ? (vec ? act8_pack_kernel<DT_FP32, true> : act8_pack_kernel<DT_FP32, false>)
+                              : (vec ? act8_pack_kernel<DT_BF16, true> : act8_pack_kernel<DT_BF16, false>);
+    else
+        k = dtype == CCL_FP32 ? (vec ? act8_unpack_kernel<DT_FP32, true> : act8_unpack_kernel<DT_FP32, false>)
+                              : (vec ? act8_unpack_kernel<DT_BF16, true> : act8_unpack_kernel<DT_BF16, false>);
+    const cudaError_t e = launch_chained(k, grid, block, 0, stream, p);
+    if (e == cudaSuccess)
+        count_launches(1);
+    return from_cuda(e);
+}
+
+} // namespace
+} // namespace ccl
+
+using namespace ccl;
+
+extern "C" {
+
+ccl_status_t ccl_plan_act8_width(size_t cols, size_t *width)
+{
+    if (!width || cols > kMaxCols)
+        return CCL_ERR_INVALID_ARG;
+    *width = (cols + kActBlock - 1) / kActBlock * kActBlock;
+    return CCL_OK;
+}
+
+ccl_status_t ccl_act8_pack(const void *x, size_t rows, size_t cols, size_t x_stride, ccl_dtype_t dtype, int8_t *codes, uint8_t *scales,
+                           cudaStream_t stream)
+{
+    TraceScope tr("act8_pack", 1, rows, (int)dtype, -1, 0, stream);
+    return tr.done(guarded([&] { return act8_impl(true, x, rows, cols, x_stride, dtype, codes, scales, stream); }));
+}
+
+ccl_status_t ccl_act8_unpack(const int8_t *codes, const uint8_t *scales, size_t rows, size_t cols, ccl_dtype_t dtype, void *x, size_t x_stride,
+                             cudaStream_t stream)
+{
+    TraceScope tr("act8_unpack", 1, rows, (int)dtype, -1, 0, stream);
+    return tr.done(guarded([&] { return act8_impl(false, x, rows, cols, x_stride, dtype, codes, scales, stream); }));
+}
+
+} // extern "C"

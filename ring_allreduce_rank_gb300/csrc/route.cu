@@ -1,0 +1,704 @@
+// route.cu -- the router of a mixture of experts: the top choices of every
+// token's softmax over the experts, the experts' counts, the balance and z
+// losses, and the gradient by the logits.
+//
+//   p = softmax(z), ids = the top largest z (ties: the lower expert), w = p_ids
+//   or p_ids / sum p_ids, load_e = choices of e / choices, importance_e = mean
+//   of p_e, balance = E sum_e load_e importance_e, zloss = mean of lse^2.
+//   dz_j = p_j (G_j - sum_i G_i p_i + 2 c_z lse / n),
+//   G_j = c_b E load_j / n + [j chosen] g_j, with g = grad_w, or for normalised
+//   weights g_i = (grad_w_i - sum_m grad_w_m w_m) / sum_top p.
+//
+// A group of 8 or 32 lanes holds a row in registers, reads it once, takes its
+// maximum, sum and choices from there, and adds its p to sums of its own
+// columns, so that the importance costs no further pass.  A choice is a
+// reduction of (ordered bits, expert) over the group, and its holder looks for
+// its next best only then.  Sums over the tokens are the groups' rows in order,
+// the groups of a CTA in order, the CTAs in order: no float is added by an
+// atomic.  Bound by memory bandwidth for many tokens, by the launch and one
+// row's chain of reductions for few.
+#include <vector>
+
+#include "../../include/ccl.h"
+#include "ccl_internal.h"
+#include "step_ops.cuh"
+
+namespace ccl {
+namespace {
+
+constexpr size_t kMaxTokens = 0x7fffffff;
+constexpr int kRouteThreads = 256;
+constexpr uint32_t kRouteCtas = 4 * 152; // at most; each leaves a row of partial sums
+
+struct RouteParams {
+    const char *logits;
+    char *grad;
+    uint64_t pitch, grad_pitch; // bytes
+    const uint8_t *valid;
+    int32_t *ids;
+    float *weights, *lse;
+    int32_t *counts;
+    float *load, *importance, *loss;
+    float *sums;     // partial: [ctas][experts + 1], the last one of lse^2
+    int32_t *hits;   // partial: [ctas][experts + 1], the last one of routed tokens
+    const float *grad_weights;
+    float balance, z; // the losses' coefficients
+    uint32_t ntokens, experts, top, ctas;
+    int normalize, vector;
+};
+
+// A float's bits in an order of unsigned numbers: both zeros equal, any NaN
+// above +inf.
+__device__ __forceinline__ uint32_t ordered(float f)
+{
+    const uint32_t b = __float_as_uint(__fadd_rn(f, 0.0f)); // -0 + 0 = 0
+    if ((b & 0x7fffffffu) > 0x7f800000u)
+        return 0xffffffffu;
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+constexpr uint32_t kNothing = 0x007fffffu; // ordered(-inf)
+
+__device__ __forceinline__ float from_ordered(uint32_t k)
+{
+    return __uint_as_float(k == 0xffffffffu ? 0x7fffffffu : k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+template <int L> __device__ __forceinline__ float group_sum(float v)
+{
+#pragma unroll
+    for (int d = L / 2; d; d /= 2)
+        v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+}
+
+template <int L> __device__ __forceinline__ uint32_t group_max(uint32_t v)
+{
+    if (L == 32)
+        return __reduce_max_sync(0xffffffffu, v);
+#pragma unroll
+    for (int d = L / 2; d; d /= 2)
+        v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+}
+
+template <int L> __device__ __forceinline__ uint32_t group_min(uint32_t v)
+{
+    if (L == 32)
+        return __reduce_min_sync(0xffffffffu, v);
+#pragma unroll
+    for (int d = L / 2; d; d /= 2)
+        v = min(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+}
+
+// Column of a lane's i-th value: vectors of N side by side, so that a group's
+// loads run along the row.
+template <int L, int N> __device__ __forceinline__ uint32_t column(uint32_t lane, int i) { return (i / N) * (L * N) + lane * N + i % N; }
+
+// A lane's V values of a row; columns past the experts are -inf.
+template <int DT, int L, int V, int N> __device__ __forceinline__ void load_row(const RouteParams &p, const char *row, uint32_t lane, float *f)
+{
+    if (N > 1) {
+#pragma unroll
+        for (int i = 0; i < V; i += N) {
+            const uint32_t c = column<L, N>(lane, i);
+            const bool in = c < p.experts;
+            const char *at = row + (uint64_t)c * DType<DT>::kSize;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (in && N * DType<DT>::kSize == 16) {
+                v = ld16(at);
+            } else if (in && N * DType<DT>::kSize == 8) {
+                const uint2 w = gload<uint2>(at);
+                v.x = w.x;
+                v.y = w.y;
+            } else if (in) {
+                v.x = gload<uint32_t>(at);
+            }
+            float h[DType<DT>::kVec];
+            unpack<DT>(v, h);
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                f[i + k] = h[k];
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                f[i + k] = in ? f[i + k] : -INFINITY;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t c = column<L, 1>(lane, i);
+            f[i] = c < p.experts ? ld_value<DT>(row, c) : -INFINITY;
+        }
+    }
+}
+
+// What the launch's last CTA, or the second launch, makes of the partial sums.
+__device__ __forceinline__ void finish_losses(const RouteParams &p, float *sums, int32_t *hits, float *shared)
+{
+    // sums and hits: [experts + 1] in shared memory, complete
+    const uint32_t E = p.experts;
+    const float n = fmaxf((float)hits[E], 1.0f);
+    long long all = 0;
+    // every thread of the first warp sums the counts of its experts, then they are joined
+    const uint32_t lane = threadIdx.x & 31;
+    if (threadIdx.x < 32) {
+        for (uint32_t e = lane; e < E; e += 32)
+            all += hits[e];
+#pragma unroll
+        for (int d = 16; d; d /= 2)
+            all += __shfl_xor_sync(0xffffffffu, all, d);
+        if (lane == 0)
+            shared[0] = __fdiv_rn(1.0f, (float)(all > 0 ? all : 1));
+    }
+    __syncthreads();
+    const float inv = shared[0];
+    __syncthreads();
+    for (uint32_t e = threadIdx.x; e < E; e += blockDim.x) {
+        const float load = __fmul_rn((float)hits[e], inv), importance = __fdiv_rn(sums[e], n);
+        gstore<int32_t>(p.counts + e, hits[e]);
+        gstore<float>(p.load + e, load);
+        gstore<float>(p.importance + e, importance);
+        sums[e] = __fmul_rn(load, importance);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        float b = 0.0f;
+        for (uint32_t e = lane; e < E; e += 32)
+            b = __fadd_rn(b, sums[e]);
+        b = group_sum<32>(b);
+        if (lane == 0) {
+            gstore<int32_t>(p.counts + E, hits[E]);
+            gstore<float>(p.loss, __fmul_rn((float)E, b));
+            gstore<float>(p.loss + 1, __fdiv_rn(sums[E], n));
+        }
+    }
+}
+
+// L lanes a row, V values a lane, loads of N values.
+template <int DT, int L, int V, int N> __global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_constant__ RouteParams p)
+{
+    chain_entry();
+    constexpr int kGroups = kRouteThreads / L;
+    extern __shared__ float shared[]; // sums [experts + 1], hits [experts + 1]
+    __shared__ float squares[kGroups];
+    __shared__ int32_t routed[kGroups];
+    __shared__ float scratch;
+    const uint32_t E = p.experts;
+    float *sums = shared;
+    int32_t *hits = reinterpret_cast<int32_t *>(shared + E + 1);
+    const uint32_t lane = threadIdx.x % L, group = threadIdx.x / L;
+    for (uint32_t e = threadIdx.x; e <= E; e += kRouteThreads)
+        hits[e] = 0;
+    __syncthreads();
+    float acc[V], square = 0.0f;
+    int32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        acc[i] = 0.0f;
+    const uint32_t stride = p.ctas * kGroups;
+    // whole warps go round together: rows past the last are rows without experts
+    const uint32_t rounds = (p.ntokens + stride - 1) / stride;
+    float f[V];
+    auto fetch = [&](uint32_t round, float *v, bool &is) {
+        const uint64_t t = (uint64_t)round * stride + blockIdx.x * kGroups + group;
+        is = round < rounds && t < p.ntokens && (!p.valid || gload<uint8_t>(p.valid + t));
+        if (is)
+            load_row<DT, L, V, N>(p, p.logits + t * p.pitch, lane, v);
+    };
+    bool is;
+    fetch(0, f, is);
+    for (uint32_t round = 0; round < rounds; ++round) {
+        const uint64_t t = (uint64_t)round * stride + blockIdx.x * kGroups + group;
+        float next[V];
+        bool next_is;
+        fetch(round + 1, next, next_is);
+        // the lane's best, and the row's
+        float m = -INFINITY;
+        uint32_t best = kNothing, at = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            f[i] = is ? f[i] : -INFINITY;
+            const uint32_t k = ordered(f[i]);
+            if (k > best) { // columns rise with i: the first of equals stays
+                best = k;
+                at = i;
+            }
+            m = fmaxf(m, f[i]);
+        }
+        const uint32_t top = group_max<L>(best);
+        const bool live = top > kNothing;
+        float total = 0.0f;
+        if (L == 32) {
+            m = top == 0xffffffffu ? m : from_ordered(top);
+            if (top == 0xffffffffu)
+                m = 0.0f; // a NaN in the row makes its sum NaN whatever is taken off
+        } else {
+#pragma unroll
+            for (int d = L / 2; d; d /= 2)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        }
+        float e[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            e[i] = live ? expf(__fsub_rn(f[i], m)) : 0.0f;
+            total = __fadd_rn(total, e[i]);
+        }
+        total = group_sum<L>(total);
+        const float inv = live ? __fdiv_rn(1.0f, total) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            acc[i] = __fmaf_rn(e[i], inv, acc[i]);
+        const float lse = live ? __fadd_rn(m, logf(total)) : 0.0f;
+        // the choices, one a step; lane s keeps the s-th (and s + L, ...)
+        float kept = 0.0f;
+        constexpr int kMine = (CCL_MAX_EXPERT_TOP + L - 1) / L;
+        float mine[kMine];
+        int32_t id[kMine];
+#pragma unroll
+        for (int s0 = 0; s0 < kMine; ++s0)
+            if (s0 * L < p.top) {
+                mine[s0] = 0.0f;
+                id[s0] = -1;
+                for (uint32_t s = 0; s < L && s0 * L + s < p.top; ++s) {
+                    const uint32_t k = group_max<L>(best);
+                    const uint32_t c = best == k ? column<L, N>(lane, at) : 0xffffffffu;
+                    const uint32_t chosen = group_min<L>(c);
+                    const bool some = k > kNothing;
+                    if (c == chosen && some) { // this lane's: out of the running, and its next best
+                        atomicAdd(&hits[chosen], 1); // whole numbers: any order gives the same count
+                        best = kNothing;
+                        uint32_t was = at;
+                        at = 0;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            if ((uint32_t)i == was)
+                                f[i] = -INFINITY;
+                            const uint32_t o = ordered(f[i]);
+                            if (o > best) {
+                                best = o;
+                                at = i;
+                            }
+                        }
+                    }
+                    const float w = some ? expf(__fsub_rn(from_ordered(k), m)) : 0.0f;
+                    kept = __fadd_rn(kept, w);
+                    if (lane == s) {
+                        mine[s0] = w;
+                        id[s0] = some ? (int32_t)chosen : -1;
+                    }
+                }
+            }
+        const float by = !live ? 0.0f : p.normalize ? __fdiv_rn(1.0f, kept) : inv;
+        if (t < p.ntokens) {
+#pragma unroll
+            for (int s0 = 0; s0 < kMine; ++s0) {
+                const uint32_t s = s0 * L + lane;
+                if (s < p.top) {
+                    gstore<int32_t>(p.ids + t * p.top + s, id[s0]);
+                    gstore<float>(p.weights + t * p.top + s, id[s0] < 0 ? 0.0f : __fmul_rn(mine[s0], by));
+                }
+            }
+            if (lane == 0)
+                gstore<float>(p.lse + t, lse);
+        }
+        square = __fmaf_rn(lse, lse, square);
+        n += live;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            f[i] = next[i];
+        is = next_is;
+    }
+    // the CTA's sums, its groups in order
+    if (lane == 0) {
+        squares[group] = square;
+        routed[group] = n;
+    }
+    for (int g = 0; g < kGroups; ++g) {
+        __syncthreads();
+        if (group == (uint32_t)g) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t c = column<L, N>(lane, i);
+                if (c < E)
+                    sums[c] = g ? __fadd_rn(sums[c], acc[i]) : acc[i];
+            }
+        }
+    }
+    if (threadIdx.x == 0) {
+        float s = 0.0f;
+        int32_t r = 0;
+        for (int g = 0; g < kGroups; ++g) {
+            s = __fadd_rn(s, squares[g]);
+            r += routed[g];
+        }
+        sums[E] = s;
+        hits[E] = r;
+    }
+    __syncthreads();
+    if (p.ctas == 1) {
+        finish_losses(p, sums, hits, &scratch);
+        return;
+    }
+    for (uint32_t e = threadIdx.x; e <= E; e += kRouteThreads) {
+        gstore<float>(p.sums + (uint64_t)blockIdx.x * (E + 1) + e, sums[e]);
+        gstore<int32_t>(p.hits + (uint64_t)blockIdx.x * (E + 1) + e, hits[e]);
+    }
+}
+
+// The CTAs' partial sums: 1024 / columns threads a column take runs of the CTAs
+// in order, and the runs are joined in order.
+__global__ void __launch_bounds__(1024) route_join_kernel(const __grid_constant__ RouteParams p)
+{
+    chain_entry();
+    extern __shared__ float shared[]; // sums, hits [parts][experts + 1]
+    __shared__ float scratch;
+    const uint32_t n = p.experts + 1, parts = max(1024u / n, 1u), part = threadIdx.x / n;
+    float *sums = shared;
+    int32_t *hits = reinterpret_cast<int32_t *>(shared + parts * n);
+    const uint32_t run = (p.ctas + parts - 1) / parts;
+    for (uint32_t c = n <= 1024 ? threadIdx.x % n : threadIdx.x; part < parts && c < n; c += 1024) {
+        float s = 0.0f;
+        int32_t h = 0;
+        const uint32_t b1 = min((part + 1) * run, p.ctas);
+        for (uint32_t b0 = part * run; b0 < b1; b0 += 8) {
+            float x[8];
+            int32_t y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint64_t at = (uint64_t)(b0 + j) * n + c;
+                x[j] = b0 + j < b1 ? gload<float>(p.sums + at) : 0.0f;
+                y[j] = b0 + j < b1 ? gload<int32_t>(p.hits + at) : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                s = __fadd_rn(s, x[j]);
+                h += y[j];
+            }
+        }
+        sums[part * n + c] = s;
+        hits[part * n + c] = h;
+    }
+    __syncthreads();
+    for (uint32_t c = threadIdx.x; c < n; c += 1024) {
+        float s = sums[c];
+        int32_t h = hits[c];
+        for (uint32_t k = 1; k < parts; ++k) {
+            s = __fadd_rn(s, sums[k * n + c]);
+            h += hits[k * n + c];
+        }
+        sums[c] = s;
+        hits[c] = h;
+    }
+    __syncthreads();
+    finish_losses(p, sums, hits, &scratch);
+}
+
+template <int DT, int L, int V, int N> __global__ void __launch_bounds__(kRouteThreads) route_grad_kernel(const __grid_constant__ RouteParams p)
+{
+    chain_entry();
+    extern __shared__ float pull[]; // balance * experts / n * load
+    constexpr int kGroups = kRouteThreads / L;
+    const uint32_t lane = threadIdx.x % L, group = threadIdx.x / L, E = p.experts;
+    const float n = fmaxf((float)gload<int32_t>(p.counts + E), 1.0f);
+    const float b = __fdiv_rn(__fmul_rn(p.balance, (float)E), n);
+    for (uint32_t e = threadIdx.x; e < E; e += kRouteThreads)
+        pull[e] = __fmul_rn(b, gload<float>(p.load + e));
+    __syncthreads();
+    const float cz = __fdiv_rn(__fmul_rn(2.0f, p.z), n);
+    const uint32_t stride = gridDim.x * kGroups, rounds = (p.ntokens + stride - 1) / stride;
+    for (uint32_t round = 0; round < rounds; ++round) {
+        const uint64_t t = (uint64_t)round * stride + blockIdx.x * kGroups + group;
+        const bool in = t < p.ntokens;
+        constexpr int kMine = (CCL_MAX_EXPERT_TOP + L - 1) / L;
+        int32_t id[kMine];
+        float g[kMine], q[kMine];
+        bool any = false;
+#pragma unroll
+        for (int s0 = 0; s0 < kMine; ++s0) {
+            const uint32_t s = s0 * L + lane;
+            id[s0] = in && s < p.top ? gload<int32_t>(p.ids + t * p.top + s) : -1;
+            if ((uint32_t)id[s0] >= E)
+                id[s0] = -1;
+            g[s0] = id[s0] >= 0 ? gload<float>(p.grad_weights + t * p.top + s) : 0.0f;
+            any |= id[s0] >= 0;
+        }
+        const bool live = group_max<L>(any ? 1u : 0u);
+        const float lse = live ? gload<float>(p.lse + t) : 0.0f;
+        const char *row = p.logits + (live ? t : 0) * p.pitch;
+        float f[V];
+        if (live)
+            load_row<DT, L, V, N>(p, row, lane, f);
+        float kept = 0.0f, gw = 0.0f;
+#pragma unroll
+        for (int s0 = 0; s0 < kMine; ++s0) {
+            q[s0] = id[s0] >= 0 ? expf(__fsub_rn(ld_value<DT>(row, (uint32_t)id[s0]), lse)) : 0.0f;
+            kept = __fadd_rn(kept, q[s0]);
+            gw = __fmaf_rn(g[s0], q[s0], gw);
+        }
+        kept = group_sum<L>(kept);
+        gw = group_sum<L>(gw);
+        if (p.normalize && live) {
+            const float inv = __fdiv_rn(1.0f, kept), mean = __fmul_rn(gw, inv);
+#pragma unroll
+            for (int s0 = 0; s0 < kMine; ++s0)
+                g[s0] = id[s0] >= 0 ? __fmul_rn(__fsub_rn(g[s0], mean), inv) : 0.0f;
+        }
+        float inner = 0.0f;
+#pragma unroll
+        for (int s0 = 0; s0 < kMine; ++s0)
+            inner = __fmaf_rn(g[s0], q[s0], inner);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t c = column<L, N>(lane, i);
+            f[i] = live && c < E ? expf(__fsub_rn(f[i], lse)) : 0.0f;
+            inner = __fmaf_rn(c < E ? pull[c] : 0.0f, f[i], inner);
+        }
+        inner = group_sum<L>(inner);
+        const float off = __fmaf_rn(cz, lse, -inner);
+        if (in) {
+            char *out = p.grad + t * p.grad_pitch;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t c = column<L, N>(lane, i);
+                f[i] = c < E ? __fmul_rn(f[i], __fadd_rn(pull[c], off)) : 0.0f;
+            }
+            if (N > 1) {
+#pragma unroll
+                for (int i = 0; i < V; i += N) {
+                    const uint32_t c = column<L, N>(lane, i);
+                    if (c < E) {
+                        char *at = out + (uint64_t)c * DType<DT>::kSize;
+                        float h[DType<DT>::kVec];
+#pragma unroll
+                        for (int k = 0; k < DType<DT>::kVec; ++k)
+                            h[k] = k < N ? f[i + (k < N ? k : 0)] : 0.0f;
+                        const uint4 v = pack<DT>(h);
+                        if (N * DType<DT>::kSize == 16)
+                            st16(at, v);
+                        else if (N * DType<DT>::kSize == 8)
+                            gstore<uint2>(at, make_uint2(v.x, v.y));
+                        else
+                            gstore<uint32_t>(at, v.x);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const uint32_t c = column<L, 1>(lane, i);
+                    if (c < E)
+                        st_value<DT>(out, c, f[i]);
+                }
+            }
+        }
+        __syncwarp();
+        // the chosen experts' entries again, with what their weights' gradients add
+        if (in) {
+            char *out = p.grad + t * p.grad_pitch;
+#pragma unroll
+            for (int s0 = 0; s0 < kMine; ++s0)
+                if (id[s0] >= 0)
+                    st_value<DT>(out, (uint32_t)id[s0], __fmul_rn(q[s0], __fadd_rn(__fadd_rn(pull[id[s0]], g[s0]), off)));
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+struct RoutePlan {
+    uint32_t lanes, ctas;
+    size_t sums, bytes;
+};
+
+bool plan_route(size_t ntokens, size_t experts, RoutePlan *p)
+{
+    if (ntokens > kMaxTokens || experts == 0 || experts > CCL_MAX_EXPERTS)
+        return false;
+    *p = RoutePlan{};
+    p->lanes = experts <= 64 ? 8 : 32;
+    const size_t groups = kRouteThreads / p->lanes;
+    // one CTA for a few rounds of rows: it needs no second launch
+    const size_t ctas = (ntokens + groups - 1) / groups;
+    p->ctas = ctas <= 2 ? 1 : (uint32_t)std::min<size_t>(ctas, kRouteCtas);
+    if (p->ctas > 1) {
+        p->sums = up(p->ctas * (experts + 1) * 4);
+        p->bytes = 2 * p->sums;
+    }
+    return true;
+}
+
+template <int DT, int L, int V, bool GRAD> cudaError_t launch_route3(const RouteParams &p, unsigned ctas, cudaStream_t stream)
+{
+    constexpr int N = V < DType<DT>::kVec ? V : DType<DT>::kVec;
+    const size_t smem = GRAD ? p.experts * 4 : (p.experts + 1) * 8;
+    void (*const vec)(RouteParams) = GRAD ? route_grad_kernel<DT, L, V, N> : route_kernel<DT, L, V, N>;
+    void (*const one)(RouteParams) = GRAD ? route_grad_kernel<DT, L, V, 1> : route_kernel<DT, L, V, 1>;
+    const uintptr_t all = (uintptr_t)p.logits | p.pitch | p.experts * DType<DT>::kSize | (GRAD ? (uintptr_t)p.grad | p.grad_pitch : 0);
+    return launch_chained(all % (N * DType<DT>::kSize) == 0 ? vec : one, dim3(ctas), dim3(kRouteThreads), smem, stream, p);
+}
+
+template <int DT, bool GRAD> cudaError_t launch_route2(const RouteParams &p, unsigned ctas, cudaStream_t stream)
+{
+    if (p.experts <= 16)
+        return launch_route3<DT, 8, 2, GRAD>(p, ctas, stream);
+    if (p.experts <= 64)
+        return launch_route3<DT, 8, 8, GRAD>(p, ctas, stream);
+    if (p.experts <= 256)
+        return launch_route3<DT, 32, 8, GRAD>(p, ctas, stream);
+    return launch_route3<DT, 32, 32, GRAD>(p, ctas, stream);
+}
+
+template <bool GRAD> cudaError_t launch_route(ccl_dtype_t dtype, const RouteParams &p, unsigned ctas, cudaStream_t stream)
+{
+    const cudaError_t e = dtype == CCL_FP32 ? launch_route2<DT_FP32, GRAD>(p, ctas, stream) : launch_route2<DT_BF16, GRAD>(p, ctas, stream);
+    if (e == cudaSuccess)
+        count_launches(1);
+    return e;
+}
+
+ccl_status_t route_impl(const void *logits, size_t ntokens, size_t experts, size_t stride, ccl_dtype_t dtype, const uint8_t *valid, size_t top,
+                        int normalize, int32_t *ids, float *weights, float *lse, int32_t *counts, float *load, float *importance, float *loss,
+                        void *work, size_t work_bytes, cudaStream_t stream)
+{
+    RoutePlan pl;
+    size_t lb;
+    if (!valid_dtype(dtype) || !plan_route(ntokens, experts, &pl) || stride < experts || top == 0 || top > experts || top > CCL_MAX_EXPERT_TOP ||
+        !extent(ntokens, experts, stride, elem_size(dtype), &lb))
+        return CCL_ERR_INVALID_ARG;
+    if (!counts || !load || !importance || !loss || (ntokens && (!logits || !lse || !ids || !weights)) ||
+        !element_aligned(elem_size(dtype), {logits}) || !element_aligned(4, {ids, weights, lse, counts, load, importance, loss}) ||
+        (pl.bytes && (!work || (uintptr_t)work % 256 || work_bytes < pl.bytes)))
+        return CCL_ERR_INVALID_ARG;
+    const size_t choices = ntokens * top;
+    const std::vector<Range> w{range_of(ids, choices * 4, 0), range_of(weights, choices * 4, 0), range_of(lse, ntokens * 4, 0),
+                               range_of(counts, (experts + 1) * 4, 0), range_of(load, experts * 4, 0), range_of(importance, experts * 4, 0),
+                               range_of(loss, 8, 0), range_of(work, pl.bytes, 0)},
+        r{range_of(logits, lb, 0), range_of(valid, valid ? ntokens : 0, 0)};
+    if (ccl_status_t st = check_overlaps(w, r, [](const Range &, const Range &) { return false; }))
+        return st;
+#ifdef CCL_DEBUG_BOUNDS
+    std::vector<DbgRange> rg;
+    for (const std::vector<Range> *v : {&w, &r})
+        for (const Range &x : *v)
+            rg.push_back(DbgRange{reinterpret_cast<const void *>(x.lo), (size_t)(x.hi - x.lo)});
+    if (cudaError_t e = dbg_set_ranges(rg, stream))
+        return from_cuda(e);
+#endif
+    RouteParams p{};
+    p.logits = static_cast<const char *>(logits);
+    p.pitch = stride * elem_size(dtype);
+    p.valid = valid;
+    p.ids = ids;
+    p.weights = weights;
+    p.lse = lse;
+    p.counts = counts;
+    p.load = load;
+    p.importance = importance;
+    p.loss = loss;
+    p.sums = static_cast<float *>(work);
+    p.hits = reinterpret_cast<int32_t *>(static_cast<char *>(work) + pl.sums);
+    p.ntokens = (uint32_t)ntokens;
+    p.experts = (uint32_t)experts;
+    p.top = (uint32_t)top;
+    p.ctas = pl.ctas;
+    p.normalize = normalize != 0;
+    cudaError_t e = launch_route<false>(dtype, p, pl.ctas, stream);
+    if (e == cudaSuccess && pl.ctas > 1) {
+        const size_t n = experts + 1, parts = std::max<size_t>(1024 / n, 1);
+        e = launch_chained(route_join_kernel, dim3(1), dim3(1024), parts * n * 8, stream, p);
+        if (e == cudaSuccess)
+            count_launches(1);
+    }
+    return from_cuda(e);
+}
+
+ccl_status_t route_grad_impl(const void *logits, size_t ntokens, size_t experts, size_t stride, ccl_dtype_t dtype, const int32_t *ids, size_t top,
+                             int normalize, const float *lse, const int32_t *counts, const float *load, const float *grad_weights, float balance,
+                             float z, void *grad, size_t grad_stride, cudaStream_t stream)
+{
+    RoutePlan pl;
+    size_t lb, gb;
+    const size_t es = elem_size(dtype);
+    if (!valid_dtype(dtype) || !plan_route(ntokens, experts, &pl) || stride < experts || grad_stride < experts || top == 0 || top > experts ||
+        top > CCL_MAX_EXPERT_TOP || !extent(ntokens, experts, stride, es, &lb) || !extent(ntokens, experts, grad_stride, es, &gb) ||
+        balance != balance || z != z)
+        return CCL_ERR_INVALID_ARG;
+    if (ntokens == 0)
+        return CCL_OK;
+    if (!logits || !grad || !lse || !counts || !load || !ids || !grad_weights || !element_aligned(es, {logits, grad}) ||
+        !element_aligned(4, {ids, lse, counts, load, grad_weights}))
+        return CCL_ERR_INVALID_ARG;
+    const size_t choices = ntokens * top;
+    // in place: the gradient may take the logits' place, row by row
+    const bool in_place = grad == logits && grad_stride == stride;
+    const std::vector<Range> w{range_of(grad, gb, 1)},
+        r{range_of(logits, lb, 1), range_of(ids, choices * 4, 0), range_of(lse, ntokens * 4, 0), range_of(counts, (experts + 1) * 4, 0),
+          range_of(load, experts * 4, 0), range_of(grad_weights, choices * 4, 0)};
+    if (ccl_status_t st = check_overlaps(w, r, [&](const Range &x, const Range &y) { return in_place && x.rank == 1 && y.rank == 1; }))
+        return st;
+#ifdef CCL_DEBUG_BOUNDS
+    std::vector<DbgRange> rg;
+    for (const std::vector<Range> *v : {&w, &r})
+        for (const Range &x : *v)
+            rg.push_back(DbgRange{reinterpret_cast<const void *>(x.lo), (size_t)(x.hi - x.lo)});
+    if (cudaError_t e = dbg_set_ranges(rg, stream))
+        return from_cuda(e);
+#endif
+    RouteParams p{};
+    p.logits = static_cast<const char *>(logits);
+    p.pitch = stride * es;
+    p.grad = static_cast<char *>(grad);
+    p.grad_pitch = grad_stride * es;
+    p.ids = const_cast<int32_t *>(ids);
+    p.lse = const_cast<float *>(lse);
+    p.counts = const_cast<int32_t *>(counts);
+    p.load = const_cast<float *>(load);
+    p.grad_weights = grad_weights;
+    p.balance = balance;
+    p.z = z;
+    p.ntokens = (uint32_t)ntokens;
+    p.experts = (uint32_t)experts;
+    p.top = (uint32_t)top;
+    p.normalize = normalize != 0;
+    const size_t groups = kRouteThreads / pl.lanes;
+    return from_cuda(launch_route<true>(dtype, p, (unsigned)std::min<size_t>((ntokens + groups - 1) / groups, 8 * 152), stream));
+}
+
+} // namespace
+} // namespace ccl
+
+using namespace ccl;
+
+extern "C" {
+
+ccl_status_t ccl_plan_route_work_bytes(size_t ntokens, size_t experts, size_t *bytes)
+{
+    RoutePlan p;
+    if (!bytes || !plan_route(ntokens, experts, &p))
+        return CCL_ERR_INVALID_ARG;
+    *bytes = p.bytes;
+    return CCL_OK;
+}
+
+ccl_status_t ccl_route(const void *logits, size_t ntokens, size_t experts, size_t logits_stride, ccl_dtype_t dtype, const uint8_t *valid, size_t top,
+                       int normalize, int32_t *ids, float *weights, float *lse, int32_t *counts, float *load, float *importance, float *losses,
+                       void *work, size_t work_bytes, cudaStream_t stream)
+{
+    TraceScope tr("route", 1, ntokens, (int)dtype, -1, 0, stream);
+    return tr.done(guarded([&] {
+        return route_impl(logits, ntokens, experts, logits_stride, dtype, valid, top, normalize, ids, weights, lse, counts, load, importance, losses,
+                          work, work_bytes, stream);
+    }));
+}
+
+ccl_status_t ccl_route_grad(const void *logits, size_t ntokens, size_t experts, size_t logits_stride, ccl_dtype_t dtype, const int32_t *ids, size_t top,
+                            int normalize, const float *lse, const int32_t *counts, const float *load, const float *grad_weights, float balance,
+                            float z, void *grad_logits, size_t grad_stride, cudaStream_t stream)
+{
+    TraceScope tr("route_grad", 1, ntokens, (int)dtype, -1, 0, stream);
+    return tr.done(guarded([&] {
+        return route_grad_impl(logits, ntokens, experts, logits_stride, dtype, ids, top, normalize, lse, counts, load, grad_weights, balance, z,
+                               grad_logits, grad_stride, stream);
+    }));
+}
+
+} // extern "C"
