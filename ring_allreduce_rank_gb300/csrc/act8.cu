@@ -31,20 +31,31 @@ __device__ __forceinline__ uint64_t row_of(const Act8Params &p, uint64_t i)
     return p.blocks >> 32 ? i / p.per : (uint32_t)i / p.per;
 }
 
-// 32 consecutive values of a row, 16-byte aligned; those past the row are 0.
-template <int DT> __device__ __forceinline__ void load_block(const char *src, uint32_t n, float *f)
+// 32 consecutive values of a row in vectors of W bytes; those past the row are 0.
+template <int DT, int W> __device__ __forceinline__ void load_block(const char *src, uint32_t n, float *f)
 {
     constexpr int V = DType<DT>::kVec;
+    uint4 v[32 / V];
+#pragma unroll
+    for (int i = 0; i < 32 / V; i += W == 32 ? 2 : 1) {
+        v[i] = v[W == 32 ? i + 1 : i] = make_uint4(0, 0, 0, 0);
+        if ((uint32_t)(i * V) < n) {
+            if (W == 32)
+                ld32(src + i * 16, v[i], v[W == 32 ? i + 1 : i]);
+            else
+                v[i] = ld16(src + i * 16);
+        }
+    }
 #pragma unroll
     for (int i = 0; i < 32 / V; ++i)
-        unpack<DT>((uint32_t)(i * V) < n ? ld16(src + i * 16) : make_uint4(0, 0, 0, 0), f + i * V);
+        unpack<DT>(v[i], f + i * V);
 }
 
-template <int DT, bool VECTOR> __global__ void __launch_bounds__(kActThreads) act8_pack_kernel(Act8Params p)
+template <int DT, int W> __global__ void __launch_bounds__(kActThreads) act8_pack_kernel(Act8Params p)
 {
     chain_entry();
     constexpr int es = DType<DT>::kSize;
-    if (VECTOR) {
+    if (W) {
         const uint64_t i = (uint64_t)blockIdx.x * kActThreads + threadIdx.x;
         if (i >= p.blocks)
             return;
@@ -53,7 +64,7 @@ template <int DT, bool VECTOR> __global__ void __launch_bounds__(kActThreads) ac
         const char *src = p.x + r * p.pitch + (uint64_t)c * es;
         float f[32];
         uint4 lo, hi;
-        load_block<DT>(src, p.cols - c, f);
+        load_block<DT, W>(src, p.cols - c, f);
         const uint32_t byte = act8_encode(f, lo, hi);
         st32(p.codes + i * kActBlock, lo, hi);
         gstore<uint8_t>(p.bytes + i, (uint8_t)byte);
@@ -88,11 +99,11 @@ template <int DT, bool VECTOR> __global__ void __launch_bounds__(kActThreads) ac
     }
 }
 
-template <int DT, bool VECTOR> __global__ void __launch_bounds__(kActThreads) act8_unpack_kernel(Act8Params p)
+template <int DT, int W> __global__ void __launch_bounds__(kActThreads) act8_unpack_kernel(Act8Params p)
 {
     chain_entry();
     constexpr int es = DType<DT>::kSize, V = DType<DT>::kVec;
-    if (VECTOR) {
+    if (W) {
         const uint64_t i = (uint64_t)blockIdx.x * kActThreads + threadIdx.x;
         if (i >= p.blocks)
             return;
@@ -104,9 +115,13 @@ template <int DT, bool VECTOR> __global__ void __launch_bounds__(kActThreads) ac
         float f[32];
         act8_decode(lo, hi, act8_step(gload<uint8_t>(p.bytes + i)), f);
 #pragma unroll
-        for (int j = 0; j < 32 / V; ++j)
-            if ((uint32_t)(j * V) < p.cols - c)
-                st16(dst + j * 16, pack<DT>(f + j * V));
+        for (int j = 0; j < 32 / V; j += W == 32 ? 2 : 1)
+            if ((uint32_t)(j * V) < p.cols - c) {
+                if (W == 32)
+                    st32(dst + j * 16, pack<DT>(f + j * V), pack<DT>(f + (W == 32 ? j + 1 : j) * V));
+                else
+                    st16(dst + j * 16, pack<DT>(f + j * V));
+            }
     } else {
         const uint32_t lane = threadIdx.x & 31;
         const uint64_t warps = (uint64_t)gridDim.x * (kActThreads / 32);
@@ -151,7 +166,9 @@ ccl_status_t act8_impl(bool pack, const void *x, size_t rows, size_t cols, size_
     p.blocks = (uint64_t)rows * per;
     p.cols = (uint32_t)cols;
     p.per = (uint32_t)per;
-    const bool vec = ((uintptr_t)x | p.pitch | cols * es) % 16 == 0;
+    const uintptr_t all = (uintptr_t)x | p.pitch | cols * es;
+    const int width = all % 32 == 0 ? 32 : all % 16 == 0 ? 16 : 0;
+    const bool vec = width != 0;
     // a thread a block: the grid's 2^31 CTAs hold 2^39 of them, and 2^31 rows of 2^24 columns have 2^50
     if (vec && p.blocks > (uint64_t)0x7fffffff * kActThreads)
         return CCL_ERR_INVALID_ARG;
@@ -159,12 +176,10 @@ ccl_status_t act8_impl(bool pack, const void *x, size_t rows, size_t cols, size_
     const uint64_t ctas = (p.blocks + per_cta - 1) / per_cta;
     const dim3 grid((unsigned)(vec ? ctas : std::min<uint64_t>(ctas, 8 * 152))), block(kActThreads);
     void (*k)(Act8Params);
-    if (pack)
-        k = dtype == CCL_FP32 ? (vec ? act8_pack_kernel<DT_FP32, true> : act8_pack_kernel<DT_FP32, false>)
-                              : (vec ? act8_pack_kernel<DT_BF16, true> : act8_pack_kernel<DT_BF16, false>);
-    else
-        k = dtype == CCL_FP32 ? (vec ? act8_unpack_kernel<DT_FP32, true> : act8_unpack_kernel<DT_FP32, false>)
-                              : (vec ? act8_unpack_kernel<DT_BF16, true> : act8_unpack_kernel<DT_BF16, false>);
+#define CCL_ACT8_KERNEL(kernel)                                                                                        \
+    (dtype == CCL_FP32 ? (width == 32 ? kernel<DT_FP32, 32> : width == 16 ? kernel<DT_FP32, 16> : kernel<DT_FP32, 0>)  \
+                       : (width == 32 ? kernel<DT_BF16, 32> : width == 16 ? kernel<DT_BF16, 16> : kernel<DT_BF16, 0>))
+    k = pack ? CCL_ACT8_KERNEL(act8_pack_kernel) : CCL_ACT8_KERNEL(act8_unpack_kernel);
     const cudaError_t e = launch_chained(k, grid, block, 0, stream, p);
     if (e == cudaSuccess)
         count_launches(1);

@@ -27,8 +27,10 @@ namespace ccl {
 namespace {
 
 constexpr size_t kMaxTokens = 0x7fffffff;
-constexpr int kRouteThreads = 256;
-constexpr uint32_t kRouteCtas = 4 * 152; // at most; each leaves a row of partial sums
+constexpr int kRouteThreads = 256; // route_grad_kernel's
+// route_kernel's, at most: one CTA an SM with eight values a lane, so that 152
+// rows of partial sums are left; two with 32, whose lanes take 128 registers.
+constexpr int route_threads(int values) { return values <= 8 ? 1024 : 256; }
 
 struct RouteParams {
     const char *logits;
@@ -40,12 +42,14 @@ struct RouteParams {
     int32_t *counts;
     float *load, *importance, *loss;
     float *sums;     // partial: [ctas][experts + 1], the last one of lse^2
-    int32_t *hits;   // partial: [ctas][experts + 1], the last one of routed tokens
+    int32_t *hits;   // partial: [ctas][experts + 2], the last ones routed tokens and choices
     const float *grad_weights;
     float balance, z; // the losses' coefficients
     uint32_t ntokens, experts, top, ctas;
     int normalize, vector;
 };
+
+constexpr uint32_t kNothing = 0x007fffffu, kNaN = 0xffffffffu; // ordered(-inf); any NaN
 
 // A float's bits in an order of unsigned numbers: both zeros equal, any NaN
 // above +inf.
@@ -53,14 +57,13 @@ __device__ __forceinline__ uint32_t ordered(float f)
 {
     const uint32_t b = __float_as_uint(__fadd_rn(f, 0.0f)); // -0 + 0 = 0
     if ((b & 0x7fffffffu) > 0x7f800000u)
-        return 0xffffffffu;
+        return kNaN;
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-constexpr uint32_t kNothing = 0x007fffffu; // ordered(-inf)
 
 __device__ __forceinline__ float from_ordered(uint32_t k)
 {
-    return __uint_as_float(k == 0xffffffffu ? 0x7fffffffu : k & 0x80000000u ? k & 0x7fffffffu : ~k);
+    return __uint_as_float(k == kNaN ? 0x7fffffffu : k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
 template <int L> __device__ __forceinline__ float group_sum(float v)
@@ -73,22 +76,26 @@ template <int L> __device__ __forceinline__ float group_sum(float v)
 
 template <int L> __device__ __forceinline__ uint32_t group_max(uint32_t v)
 {
-    if (L == 32)
+    if constexpr (L == 32) {
         return __reduce_max_sync(0xffffffffu, v);
+    } else {
 #pragma unroll
-    for (int d = L / 2; d; d /= 2)
-        v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
-    return v;
+        for (int d = L / 2; d; d /= 2)
+            v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
+        return v;
+    }
 }
 
 template <int L> __device__ __forceinline__ uint32_t group_min(uint32_t v)
 {
-    if (L == 32)
+    if constexpr (L == 32) {
         return __reduce_min_sync(0xffffffffu, v);
+    } else {
 #pragma unroll
-    for (int d = L / 2; d; d /= 2)
-        v = min(v, __shfl_xor_sync(0xffffffffu, v, d));
-    return v;
+        for (int d = L / 2; d; d /= 2)
+            v = min(v, __shfl_xor_sync(0xffffffffu, v, d));
+        return v;
+    }
 }
 
 // Column of a lane's i-th value: vectors of N side by side, so that a group's
@@ -132,27 +139,12 @@ template <int DT, int L, int V, int N> __device__ __forceinline__ void load_row(
     }
 }
 
-// What the launch's last CTA, or the second launch, makes of the partial sums.
-__device__ __forceinline__ void finish_losses(const RouteParams &p, float *sums, int32_t *hits, float *shared)
+// What the partial sums' last reader makes of them: sums [experts + 1], hits
+// [experts + 2] in shared memory, complete and visible.
+__device__ __forceinline__ void finish_losses(const RouteParams &p, float *sums, const int32_t *hits)
 {
-    // sums and hits: [experts + 1] in shared memory, complete
     const uint32_t E = p.experts;
-    const float n = fmaxf((float)hits[E], 1.0f);
-    long long all = 0;
-    // every thread of the first warp sums the counts of its experts, then they are joined
-    const uint32_t lane = threadIdx.x & 31;
-    if (threadIdx.x < 32) {
-        for (uint32_t e = lane; e < E; e += 32)
-            all += hits[e];
-#pragma unroll
-        for (int d = 16; d; d /= 2)
-            all += __shfl_xor_sync(0xffffffffu, all, d);
-        if (lane == 0)
-            shared[0] = __fdiv_rn(1.0f, (float)(all > 0 ? all : 1));
-    }
-    __syncthreads();
-    const float inv = shared[0];
-    __syncthreads();
+    const float n = fmaxf((float)hits[E], 1.0f), inv = __fdiv_rn(1.0f, fmaxf((float)hits[E + 1], 1.0f));
     for (uint32_t e = threadIdx.x; e < E; e += blockDim.x) {
         const float load = __fmul_rn((float)hits[e], inv), importance = __fdiv_rn(sums[e], n);
         gstore<int32_t>(p.counts + e, hits[e]);
@@ -163,10 +155,10 @@ __device__ __forceinline__ void finish_losses(const RouteParams &p, float *sums,
     __syncthreads();
     if (threadIdx.x < 32) {
         float b = 0.0f;
-        for (uint32_t e = lane; e < E; e += 32)
+        for (uint32_t e = threadIdx.x; e < E; e += 32)
             b = __fadd_rn(b, sums[e]);
         b = group_sum<32>(b);
-        if (lane == 0) {
+        if (threadIdx.x == 0) {
             gstore<int32_t>(p.counts + E, hits[E]);
             gstore<float>(p.loss, __fmul_rn((float)E, b));
             gstore<float>(p.loss + 1, __fdiv_rn(sums[E], n));
@@ -174,209 +166,201 @@ __device__ __forceinline__ void finish_losses(const RouteParams &p, float *sums,
     }
 }
 
-// L lanes a row, V values a lane, loads of N values.
-template <int DT, int L, int V, int N> __global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_constant__ RouteParams p)
+// L lanes a row, V values a lane, loads of N values; the block has whole warps.
+template <int DT, int L, int V, int N> __global__ void __launch_bounds__(route_threads(V)) route_kernel(const __grid_constant__ RouteParams p)
 {
     chain_entry();
-    constexpr int kGroups = kRouteThreads / L;
-    extern __shared__ float shared[]; // sums [experts + 1], hits [experts + 1]
-    __shared__ float squares[kGroups];
-    __shared__ int32_t routed[kGroups];
-    __shared__ float scratch;
-    const uint32_t E = p.experts;
-    float *sums = shared;
-    int32_t *hits = reinterpret_cast<int32_t *>(shared + E + 1);
-    const uint32_t lane = threadIdx.x % L, group = threadIdx.x / L;
-    for (uint32_t e = threadIdx.x; e <= E; e += kRouteThreads)
+    extern __shared__ float shared[]; // sums [warps][experts + 1], hits [experts + 2]
+    const uint32_t E = p.experts, warps = blockDim.x / 32, groups = blockDim.x / L;
+    int32_t *hits = reinterpret_cast<int32_t *>(shared + warps * (E + 1));
+    const uint32_t lane = threadIdx.x % L, group = threadIdx.x / L, warp = threadIdx.x / 32;
+    for (uint32_t e = threadIdx.x; e < E + 2; e += blockDim.x)
         hits[e] = 0;
     __syncthreads();
     float acc[V], square = 0.0f;
-    int32_t n = 0;
+    int32_t routed = 0, choices = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i)
         acc[i] = 0.0f;
-    const uint32_t stride = p.ctas * kGroups;
+    const uint32_t stride = p.ctas * groups;
     // whole warps go round together: rows past the last are rows without experts
     const uint32_t rounds = (p.ntokens + stride - 1) / stride;
-    float f[V];
-    auto fetch = [&](uint32_t round, float *v, bool &is) {
-        const uint64_t t = (uint64_t)round * stride + blockIdx.x * kGroups + group;
-        is = round < rounds && t < p.ntokens && (!p.valid || gload<uint8_t>(p.valid + t));
-        if (is)
+    auto fetch = [&](uint32_t round, float *v) {
+        const uint64_t t = (uint64_t)round * stride + blockIdx.x * groups + group;
+        if (round < rounds && t < p.ntokens && (!p.valid || gload<uint8_t>(p.valid + t))) {
             load_row<DT, L, V, N>(p, p.logits + t * p.pitch, lane, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                v[i] = -INFINITY;
+        }
     };
-    bool is;
-    fetch(0, f, is);
+    constexpr bool kAhead = V <= 8; // the next row's values fit beside this one's
+    float f[V], next[kAhead ? V : 1];
+    if (kAhead)
+        fetch(0, f);
     for (uint32_t round = 0; round < rounds; ++round) {
-        const uint64_t t = (uint64_t)round * stride + blockIdx.x * kGroups + group;
-        float next[V];
-        bool next_is;
-        fetch(round + 1, next, next_is);
-        // the lane's best, and the row's
-        float m = -INFINITY;
-        uint32_t best = kNothing, at = 0;
+        const uint64_t t = (uint64_t)round * stride + blockIdx.x * groups + group;
+        if (kAhead)
+            fetch(round + 1, next);
+        else
+            fetch(round, f);
+        uint32_t key[V], best = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            f[i] = is ? f[i] : -INFINITY;
-            const uint32_t k = ordered(f[i]);
-            if (k > best) { // columns rise with i: the first of equals stays
-                best = k;
-                at = i;
-            }
-            m = fmaxf(m, f[i]);
+            key[i] = ordered(f[i]);
+            best = max(best, key[i]);
         }
         const uint32_t top = group_max<L>(best);
         const bool live = top > kNothing;
+        // a NaN in the row makes its sum NaN whatever is taken off
+        const float m = live && top != kNaN ? from_ordered(top) : 0.0f;
         float total = 0.0f;
-        if (L == 32) {
-            m = top == 0xffffffffu ? m : from_ordered(top);
-            if (top == 0xffffffffu)
-                m = 0.0f; // a NaN in the row makes its sum NaN whatever is taken off
-        } else {
-#pragma unroll
-            for (int d = L / 2; d; d /= 2)
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        }
-        float e[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            e[i] = live ? expf(__fsub_rn(f[i], m)) : 0.0f;
-            total = __fadd_rn(total, e[i]);
+            f[i] = expf(__fsub_rn(f[i], m)); // 0 for -inf
+            total = __fadd_rn(total, f[i]);
         }
         total = group_sum<L>(total);
         const float inv = live ? __fdiv_rn(1.0f, total) : 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            acc[i] = __fmaf_rn(e[i], inv, acc[i]);
+            acc[i] = __fmaf_rn(f[i], inv, acc[i]);
         const float lse = live ? __fadd_rn(m, logf(total)) : 0.0f;
-        // the choices, one a step; lane s keeps the s-th (and s + L, ...)
-        float kept = 0.0f;
+        // the choices, one a step: the largest key, at its lowest column; lane s
+        // keeps the s-th (and s + L, ...)
         constexpr int kMine = (CCL_MAX_EXPERT_TOP + L - 1) / L;
-        float mine[kMine];
+        uint32_t mine[kMine];
         int32_t id[kMine];
+        uint32_t k = top;
 #pragma unroll
-        for (int s0 = 0; s0 < kMine; ++s0)
-            if (s0 * L < p.top) {
-                mine[s0] = 0.0f;
-                id[s0] = -1;
+        for (int s0 = 0; s0 < kMine; ++s0) {
+            mine[s0] = kNothing;
+            id[s0] = -1;
+            if (s0 * L < p.top)
                 for (uint32_t s = 0; s < L && s0 * L + s < p.top; ++s) {
-                    const uint32_t k = group_max<L>(best);
-                    const uint32_t c = best == k ? column<L, N>(lane, at) : 0xffffffffu;
-                    const uint32_t chosen = group_min<L>(c);
-                    const bool some = k > kNothing;
-                    if (c == chosen && some) { // this lane's: out of the running, and its next best
-                        atomicAdd(&hits[chosen], 1); // whole numbers: any order gives the same count
-                        best = kNothing;
-                        uint32_t was = at;
-                        at = 0;
+                    uint32_t c = 0xffffffffu;
 #pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            if ((uint32_t)i == was)
-                                f[i] = -INFINITY;
-                            const uint32_t o = ordered(f[i]);
-                            if (o > best) {
-                                best = o;
-                                at = i;
-                            }
-                        }
+                    for (int i = V - 1; i >= 0; --i) // columns rise with i: the first of equals stays
+                        c = key[i] == k ? column<L, N>(lane, i) : c;
+                    c = group_min<L>(c);
+                    if (lane == s && k > kNothing) {
+                        mine[s0] = k;
+                        id[s0] = (int32_t)c;
                     }
-                    const float w = some ? expf(__fsub_rn(from_ordered(k), m)) : 0.0f;
-                    kept = __fadd_rn(kept, w);
-                    if (lane == s) {
-                        mine[s0] = w;
-                        id[s0] = some ? (int32_t)chosen : -1;
+                    best = 0;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        key[i] = column<L, N>(lane, i) == c ? 0 : key[i]; // out of the running
+                        best = max(best, key[i]);
                     }
+                    k = group_max<L>(best);
                 }
-            }
-        const float by = !live ? 0.0f : p.normalize ? __fdiv_rn(1.0f, kept) : inv;
+        }
+        float w[kMine], kept = 0.0f;
+#pragma unroll
+        for (int s0 = 0; s0 < kMine; ++s0) {
+            w[s0] = id[s0] >= 0 ? expf(__fsub_rn(from_ordered(mine[s0]), m)) : 0.0f;
+            kept = __fadd_rn(kept, w[s0]);
+        }
+        const float by = p.normalize ? __fdiv_rn(1.0f, group_sum<L>(kept)) : inv;
         if (t < p.ntokens) {
 #pragma unroll
             for (int s0 = 0; s0 < kMine; ++s0) {
                 const uint32_t s = s0 * L + lane;
                 if (s < p.top) {
                     gstore<int32_t>(p.ids + t * p.top + s, id[s0]);
-                    gstore<float>(p.weights + t * p.top + s, id[s0] < 0 ? 0.0f : __fmul_rn(mine[s0], by));
+                    gstore<float>(p.weights + t * p.top + s, id[s0] < 0 ? 0.0f : __fmul_rn(w[s0], by));
+                    if (id[s0] >= 0) {
+                        atomicAdd(&hits[id[s0]], 1); // whole numbers: any order gives the same count
+                        ++choices;
+                    }
                 }
             }
             if (lane == 0)
                 gstore<float>(p.lse + t, lse);
         }
         square = __fmaf_rn(lse, lse, square);
-        n += live;
+        routed += live;
+        if (kAhead) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                f[i] = next[kAhead ? i : 0];
+        }
+    }
+    // the warp's sums, its groups pairwise
+#pragma unroll
+    for (int d = L; d < 32; d *= 2) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            f[i] = next[i];
-        is = next_is;
+            acc[i] = __fadd_rn(acc[i], __shfl_xor_sync(0xffffffffu, acc[i], d));
+        square = __fadd_rn(square, __shfl_xor_sync(0xffffffffu, square, d));
+        routed += __shfl_xor_sync(0xffffffffu, routed, d);
     }
-    // the CTA's sums, its groups in order
-    if (lane == 0) {
-        squares[group] = square;
-        routed[group] = n;
-    }
-    for (int g = 0; g < kGroups; ++g) {
-        __syncthreads();
-        if (group == (uint32_t)g) {
+    choices = __reduce_add_sync(0xffffffffu, choices);
+    float *mine = shared + warp * (E + 1);
+    if (threadIdx.x % 32 < L) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const uint32_t c = column<L, N>(lane, i);
-                if (c < E)
-                    sums[c] = g ? __fadd_rn(sums[c], acc[i]) : acc[i];
-            }
+        for (int i = 0; i < V; ++i) {
+            const uint32_t c = column<L, N>(lane, i);
+            if (c < E)
+                mine[c] = acc[i];
         }
     }
-    if (threadIdx.x == 0) {
-        float s = 0.0f;
-        int32_t r = 0;
-        for (int g = 0; g < kGroups; ++g) {
-            s = __fadd_rn(s, squares[g]);
-            r += routed[g];
-        }
-        sums[E] = s;
-        hits[E] = r;
+    if (threadIdx.x % 32 == 0) {
+        mine[E] = square;
+        atomicAdd(&hits[E], routed);
+        atomicAdd(&hits[E + 1], choices);
     }
     __syncthreads();
-    if (p.ctas == 1) {
-        finish_losses(p, sums, hits, &scratch);
-        return;
+    // the CTA's, its warps in order; each column is one thread's from here on
+    for (uint32_t e = threadIdx.x; e <= E; e += blockDim.x) {
+        float v = shared[e];
+        for (uint32_t k = 1; k < warps; ++k)
+            v = __fadd_rn(v, shared[k * (E + 1) + e]);
+        if (p.ctas == 1)
+            shared[e] = v;
+        else
+            gstore<float>(p.sums + (uint64_t)blockIdx.x * (E + 1) + e, v);
     }
-    for (uint32_t e = threadIdx.x; e <= E; e += kRouteThreads) {
-        gstore<float>(p.sums + (uint64_t)blockIdx.x * (E + 1) + e, sums[e]);
-        gstore<int32_t>(p.hits + (uint64_t)blockIdx.x * (E + 1) + e, hits[e]);
+    if (p.ctas == 1) {
+        __syncthreads();
+        finish_losses(p, shared, hits);
+    } else {
+        for (uint32_t e = threadIdx.x; e < E + 2; e += blockDim.x)
+            gstore<int32_t>(p.hits + (uint64_t)blockIdx.x * (E + 2) + e, hits[e]);
     }
 }
 
 // The CTAs' partial sums: 1024 / columns threads a column take runs of the CTAs
-// in order, and the runs are joined in order.
+// in order, sixteen loads in flight, and the runs are joined in order.
 __global__ void __launch_bounds__(1024) route_join_kernel(const __grid_constant__ RouteParams p)
 {
     chain_entry();
-    extern __shared__ float shared[]; // sums, hits [parts][experts + 1]
-    __shared__ float scratch;
-    const uint32_t n = p.experts + 1, parts = max(1024u / n, 1u), part = threadIdx.x / n;
+    extern __shared__ float shared[]; // sums [parts][columns], hits [parts][columns]
+    const uint32_t n = p.experts + 2, parts = max(1024u / n, 1u), run = (p.ctas + parts - 1) / parts;
     float *sums = shared;
     int32_t *hits = reinterpret_cast<int32_t *>(shared + parts * n);
-    const uint32_t run = (p.ctas + parts - 1) / parts;
-    for (uint32_t c = n <= 1024 ? threadIdx.x % n : threadIdx.x; part < parts && c < n; c += 1024) {
+    for (uint32_t i = threadIdx.x; i < parts * n; i += 1024) {
+        const uint32_t part = i / n, c = i - part * n, b1 = min((part + 1) * run, p.ctas);
         float s = 0.0f;
         int32_t h = 0;
-        const uint32_t b1 = min((part + 1) * run, p.ctas);
-        for (uint32_t b0 = part * run; b0 < b1; b0 += 8) {
-            float x[8];
-            int32_t y[8];
+        for (uint32_t b0 = part * run; b0 < b1; b0 += 16) {
+            float x[16];
+            int32_t y[16];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint64_t at = (uint64_t)(b0 + j) * n + c;
-                x[j] = b0 + j < b1 ? gload<float>(p.sums + at) : 0.0f;
-                y[j] = b0 + j < b1 ? gload<int32_t>(p.hits + at) : 0;
+            for (int j = 0; j < 16; ++j) {
+                x[j] = b0 + j < b1 && c + 1 < n ? gload<float>(p.sums + (uint64_t)(b0 + j) * (n - 1) + c) : 0.0f;
+                y[j] = b0 + j < b1 ? gload<int32_t>(p.hits + (uint64_t)(b0 + j) * n + c) : 0;
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 16; ++j) {
                 s = __fadd_rn(s, x[j]);
                 h += y[j];
             }
         }
-        sums[part * n + c] = s;
-        hits[part * n + c] = h;
+        sums[i] = s;
+        hits[i] = h;
     }
     __syncthreads();
     for (uint32_t c = threadIdx.x; c < n; c += 1024) {
@@ -390,7 +374,7 @@ __global__ void __launch_bounds__(1024) route_join_kernel(const __grid_constant_
         hits[c] = h;
     }
     __syncthreads();
-    finish_losses(p, sums, hits, &scratch);
+    finish_losses(p, sums, hits);
 }
 
 template <int DT, int L, int V, int N> __global__ void __launch_bounds__(kRouteThreads) route_grad_kernel(const __grid_constant__ RouteParams p)
@@ -505,7 +489,7 @@ template <int DT, int L, int V, int N> __global__ void __launch_bounds__(kRouteT
 // ------------------------------------------------------------------ host side
 
 struct RoutePlan {
-    uint32_t lanes, ctas;
+    uint32_t lanes, threads, ctas;
     size_t sums, bytes;
 };
 
@@ -515,41 +499,41 @@ bool plan_route(size_t ntokens, size_t experts, RoutePlan *p)
         return false;
     *p = RoutePlan{};
     p->lanes = experts <= 64 ? 8 : 32;
-    const size_t groups = kRouteThreads / p->lanes;
-    // one CTA for a few rounds of rows: it needs no second launch
-    const size_t ctas = (ntokens + groups - 1) / groups;
-    p->ctas = ctas <= 2 ? 1 : (uint32_t)std::min<size_t>(ctas, kRouteCtas);
+    const size_t most = route_threads(experts <= 256 ? 8 : 32), groups = most / p->lanes, all = (ntokens + groups - 1) / groups;
+    // one CTA for two rounds of rows: it needs no second launch
+    p->ctas = all <= 2 ? 1 : (uint32_t)std::min<size_t>(all, experts <= 256 ? 152 : 304);
+    p->threads = (uint32_t)std::min<size_t>(most, std::max<size_t>(ntokens * p->lanes + 31, 32) / 32 * 32);
     if (p->ctas > 1) {
         p->sums = up(p->ctas * (experts + 1) * 4);
-        p->bytes = 2 * p->sums;
+        p->bytes = p->sums + up(p->ctas * (experts + 2) * 4);
     }
     return true;
 }
 
-template <int DT, int L, int V, bool GRAD> cudaError_t launch_route3(const RouteParams &p, unsigned ctas, cudaStream_t stream)
+template <int DT, int L, int V, bool GRAD> cudaError_t launch_route3(const RouteParams &p, unsigned ctas, unsigned threads, cudaStream_t stream)
 {
     constexpr int N = V < DType<DT>::kVec ? V : DType<DT>::kVec;
-    const size_t smem = GRAD ? p.experts * 4 : (p.experts + 1) * 8;
+    const size_t smem = GRAD ? p.experts * 4 : (threads / 32 * (p.experts + 1) + p.experts + 2) * 4;
     void (*const vec)(RouteParams) = GRAD ? route_grad_kernel<DT, L, V, N> : route_kernel<DT, L, V, N>;
     void (*const one)(RouteParams) = GRAD ? route_grad_kernel<DT, L, V, 1> : route_kernel<DT, L, V, 1>;
     const uintptr_t all = (uintptr_t)p.logits | p.pitch | p.experts * DType<DT>::kSize | (GRAD ? (uintptr_t)p.grad | p.grad_pitch : 0);
-    return launch_chained(all % (N * DType<DT>::kSize) == 0 ? vec : one, dim3(ctas), dim3(kRouteThreads), smem, stream, p);
+    return launch_chained(all % (N * DType<DT>::kSize) == 0 ? vec : one, dim3(ctas), dim3(threads), smem, stream, p);
 }
 
-template <int DT, bool GRAD> cudaError_t launch_route2(const RouteParams &p, unsigned ctas, cudaStream_t stream)
+template <int DT, bool GRAD> cudaError_t launch_route2(const RouteParams &p, unsigned ctas, unsigned threads, cudaStream_t stream)
 {
     if (p.experts <= 16)
-        return launch_route3<DT, 8, 2, GRAD>(p, ctas, stream);
+        return launch_route3<DT, 8, 2, GRAD>(p, ctas, threads, stream);
     if (p.experts <= 64)
-        return launch_route3<DT, 8, 8, GRAD>(p, ctas, stream);
+        return launch_route3<DT, 8, 8, GRAD>(p, ctas, threads, stream);
     if (p.experts <= 256)
-        return launch_route3<DT, 32, 8, GRAD>(p, ctas, stream);
-    return launch_route3<DT, 32, 32, GRAD>(p, ctas, stream);
+        return launch_route3<DT, 32, 8, GRAD>(p, ctas, threads, stream);
+    return launch_route3<DT, 32, 32, GRAD>(p, ctas, threads, stream);
 }
 
-template <bool GRAD> cudaError_t launch_route(ccl_dtype_t dtype, const RouteParams &p, unsigned ctas, cudaStream_t stream)
+template <bool GRAD> cudaError_t launch_route(ccl_dtype_t dtype, const RouteParams &p, unsigned ctas, unsigned threads, cudaStream_t stream)
 {
-    const cudaError_t e = dtype == CCL_FP32 ? launch_route2<DT_FP32, GRAD>(p, ctas, stream) : launch_route2<DT_BF16, GRAD>(p, ctas, stream);
+    const cudaError_t e = dtype == CCL_FP32 ? launch_route2<DT_FP32, GRAD>(p, ctas, threads, stream) : launch_route2<DT_BF16, GRAD>(p, ctas, threads, stream);
     if (e == cudaSuccess)
         count_launches(1);
     return e;
@@ -601,9 +585,9 @@ ccl_status_t route_impl(const void *logits, size_t ntokens, size_t experts, size
     p.top = (uint32_t)top;
     p.ctas = pl.ctas;
     p.normalize = normalize != 0;
-    cudaError_t e = launch_route<false>(dtype, p, pl.ctas, stream);
+    cudaError_t e = launch_route<false>(dtype, p, pl.ctas, pl.threads, stream);
     if (e == cudaSuccess && pl.ctas > 1) {
-        const size_t n = experts + 1, parts = std::max<size_t>(1024 / n, 1);
+        const size_t n = experts + 2, parts = std::max<size_t>(1024 / n, 1);
         e = launch_chained(route_join_kernel, dim3(1), dim3(1024), parts * n * 8, stream, p);
         if (e == cudaSuccess)
             count_launches(1);
@@ -660,7 +644,7 @@ ccl_status_t route_grad_impl(const void *logits, size_t ntokens, size_t experts,
     p.top = (uint32_t)top;
     p.normalize = normalize != 0;
     const size_t groups = kRouteThreads / pl.lanes;
-    return from_cuda(launch_route<true>(dtype, p, (unsigned)std::min<size_t>((ntokens + groups - 1) / groups, 8 * 152), stream));
+    return from_cuda(launch_route<true>(dtype, p, (unsigned)std::min<size_t>((ntokens + groups - 1) / groups, 8 * 152), kRouteThreads, stream));
 }
 
 } // namespace
