@@ -41,13 +41,13 @@ namespace {
 constexpr int kTileM = 256, kTileN = 256, kTileK = 64; // a CTA pair's tile
 constexpr int kOperandBytes = 128 * kTileK * 2;        // one CTA's part of A or B in a stage
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kStages = 6, kTurnStages = 5; // the latter beside the room to turn values in
-constexpr int kThreads2 = 384; // producer, issuer, tensor memory, table, eight epilogue warps
+constexpr int kStages = 6, kTurnStages = 4; // the latter beside the room to turn values in
+constexpr int kThreads2 = 384; // producer, issuer, tensor memory, one idle warp, eight epilogue warps
 constexpr int kEpiWarps = 8;
 constexpr int kTurnFloats = 32 * 33; // an epilogue warp's 32 x 32 values, rows padded against bank conflicts
 constexpr int kTableBytes = 3 * (CCL_MAX_EXPERTS + 2) * 4;
 constexpr int kGemmSmem = 1024 /* alignment */ + kTableBytes +
-                          std::max(kStages * kStageBytes, kTurnStages * kStageBytes + kEpiWarps * kTurnFloats * 4);
+                          std::max(kStages * kStageBytes, kTurnStages * kStageBytes + 16 * kTurnFloats * 4);
 constexpr int kGroupM = 8; // row tiles walked before the next column tile
 constexpr uint32_t kPad = kTileK; // an expert's rows in the padded layout are a multiple of this
 constexpr int kFewStages = 6;
@@ -55,6 +55,12 @@ constexpr int kFewBytes = 190 * 1024; // its stages', at most
 constexpr uint32_t kFewMost = 128;    // tokens of one tile
 
 enum Epilogue { EPI_GATED = 0, EPI_STORE = 1, EPI_BACKWARD = 2, EPI_WEIGHTS = 3 };
+
+// Epilogue warps of expert_gemm_kernel: two a scheduler for g and u, whose 64
+// values of a row take the registers, else four, which hide one another's
+// latencies.
+template <int EPI> constexpr int kEpilogueWarps = EPI == EPI_GATED ? kEpiWarps : 16;
+template <int EPI> constexpr int kGemmThreads = 128 + 32 * kEpilogueWarps<EPI>;
 
 // C[M, N] = sum over segments of A_s[M, K] B_s[N, K]^T for each expert: M its
 // rows, or for EPI_WEIGHTS K its rows.
@@ -64,6 +70,9 @@ struct Problem {
     uint32_t m, n;  // m: EPI_WEIGHTS only
     uint32_t mt, nt; // tiles (mt: EPI_WEIGHTS only)
     uint32_t kblocks, segs;
+    // EPI_WEIGHTS: a[1], b[1] are the rows as they lie, which full blocks of K
+    // are read from; the last, partial one is in the padded layout (a[0], b[0])
+    int direct_a, direct_b;
 };
 
 struct ExpertParams {
@@ -77,6 +86,7 @@ struct ExpertParams {
     uint8_t *scales[2];
     uint32_t ldh;
     int padded;  // A's rows are those of the padded layout
+    uint32_t half; // columns of B that a CTA of the pair brings: half a tile's
     int vectors; // every output row is 16-byte aligned and whole vectors of 8 columns
     unsigned long long wait_ns;
     // expert_few_kernel
@@ -173,6 +183,7 @@ __device__ __forceinline__ uint32_t expert_at(const int32_t *first, uint32_t exp
 
 struct Unit {
     uint32_t prob, expert, m, n, kblocks, split;
+    uint32_t half; // columns of B that each CTA of the pair brings: p.half, or fewer in the last column tile
     uint32_t row0, rows, pad0; // the expert's
 };
 
@@ -217,6 +228,8 @@ template <int EPI> __device__ __forceinline__ Unit unit_at(const ExpertParams &p
     u.rows = (uint32_t)tb.row0[u.expert + 1] - u.row0;
     u.pad0 = (uint32_t)tb.pad0[u.expert];
     u.kblocks = EPI == EPI_WEIGHTS ? (u.rows + kTileK - 1) / kTileK : q.kblocks * q.segs;
+    const uint32_t left = EPI == EPI_GATED ? q.n - u.n * p.half : (q.n - u.n * 2 * p.half + 1) / 2;
+    u.half = min(p.half, EPI == EPI_GATED ? (left + 31) / 32 * 32 : (left + 15) / 16 * 16);
     return u;
 }
 
@@ -306,45 +319,39 @@ struct Saved {
     }
 };
 
-// dh to dg, du and h, 32 columns of a row; four at a time keep the registers few.
-__device__ __forceinline__ void finish_backward(const ExpertParams &p, uint64_t to, const Saved &s, float *v)
+// dh to dg, du and h, sixteen columns of a row: the first or second half of a block.
+__device__ __forceinline__ void finish_backward(const ExpertParams &p, uint64_t to, const Saved &s, uint32_t second, const float *v)
 {
     const float sg = act8_step(s.bg), su = act8_step(s.bu);
-    const uint32_t wg[8] = {s.g[0].x, s.g[0].y, s.g[0].z, s.g[0].w, s.g[1].x, s.g[1].y, s.g[1].z, s.g[1].w};
-    const uint32_t wu[8] = {s.u[0].x, s.u[0].y, s.u[0].z, s.u[0].w, s.u[1].x, s.u[1].y, s.u[1].z, s.u[1].w};
+    const uint4 cg = s.g[second], cu = s.u[second];
+    const uint32_t wg[4] = {cg.x, cg.y, cg.z, cg.w}, wu[4] = {cu.x, cu.y, cu.z, cu.w};
+    float h[16], dg[16], du[16];
 #pragma unroll
-    for (int c = 0; c < 32; c += 16) {
-        float h[16], dg[16], du[16];
+    for (int j = 0; j < 16; j += 4) {
+        float g[4], u[4];
+        act8_decode4(wg[j / 4], sg, g);
+        act8_decode4(wu[j / 4], su, u);
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-            float g[4], u[4];
-            act8_decode4(wg[(c + j) / 4], sg, g);
-            act8_decode4(wu[(c + j) / 4], su, u);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float a, da;
-                activation(p.act, g[k], a, da);
-                const float d = v[c + j + k];
-                h[j + k] = __fmul_rn(a, u[k]);
-                dg[j + k] = __fmul_rn(__fmul_rn(d, u[k]), da);
-                du[j + k] = __fmul_rn(d, a);
-            }
+        for (int k = 0; k < 4; ++k) {
+            float a, da;
+            activation(p.act, g[k], a, da);
+            const float d = v[j + k];
+            h[j + k] = __fmul_rn(a, u[k]);
+            dg[j + k] = __fmul_rn(__fmul_rn(d, u[k]), da);
+            du[j + k] = __fmul_rn(d, a);
         }
-        st32(p.h + to + c, pack<DT_BF16>(h), pack<DT_BF16>(h + 8));
-        st32(p.dg + to + c, pack<DT_BF16>(dg), pack<DT_BF16>(dg + 8));
-        st32(p.du + to + c, pack<DT_BF16>(du), pack<DT_BF16>(du + 8));
     }
+    st32(p.h + to, pack<DT_BF16>(h), pack<DT_BF16>(h + 8));
+    st32(p.dg + to, pack<DT_BF16>(dg), pack<DT_BF16>(dg + 8));
+    st32(p.du + to, pack<DT_BF16>(du), pack<DT_BF16>(du + 8));
 }
 
 __device__ __forceinline__ void backward_zeros(const ExpertParams &p, uint64_t to)
 {
     const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int c = 0; c < 32; c += 16) {
-        st32(p.h + to + c, z, z);
-        st32(p.dg + to + c, z, z);
-        st32(p.du + to + c, z, z);
-    }
+    st32(p.h + to, z, z);
+    st32(p.dg + to, z, z);
+    st32(p.du + to, z, z);
 }
 
 // Sixteen (or eight) finished sums of one row of an output, added to what is
@@ -378,7 +385,7 @@ template <int EPI> __device__ __forceinline__ uint16_t *unit_out(const ExpertPar
 // ------------------------------------------------------------------ the product on CTA pairs
 
 template <int EPI, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(kThreads2, 1) expert_gemm_kernel(const __grid_constant__ ExpertParams p)
+__global__ void __launch_bounds__(kGemmThreads<EPI>, 1) expert_gemm_kernel(const __grid_constant__ ExpertParams p)
 {
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t bars[2 * kStages + 4];
@@ -402,7 +409,7 @@ __global__ void __launch_bounds__(kThreads2, 1) expert_gemm_kernel(const __grid_
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
-            mbar_init(acc_empty + 8 * i, 2 * kEpiWarps);
+            mbar_init(acc_empty + 8 * i, 2 * kEpilogueWarps<EPI>);
         }
         if ((gave_up = p.wait_ns == 0))
             atomicAdd(&g_expert_timeouts, 1ull);
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(kThreads2, 1) expert_gemm_kernel(const __grid_
     if (warp == 3 && lane / 4 < p.nprob) {
         const Problem &q = p.prob[lane / 4];
         const int i = lane & 1;
-        if (lane & 2 ? i < (EPI == EPI_GATED ? 2 : q.segs) : i < q.segs)
+        if (lane & 2 ? i < (EPI == EPI_GATED ? 2 : q.segs + q.direct_b) : i < q.segs + q.direct_a)
             prefetch_map(lane & 2 ? &q.b[i] : &q.a[i]);
     }
     if (warp == 2) {
@@ -435,21 +442,28 @@ __global__ void __launch_bounds__(kThreads2, 1) expert_gemm_kernel(const __grid_
         for (uint32_t i = pair; ok && i < total; i += pairs) {
             const Unit u = unit_at<EPI>(p, table, i);
             const Problem &q = p.prob[u.prob];
-            const int am = (int)(u.m * kTileM + rank * 128 + (EPI == EPI_WEIGHTS ? 0 : p.padded ? u.pad0 : u.row0));
-            const int bn = EPI == EPI_GATED ? (int)(u.n * 128) : (int)(u.n * kTileN + rank * 128);
+            // a half tile behind the expert's rows: from past the matrix, zeros that cost neither traffic nor much power
+            const uint32_t in = u.m * kTileM + rank * 128;
+            const int am = EPI == EPI_WEIGHTS ? (int)in : in >= u.rows ? 0x7fffff00 : (int)(in + (p.padded ? u.pad0 : u.row0));
+            const int bn = (int)(EPI == EPI_GATED ? u.n * p.half : u.n * 2 * p.half + rank * u.half);
             for (uint32_t kb = 0; kb < u.kblocks; ++kb) {
                 if (!(ok = mbar_wait(empty + 8 * s, phase ^ 1, &gave_up, p.wait_ns)))
                     break;
                 if (rank == 0)
                     mbar_expect(full + 8 * s, 2 * kStageBytes);
-                const uint32_t seg = EPI != EPI_WEIGHTS && kb >= q.kblocks ? 1 : 0;
-                const int k = (int)(EPI == EPI_WEIGHTS ? u.pad0 + kb * kTileK : (kb - seg * q.kblocks) * kTileK);
                 const uint32_t at = stages + s * kStageBytes;
-                load_rows<A_MN>(at, &q.a[seg], am, k, leader_full + 8 * s);
-                if (EPI == EPI_WEIGHTS)
-                    load_rows<B_MN>(at + kOperandBytes, &q.b[0], bn, k, leader_full + 8 * s);
-                else
+                if (EPI == EPI_WEIGHTS) {
+                    const int padded = (int)(u.pad0 + kb * kTileK), lies = (int)(u.row0 + kb * kTileK);
+                    const bool whole = (kb + 1) * kTileK <= u.rows;
+                    const bool da = q.direct_a && whole, db = q.direct_b && whole;
+                    load_rows<A_MN>(at, &q.a[da], am, da ? lies : padded, leader_full + 8 * s);
+                    load_rows<B_MN>(at + kOperandBytes, &q.b[db], bn, db ? lies : padded, leader_full + 8 * s);
+                } else {
+                    const uint32_t seg = kb >= q.kblocks ? 1 : 0;
+                    const int k = (int)((kb - seg * q.kblocks) * kTileK);
+                    load_rows<A_MN>(at, &q.a[seg], am, k, leader_full + 8 * s);
                     load_expert<B_MN>(at + kOperandBytes, EPI == EPI_GATED ? &q.b[rank] : &q.b[seg], bn, k, (int)u.expert, leader_full + 8 * s);
+                }
                 if (++s == nstages) {
                     s = 0;
                     phase ^= 1;
@@ -466,12 +480,12 @@ __global__ void __launch_bounds__(kThreads2, 1) expert_gemm_kernel(const __grid_
         }
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // issuer: fp32 accumulator, bf16 operands, their majorness, N, M
-        const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (A_MN ? 1u << 15 : 0) | (B_MN ? 1u << 16 : 0) |
-                               (kTileN >> 3) << 17 | (kTileM >> 4) << 24;
+        const uint32_t form = 1u << 4 | 1u << 7 | 1u << 10 | (A_MN ? 1u << 15 : 0) | (B_MN ? 1u << 16 : 0) | (kTileM >> 4) << 24;
         uint32_t s = 0, phase = 0, t = 0;
         bool ok = p.wait_ns != 0;
         for (uint32_t i = pair; ok && i < total; i += pairs) {
             const Unit u = unit_at<EPI>(p, table, i);
+            const uint32_t idesc = form | (2 * u.half >> 3) << 17;
             if (u.kblocks == 0)
                 continue; // an expert without rows: the epilogue needs no accumulator
             const uint32_t buf = t & 1;
@@ -498,25 +512,25 @@ __global__ void __launch_bounds__(kThreads2, 1) expert_gemm_kernel(const __grid_
             ++t;
         }
     } else if (warp >= 4) {
-        // epilogue: warp w reads lanes 32 (w % 4) .. + 32 and half of the columns
-        const uint32_t half = (warp - 4) / 4;
+        // epilogue: warp w reads lanes 32 (w % 4) .. + 32 and every kStride-th 32 columns
+        constexpr uint32_t kStride = 32 * kEpilogueWarps<EPI> / 4;
+        const uint32_t c0 = (warp - 4) / 4 * 32;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32;
         const uint32_t leader_empty = in_cta(acc_empty, 0);
         float *turn = reinterpret_cast<float *>(behind + kTableBytes) + (warp - 4) * kTurnFloats;
-        constexpr uint32_t kCols = EPI == EPI_GATED ? 64 : 128;
         uint32_t t = 0, i = pair;
         for (; p.wait_ns && i < total; i += pairs) {
             const Unit u = unit_at<EPI>(p, table, i);
             const Problem &q = p.prob[u.prob];
             const uint32_t buf = t & 1;
             const uint32_t in0 = u.m * kTileM + rank * 128 + lanes, in = in0 + lane; // rows within the expert's
-            const uint32_t c0 = half * kCols, col0 = u.n * (2 * kCols) + c0;
+            const uint32_t cols = EPI == EPI_GATED ? u.half : 2 * u.half, col0 = u.n * (EPI == EPI_GATED ? 1 : 2) * p.half;
             const bool some = EPI != EPI_WEIGHTS || u.kblocks;
             if (!some && p.accumulate)
                 continue; // nothing is added
             Saved ahead;
             if (EPI == EPI_BACKWARD)
-                ahead.load(p, (uint64_t)(u.row0 + in) * p.ldh + col0, in < u.rows && col0 < p.ldh);
+                ahead.load(p, (uint64_t)(u.row0 + in) * p.ldh + col0 + c0, in < u.rows && c0 < cols);
             if (some) {
                 if (!__all_sync(0xffffffffu, mbar_wait(acc_full + 8 * buf, (t >> 1) & 1, &gave_up, p.wait_ns)))
                     break;
@@ -524,25 +538,26 @@ __global__ void __launch_bounds__(kThreads2, 1) expert_gemm_kernel(const __grid_
             }
             const uint32_t acc = tmem + buf * kTileN + (lanes << 16);
             if (EPI == EPI_GATED) {
-                for (uint32_t c = 0; c < kCols; c += 32) {
+                for (uint32_t c = c0; c < cols; c += kStride) {
                     float g[32], v[32];
-                    tc_load32(acc + c0 + c, g);
-                    tc_load32(acc + 128 + c0 + c, v);
-                    if (in < u.rows && col0 + c < p.ldh)
+                    tc_load32(acc + c, g);
+                    tc_load32(acc + u.half + c, v);
+                    if (in < u.rows)
                         finish_gated(p, (uint64_t)(u.row0 + in) * p.ldh + col0 + c, g, v);
                 }
             } else if (EPI == EPI_BACKWARD) {
-                for (uint32_t c = 0; c < kCols; c += 32) {
-                    float v[32];
-                    tc_load32(acc + c0 + c, v);
+                for (uint32_t c = c0; c < cols; c += kStride) {
                     Saved next;
-                    next.load(p, (uint64_t)(u.row0 + in) * p.ldh + col0 + c + 32, c + 32 < kCols && in < u.rows && col0 + c + 32 < p.ldh);
-                    if (col0 + c < p.ldh) {
-                        const uint64_t to = (uint64_t)(u.pad0 + in) * p.ldh + col0 + c;
+                    next.load(p, (uint64_t)(u.row0 + in) * p.ldh + col0 + c + kStride, in < u.rows && c + kStride < cols);
+                    const uint64_t to = (uint64_t)(u.pad0 + in) * p.ldh + col0 + c;
+#pragma unroll
+                    for (uint32_t h = 0; h < 2; ++h) {
+                        float v[16];
+                        tc_load16(acc + c + 16 * h, v);
                         if (in < u.rows)
-                            finish_backward(p, to, ahead, v);
+                            finish_backward(p, to + 16 * h, ahead, h, v);
                         else if (in < (u.rows + kPad - 1) / kPad * kPad)
-                            backward_zeros(p, to);
+                            backward_zeros(p, to + 16 * h);
                     }
                     ahead = next;
                 }
@@ -550,34 +565,34 @@ __global__ void __launch_bounds__(kThreads2, 1) expert_gemm_kernel(const __grid_
                 uint32_t rows;
                 uint16_t *out = unit_out<EPI>(p, u, rows);
                 if (p.vectors) {
-                    // a lane keeps its row, sixteen columns at a time, what it adds to asked for one step ahead
+                    // a lane keeps its row, sixteen columns at a time
                     uint16_t *at = out + (uint64_t)in * q.n + col0;
-                    Vals16 old;
-                    if (p.accumulate && in < rows && col0 < q.n)
-                        old.load(at, col0 + 8 < q.n);
-#pragma unroll 2
-                    for (uint32_t c = 0; c < kCols; c += 16) {
-                        float v[16];
+                    const uint32_t n = in < rows ? q.n - col0 : 0; // columns of this row from the tile's first on
+                    for (uint32_t c = c0; c < cols; c += kStride) {
+                        Vals16 old[2];
+#pragma unroll
+                        for (uint32_t h = 0; h < 2; ++h)
+                            if (p.accumulate && c + 16 * h < n)
+                                old[h].load(at + c + 16 * h, c + 16 * h + 8 < n);
+                        float v[32];
                         if (some) {
-                            tc_load16(acc + c0 + c, v);
+                            tc_load32(acc + c, v);
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
+                            for (int j = 0; j < 32; ++j)
                                 v[j] = 0.0f;
                         }
-                        Vals16 next;
-                        if (p.accumulate && c + 16 < kCols && in < rows && col0 + c + 16 < q.n)
-                            next.load(at + c + 16, col0 + c + 24 < q.n);
-                        if (in < rows && col0 + c < q.n)
-                            finish_store(p, at + c, col0 + c + 8 < q.n, old, v);
-                        old = next;
+#pragma unroll
+                        for (uint32_t h = 0; h < 2; ++h)
+                            if (c + 16 * h < n)
+                                finish_store(p, at + c + 16 * h, c + 16 * h + 8 < n, old[h], v + 16 * h);
                     }
                 } else {
                     // turned in shared memory, so that a warp's accesses run along a row
-                    for (uint32_t c = 0; c < kCols; c += 32) {
+                    for (uint32_t c = c0; c < cols; c += kStride) {
                         float v[32];
                         if (some) {
-                            tc_load32(acc + c0 + c, v);
+                            tc_load32(acc + c, v);
                         } else {
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
@@ -619,37 +634,33 @@ __global__ void __launch_bounds__(kThreads2, 1) expert_gemm_kernel(const __grid_
         for (; i < total; i += pairs) {
             const Unit u = unit_at<EPI>(p, table, i);
             const Problem &q = p.prob[u.prob];
-            const uint32_t in = u.m * kTileM + rank * 128 + lanes + lane, c0 = half * kCols, col0 = u.n * (2 * kCols) + c0;
-            float v[32];
-            if (EPI == EPI_GATED || EPI == EPI_BACKWARD) {
-                for (uint32_t c = 0; c < kCols && col0 + c < p.ldh; c += 32) {
+            const uint32_t in = u.m * kTileM + rank * 128 + lanes + lane;
+            const uint32_t cols = EPI == EPI_GATED ? u.half : 2 * u.half, col0 = u.n * (EPI == EPI_GATED ? 1 : 2) * p.half;
+            const bool none = EPI == EPI_WEIGHTS && u.kblocks == 0; // no sum to give up
+            for (uint32_t c = c0; c < cols; c += kStride) {
+                float v[32], w[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[j] = nan;
-                    if (EPI == EPI_GATED) {
-                        float w[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            w[j] = nan;
-                        if (in < u.rows)
-                            finish_gated(p, (uint64_t)(u.row0 + in) * p.ldh + col0 + c, v, w);
-                    } else {
-                        const uint64_t to = (uint64_t)(u.pad0 + in) * p.ldh + col0 + c;
-                        if (in < u.rows) {
-                            store32(p.h + to, v);
-                            store32(p.dg + to, v);
-                            store32(p.du + to, v);
-                        } else if (in < (u.rows + kPad - 1) / kPad * kPad) {
-                            backward_zeros(p, to);
-                        }
+                for (int j = 0; j < 32; ++j)
+                    v[j] = w[j] = nan;
+                if (EPI == EPI_GATED) {
+                    if (in < u.rows)
+                        finish_gated(p, (uint64_t)(u.row0 + in) * p.ldh + col0 + c, v, w);
+                } else if (EPI == EPI_BACKWARD) {
+                    const uint64_t to = (uint64_t)(u.pad0 + in) * p.ldh + col0 + c;
+                    if (in < u.rows) {
+                        store32(p.h + to, v);
+                        store32(p.dg + to, v);
+                        store32(p.du + to, v);
+                    } else if (in < (u.rows + kPad - 1) / kPad * kPad) {
+                        backward_zeros(p, to);
+                        backward_zeros(p, to + 16);
                     }
+                } else {
+                    uint32_t rows;
+                    uint16_t *out = unit_out<EPI>(p, u, rows);
+                    for (uint32_t k = col0 + c; in < rows && k < min(col0 + c + 32, q.n) && !(none && p.accumulate); ++k)
+                        st_value<DT_BF16>(out, (uint64_t)in * q.n + k, none ? 0.0f : nan);
                 }
-            } else {
-                uint32_t rows;
-                uint16_t *out = unit_out<EPI>(p, u, rows);
-                const bool none = EPI == EPI_WEIGHTS && u.kblocks == 0; // no sum to give up
-                for (uint32_t c = col0; in < rows && c < min(col0 + kCols, q.n) && !(none && p.accumulate); ++c)
-                    st_value<DT_BF16>(out, (uint64_t)in * q.n + c, none ? 0.0f : nan);
             }
         }
     }
@@ -971,25 +982,43 @@ struct PadParams {
         const int8_t *codes;   // rows of `width`
         const uint8_t *scales;
         uint16_t *dst; // rows of ld
+        int tails;     // only the last, partial block of 64 rows of each expert
     } m[2];
+    uint32_t nrows; // matrices of rows (m); then those of `weights`
     uint32_t cols, ld, width;
     int vector; // src: 16-byte aligned rows of whole vectors
+    PackParams weights;
 };
 
 // Every expert's rows at their place in the padded layout and zeros behind them,
-// a warp a row, blockIdx.y the matrix.
+// a warp a row; in the same launch the weights that TMA cannot address, to rows
+// of a padded stride.  blockIdx.y is the matrix.
 __global__ void __launch_bounds__(256) expert_pad_kernel(const __grid_constant__ PadParams q)
 {
     chain_entry();
     __shared__ int32_t tables[3 * (CCL_MAX_EXPERTS + 2)];
+    if (blockIdx.y >= q.nrows) {
+        pack_operand(q.weights, blockIdx.y - q.nrows);
+        return;
+    }
     const ExpertParams &p = q.p;
     const Table t{tables, tables + CCL_MAX_EXPERTS + 2, tables + 2 * (CCL_MAX_EXPERTS + 2)};
     make_table(p, t, kTileM);
     const auto &m = q.m[blockIdx.y];
-    const uint32_t lane = threadIdx.x & 31, total = (uint32_t)t.pad0[p.experts];
-    for (uint32_t r = blockIdx.x * 8 + (threadIdx.x >> 5); r < total; r += gridDim.x * 8) {
-        const uint32_t e = expert_at(t.pad0, p.experts, (int32_t)r), in = r - (uint32_t)t.pad0[e];
-        const uint32_t row = (uint32_t)t.row0[e] + in;
+    const uint32_t lane = threadIdx.x & 31, total = m.tails ? p.experts * kPad : (uint32_t)t.pad0[p.experts];
+    for (uint32_t i = blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += gridDim.x * 8) {
+        uint32_t e, in; // row `in` of expert e
+        if (m.tails) {
+            e = i / kPad;
+            const uint32_t n = (uint32_t)(t.row0[e + 1] - t.row0[e]);
+            if (n % kPad == 0)
+                continue;
+            in = n / kPad * kPad + i % kPad;
+        } else {
+            e = expert_at(t.pad0, p.experts, (int32_t)i);
+            in = i - (uint32_t)t.pad0[e];
+        }
+        const uint32_t r = (uint32_t)t.pad0[e] + in, row = (uint32_t)t.row0[e] + in;
         const bool has = row < (uint32_t)t.row0[e + 1];
         uint16_t *dst = m.dst + (uint64_t)r * q.ld;
         if (!has) {
@@ -1101,7 +1130,7 @@ bool make_plan(size_t r, size_t e, size_t d, size_t f, bool backward, bool align
         (uint64_t)d * f > (1ull << 38) /* an expert's stride in its tensor map */ || (uint64_t)e * d * f > (1ull << 44))
         return false;
     const uint64_t pads = r + (kPad - 1) * std::min(r, e);
-    if (pads > 0x7fffffff) // rows are 32-bit
+    if (pads > kMaxRows) // rows are 32-bit
         return false;
     *p = ExpertPlan{};
     p->r = r;
@@ -1112,8 +1141,8 @@ bool make_plan(size_t r, size_t e, size_t d, size_t f, bool backward, bool align
     const bool pd = p->dp != d || !aligned, pf = p->fp != f || !aligned;
     const uint64_t active = std::min(r, e);
     // units are counted in 32 bits
-    const uint64_t most = ((r + kTileM - 1) / kTileM + active) * std::max(tiles_of(f, 128), tiles_of(d, kTileN));
-    const uint64_t weights = (uint64_t)e * 3 * tiles_of(f, kTileM) * tiles_of(d, kTileN) + e * (tiles_of(f, kTileM) + tiles_of(d, kTileN));
+    const uint64_t most = ((r + kTileM - 1) / kTileM + active) * std::max(tiles_of(f, 32), tiles_of(d, 64));
+    const uint64_t weights = (uint64_t)e * 3 * (tiles_of(f, 64) + 1) * (tiles_of(d, 64) + 1);
     if (most > 0x3fffffff || weights > 0x3fffffff)
         return false;
     p->few = !backward && e && r <= kFewRows * e;
@@ -1154,11 +1183,11 @@ bool make_plan(size_t r, size_t e, size_t d, size_t f, bool backward, bool align
     return true;
 }
 
-cudaLaunchConfig_t pair_launch(cudaLaunchAttribute *attr, unsigned pairs, cudaStream_t stream)
+cudaLaunchConfig_t pair_launch(cudaLaunchAttribute *attr, unsigned pairs, unsigned threads, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs);
-    cfg.blockDim = dim3(kThreads2);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = kGemmSmem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1179,7 +1208,7 @@ template <int EPI, bool A_MN, bool B_MN> cudaError_t launch_gemm(const ExpertPar
     if (e != cudaSuccess)
         return e;
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = pair_launch(attr, (unsigned)std::max<uint64_t>(1, std::min<uint64_t>(units, kPairs)), stream);
+    const cudaLaunchConfig_t cfg = pair_launch(attr, (unsigned)std::max<uint64_t>(1, std::min<uint64_t>(units, kPairs)), kGemmThreads<EPI>, stream);
     if ((e = cudaLaunchKernelEx(&cfg, expert_gemm_kernel<EPI, A_MN, B_MN>, p)) == cudaSuccess)
         count_launches(1);
     return e;
@@ -1282,6 +1311,13 @@ ExpertParams params_of(const ExpertArgs &a, const ExpertPlan &pl)
     return p;
 }
 
+// Columns of a pair's tile: 256, whose products reuse what they read most, or
+// fewer where that leaves pairs without a tile (units of 256 columns: `wide`).
+uint32_t half_tile(uint64_t wide)
+{
+    return wide * 2 <= kPairs ? 32 : wide <= kPairs ? 64 : 128;
+}
+
 void set_problem(Problem &q, uint64_t n, uint32_t tile, uint64_t k, uint32_t segs)
 {
     q.n = (uint32_t)n;
@@ -1336,13 +1372,15 @@ ccl_status_t expert_ffn_impl(const ExpertArgs &a, void *out, cudaStream_t stream
         return from_cuda(launch_few<EPI_STORE>(p, tiles, stream));
     }
     const uint64_t tiles = a.r / kTileM + active; // at most
-    set_problem(q, a.f, 128, a.d, 1);
+    p.half = half_tile(tiles * tiles_of(a.f, 128));
+    set_problem(q, a.f, p.half, a.d, 1);
     p.vectors = 1;
     if (!encode_rows(&q.a[0], x, false) || !encode_experts(&q.b[0], w2[0], a.e, false) || !encode_experts(&q.b[1], w2[1], a.e, false))
         return CCL_ERR_CUDA;
     if (cudaError_t e = launch_gemm<EPI_GATED, false, false>(p, tiles * q.nt, stream))
         return from_cuda(e);
-    set_problem(q, a.d, kTileN, a.f, 1);
+    p.half = half_tile(tiles * tiles_of(a.d, kTileN));
+    set_problem(q, a.d, 2 * p.half, a.f, 1);
     q.out = out;
     p.vectors = a.d % 8 == 0 && (uintptr_t)out % 16 == 0;
     if (!encode_rows(&q.a[0], h, false) || !encode_experts(&q.b[0], wd, a.e, false))
@@ -1402,14 +1440,18 @@ ccl_status_t expert_ffn_grad_impl(const ExpertArgs &a, const void *dy, void *dx,
     const Matrix x{work + pl.x, pl.rp, a.d, pl.dp}, y{work + pl.y, pl.rp, a.d, pl.dp};
     const Matrix h{work + pl.h, pl.rp, a.f, pl.fw};
     const Matrix d2[2] = {{work + pl.dg, pl.rp, a.f, pl.fw}, {work + pl.du, pl.rp, a.f, pl.fw}};
-    if ((e = ops.copy(stream)))
-        return from_cuda(e);
     ExpertParams p = params_of(a, pl);
-    p.padded = 1;
     PadParams pad{};
+    pad.weights = ops.params();
+    pad.nrows = need_x ? 2 : 1;
     pad.p = p;
     pad.m[0].src = static_cast<const uint16_t *>(dy);
     pad.m[0].dst = reinterpret_cast<uint16_t *>(work + pl.y);
+    // rows that TMA can address are read where they lie, but for the partial blocks
+    const bool direct_y = a.d % 8 == 0 && all_aligned({dy}), direct_x = need_x && !eight && a.d % 8 == 0 && all_aligned({a.x});
+    const Matrix ly{dy, a.r, a.d, a.d}, lx{a.x, a.r, a.d, a.d};
+    pad.m[0].tails = direct_y;
+    pad.m[1].tails = direct_x;
     pad.m[1].src = static_cast<const uint16_t *>(a.x);
     pad.m[1].codes = a.x_codes;
     pad.m[1].scales = a.x_scales;
@@ -1418,19 +1460,24 @@ ccl_status_t expert_ffn_grad_impl(const ExpertArgs &a, const void *dy, void *dx,
     pad.ld = (uint32_t)pl.dp;
     pad.width = (uint32_t)xw;
     pad.vector = a.d % 8 == 0 && all_aligned({dy, need_x ? a.x : nullptr});
-    if ((e = launch_chained(expert_pad_kernel, dim3((unsigned)std::min<uint64_t>((pl.rp + 7) / 8, 8 * kSms), need_x ? 2 : 1), dim3(256), 0, stream, pad)))
+    const uint64_t most = std::max((pl.rp + 7) / 8, (ops.most() + 255) / 256);
+    if ((e = launch_chained(expert_pad_kernel, dim3((unsigned)std::min<uint64_t>(most, 8 * kSms), pad.nrows + (unsigned)pad.weights.n), dim3(256), 0, stream, pad)))
         return from_cuda(e);
     count_launches(1);
     const uint64_t tiles = a.r / kTileM + std::min<uint64_t>(a.r, a.e); // at most
     Problem &q = p.prob[0];
-    set_problem(q, a.f, kTileN, a.d, 1);
+    p.half = half_tile(tiles * tiles_of(a.f, kTileN));
+    set_problem(q, a.f, 2 * p.half, a.d, 1);
     p.vectors = 1;
-    if (!encode_rows(&q.a[0], y, false) || !encode_experts(&q.b[0], wd, a.e, true))
+    p.padded = !direct_y;
+    if (!encode_rows(&q.a[0], direct_y ? ly : y, false) || !encode_experts(&q.b[0], wd, a.e, true))
         return CCL_ERR_CUDA;
     if ((e = launch_gemm<EPI_BACKWARD, false, true>(p, tiles * q.nt, stream)))
         return from_cuda(e);
+    p.padded = 1;
     if (dx) {
-        set_problem(q, a.d, kTileN, a.f, 2);
+        p.half = half_tile(tiles * tiles_of(a.d, kTileN));
+        set_problem(q, a.d, 2 * p.half, a.f, 2);
         q.out = dx;
         p.vectors = a.d % 8 == 0 && (uintptr_t)dx % 16 == 0;
         for (int i = 0; i < 2; ++i)
@@ -1446,6 +1493,7 @@ ccl_status_t expert_ffn_grad_impl(const ExpertArgs &a, const void *dy, void *dx,
     p.vectors = a.d % 8 == 0 && a.f % 8 == 0;
     p.nprob = 0;
     uint64_t units = 0;
+    p.half = half_tile(a.e * ((dwg != nullptr) + (dwu != nullptr) + (dwd != nullptr)) * tiles_of(a.f, kTileM) * tiles_of(a.d, kTileN));
     const Matrix *am[3] = {&d2[0], &d2[1], &y}, *bm[3] = {&x, &x, &h};
     void *out[3] = {dwg, dwu, dwd};
     for (int i = 0; i < 3; ++i)
@@ -1453,10 +1501,13 @@ ccl_status_t expert_ffn_grad_impl(const ExpertArgs &a, const void *dy, void *dx,
             Problem &o = p.prob[p.nprob++];
             o.m = (uint32_t)am[i]->cols;
             o.mt = tiles_of(o.m, kTileM);
-            set_problem(o, bm[i]->cols, kTileN, 0, 1);
+            set_problem(o, bm[i]->cols, 2 * p.half, 0, 1);
             o.out = out[i];
             p.vectors = p.vectors && (uintptr_t)out[i] % 16 == 0;
-            if (!encode_rows(&o.a[0], *am[i], true) || !encode_rows(&o.b[0], *bm[i], true))
+            o.direct_a = i == 2 && direct_y;
+            o.direct_b = i < 2 && direct_x;
+            if (!encode_rows(&o.a[0], *am[i], true) || !encode_rows(&o.b[0], *bm[i], true) || (o.direct_a && !encode_rows(&o.a[1], ly, true)) ||
+                (o.direct_b && !encode_rows(&o.b[1], lx, true)))
                 return CCL_ERR_CUDA;
             units += (uint64_t)o.mt * o.nt * a.e;
         }

@@ -274,12 +274,11 @@ struct PackParams {
     int n;
 };
 
-// Rows of `cols` elements to rows `ld` apart (ld a multiple of 8), the rest of
-// a row zero; a thread writes a vector of eight, blockIdx.y is the matrix.
-static __global__ void __launch_bounds__(256) pack_operands_kernel(const __grid_constant__ PackParams p)
+// Rows of `cols` elements of the i-th matrix to rows `ld` apart (ld a multiple
+// of 8), the rest of a row zero; a thread (of 256) writes a vector of eight.
+__device__ __forceinline__ void pack_operand(const PackParams &p, uint32_t i)
 {
-    chain_entry();
-    const auto &m = p.m[blockIdx.y];
+    const auto &m = p.m[i];
     const uint32_t per = m.ld / 8;
     for (uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x; e < m.vectors; e += (uint64_t)gridDim.x * 256) {
         const uint64_t r = m.vectors >> 32 ? e / per : (uint32_t)e / per;
@@ -306,6 +305,12 @@ static __global__ void __launch_bounds__(256) pack_operands_kernel(const __grid_
             h[i] = c + i < m.cols ? gload<uint16_t>(src + i) : 0;
         st16(m.dst + e * 8, make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16));
     }
+}
+
+static __global__ void __launch_bounds__(256) pack_operands_kernel(const __grid_constant__ PackParams p)
+{
+    chain_entry();
+    pack_operand(p, blockIdx.y); // the matrix
 }
 
 // ------------------------------------------------------------------ host side
@@ -360,6 +365,10 @@ class Operands {
             count_launches(1);
         return e;
     }
+
+    // for a kernel that makes the copies beside its own work
+    const PackParams &params() const { return p_; }
+    uint64_t most() const { return most_; } // vectors of the largest one
 
   private:
     PackParams p_{};
