@@ -480,19 +480,11 @@ __global__ void __launch_bounds__(kGemmThreads<EPI>, 1) expert_gemm_kernel(const
         }
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // issuer: fp32 accumulator, bf16 operands, their majorness, N, M
-        const uint32_t form = 1u << 4 | 1u << 7 | 1u << 10 | (A_MN ? 1u << 15 : 0) | (B_MN ? 1u << 16 : 0) | (kTileM >> 4) << 24;
+        constexpr uint32_t form = 1u << 4 | 1u << 7 | 1u << 10 | (A_MN ? 1u << 15 : 0) | (B_MN ? 1u << 16 : 0) | (kTileM >> 4) << 24;
         uint32_t s = 0, phase = 0, t = 0;
         bool ok = p.wait_ns != 0;
-        for (uint32_t i = pair; ok && i < total; i += pairs) {
-            const Unit u = unit_at<EPI>(p, table, i);
-            const uint32_t idesc = form | (2 * u.half >> 3) << 17;
-            if (u.kblocks == 0)
-                continue; // an expert without rows: the epilogue needs no accumulator
-            const uint32_t buf = t & 1;
-            if (!(ok = mbar_wait(acc_empty + 8 * buf, ((t >> 1) & 1) ^ 1, &gave_up, p.wait_ns)))
-                break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            for (uint32_t kb = 0; kb < u.kblocks; ++kb) {
+        auto products = [&](uint32_t buf, uint32_t kblocks, uint32_t idesc) {
+            for (uint32_t kb = 0; kb < kblocks; ++kb) {
                 if (!(ok = mbar_wait(full + 8 * s, phase, &gave_up, p.wait_ns)))
                     break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -507,6 +499,20 @@ __global__ void __launch_bounds__(kGemmThreads<EPI>, 1) expert_gemm_kernel(const
                     phase ^= 1;
                 }
             }
+        };
+        for (uint32_t i = pair; ok && i < total; i += pairs) {
+            const Unit u = unit_at<EPI>(p, table, i);
+            if (u.kblocks == 0)
+                continue; // an expert without rows: the epilogue needs no accumulator
+            const uint32_t buf = t & 1;
+            if (!(ok = mbar_wait(acc_empty + 8 * buf, ((t >> 1) & 1) ^ 1, &gave_up, p.wait_ns)))
+                break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            // a tile of full width by a constant: a descriptor that is not costs the products 3 %
+            if (u.half == 128)
+                products(buf, u.kblocks, form | (kTileN >> 3) << 17);
+            else
+                products(buf, u.kblocks, form | (2 * u.half >> 3) << 17);
             if (ok)
                 tc_commit(acc_full + 8 * buf);
             ++t;
