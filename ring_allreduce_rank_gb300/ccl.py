@@ -537,11 +537,11 @@ def _flat(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype):
     """Pointer of a contiguous tensor of the given shape and type (None: a null pointer)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous tensor of shape %s" % (name, tuple(shape)))
-    return t.data_ptr()
+    raise ValueError("%s must be a contiguous tensor of shape %s" % (name, tuple(shape)))
 
 
 def _on_gpu(*ts: Optional[torch.Tensor]) -> int:
@@ -585,7 +585,7 @@ def _work(work: Optional[torch.Tensor], nbytes: int, like: torch.Tensor, stream)
             work = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
     elif not work.is_contiguous():
         raise ValueError("work must be a contiguous CUDA tensor")
-    return work, work.numel() * work.element_size()
+    return work, work.nbytes
 
 
 def ccl_embedding(table: torch.Tensor, ids: torch.Tensor, out: torch.Tensor, scale: float = 1.0, first_row: int = 0,
@@ -783,9 +783,10 @@ def ccl_plan_expert_ffn_work_bytes(nrows: int, experts: int, dim: int, ffn: int,
 
 def _choices(t: torch.Tensor, name: str):
     """(pointer, tokens, top) of a contiguous [tokens, top] int32 tensor."""
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError("%s must be a tensor of shape [tokens, top]" % name)
-    return (_flat(t, name, t.shape, torch.int32), *t.shape)
+    return _flat(t, name, shape, torch.int32), shape[0], shape[1]
 
 
 def ccl_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, lse: torch.Tensor, counts: torch.Tensor,
@@ -805,11 +806,11 @@ def ccl_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, ls
     ip, tokens, top = _choices(ids, "ids")
     if tokens != n:
         raise ValueError("ids has %d tokens, expected %d" % (tokens, n))
-    f32 = torch.float32
+    f32, of_experts = torch.float32, (experts,)
     ptrs = (ip, _flat(weights, "weights", (n, top), f32), _flat(lse, "lse", (n,), f32),
-            _flat(counts, "counts", (experts + 1,), torch.int32), _flat(load, "load", (experts,), f32),
-            _flat(importance, "importance", (experts,), f32), _flat(losses, "losses", (2,), f32))
-    vp = None if valid is None else _flat(valid, "valid", (n,), valid.dtype if valid.dtype == torch.bool else torch.uint8)
+            _flat(counts, "counts", (experts + 1,), torch.int32), _flat(load, "load", of_experts, f32),
+            _flat(importance, "importance", of_experts, f32), _flat(losses, "losses", (2,), f32))
+    vp = None if valid is None else _flat(valid, "valid", (n,), torch.bool if valid.dtype is torch.bool else torch.uint8)
     work, nbytes = _work(work, 0 if work is not None else ccl_plan_route_work_bytes(n, experts), logits, stream)
     _check(lib().ccl_route(lp, n, experts, ls, _dtype(logits), vp, top, int(bool(normalize)), *ptrs, work.data_ptr(), nbytes,
                            _stream_on(stream, dev)), "ccl_route")
@@ -922,8 +923,8 @@ def ccl_combine_grad(grad_out: torch.Tensor, place: torch.Tensor, rows: Optional
 
 def _act8(pair, name: str, lead, cols: int):
     """Pointers of (codes, scales) of rows of `cols` values."""
-    width = -(-cols // ACT8_BLOCK) * ACT8_BLOCK
     codes, scales = pair
+    width = (cols + ACT8_BLOCK - 1) // ACT8_BLOCK * ACT8_BLOCK
     return (_flat(codes, name + "'s codes", (*lead, width), torch.int8),
             _flat(scales, name + "'s scales", (*lead, width // ACT8_BLOCK), torch.uint8))
 

@@ -27,7 +27,7 @@ def _built():
     ccl.lib()
 
 
-def _route(L, z=1 * T40, n=100, e=8, zs=8, dt=0, valid=None, top=2, norm=1, ids=2 * T40, w=3 * T40, lse=4 * T40, counts=5 * T40, load=6 * T40,
+def _route(L, z=1 * T40, n=1000, e=8, zs=8, dt=0, valid=None, top=2, norm=1, ids=2 * T40, w=3 * T40, lse=4 * T40, counts=5 * T40, load=6 * T40,
            imp=7 * T40, loss=8 * T40, work=9 * T40, nbytes=1 << 20):
     return L.ccl_route(z, n, e, zs, dt, valid, top, norm, ids, w, lse, counts, load, imp, loss, work, nbytes, None)
 
