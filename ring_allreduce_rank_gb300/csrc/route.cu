@@ -17,15 +17,20 @@
 // the groups of a CTA in order, the CTAs in order: no float is added by an
 // atomic.  Bound by memory bandwidth for many tokens, by the launch and one
 // row's chain of reductions for few.
+#include <cooperative_groups.h>
+
 #include <vector>
 
 #include "../../include/ccl.h"
 #include "ccl_internal.h"
 #include "step_ops.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace ccl {
 namespace {
 
+constexpr int kJoinCtas = 8; // one portable cluster
 constexpr size_t kMaxTokens = 0x7fffffff;
 constexpr int kRouteThreads = 256; // route_grad_kernel's
 // route_kernel's, at most: one CTA an SM with eight values a lane, so that 152
@@ -65,6 +70,10 @@ __device__ __forceinline__ float from_ordered(uint32_t k)
 {
     return __uint_as_float(k == kNaN ? 0x7fffffffu : k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
+
+// e^x for x <= 0, to 2 + 1.2 |x| units in the last place: as good as x, the
+// rounded difference of two logits, is for it.
+__device__ __forceinline__ float exp_of(float x) { return __expf(x); }
 
 template <int L> __device__ __forceinline__ float group_sum(float v)
 {
@@ -186,7 +195,7 @@ template <int DT, int L, int V, int N> __global__ void __launch_bounds__(route_t
     // whole warps go round together: rows past the last are rows without experts
     const uint32_t rounds = (p.ntokens + stride - 1) / stride;
     auto fetch = [&](uint32_t round, float *v) {
-        const uint64_t t = (uint64_t)round * stride + blockIdx.x * groups + group;
+        const uint64_t t = (uint64_t)round * stride + group * p.ctas + blockIdx.x; // a partly filled last round falls on every CTA
         if (round < rounds && t < p.ntokens && (!p.valid || gload<uint8_t>(p.valid + t))) {
             load_row<DT, L, V, N>(p, p.logits + t * p.pitch, lane, v);
         } else {
@@ -200,7 +209,7 @@ template <int DT, int L, int V, int N> __global__ void __launch_bounds__(route_t
     if (kAhead)
         fetch(0, f);
     for (uint32_t round = 0; round < rounds; ++round) {
-        const uint64_t t = (uint64_t)round * stride + blockIdx.x * groups + group;
+        const uint64_t t = (uint64_t)round * stride + group * p.ctas + blockIdx.x; // a partly filled last round falls on every CTA
         if (kAhead)
             fetch(round + 1, next);
         else
@@ -218,7 +227,7 @@ template <int DT, int L, int V, int N> __global__ void __launch_bounds__(route_t
         float total = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            f[i] = expf(__fsub_rn(f[i], m)); // 0 for -inf
+            f[i] = exp_of(__fsub_rn(f[i], m)); // 0 for -inf
             total = __fadd_rn(total, f[i]);
         }
         total = group_sum<L>(total);
@@ -260,7 +269,7 @@ template <int DT, int L, int V, int N> __global__ void __launch_bounds__(route_t
         float w[kMine], kept = 0.0f;
 #pragma unroll
         for (int s0 = 0; s0 < kMine; ++s0) {
-            w[s0] = id[s0] >= 0 ? expf(__fsub_rn(from_ordered(mine[s0]), m)) : 0.0f;
+            w[s0] = id[s0] >= 0 ? exp_of(__fsub_rn(from_ordered(mine[s0]), m)) : 0.0f;
             kept = __fadd_rn(kept, w[s0]);
         }
         const float by = p.normalize ? __fdiv_rn(1.0f, group_sum<L>(kept)) : inv;
@@ -332,29 +341,32 @@ template <int DT, int L, int V, int N> __global__ void __launch_bounds__(route_t
     }
 }
 
-// The CTAs' partial sums: 1024 / columns threads a column take runs of the CTAs
-// in order, sixteen loads in flight, and the runs are joined in order.
-__global__ void __launch_bounds__(1024) route_join_kernel(const __grid_constant__ RouteParams p)
+// The CTAs' partial sums, by one cluster: each of its CTAs takes a run of rows,
+// 1024 / columns threads a column take parts of it, eight loads in flight, and
+// the parts, then the runs, are joined in order.
+__global__ void __cluster_dims__(kJoinCtas) __launch_bounds__(1024) route_join_kernel(const __grid_constant__ RouteParams p)
 {
     chain_entry();
+    cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ float shared[]; // sums [parts][columns], hits [parts][columns]
-    const uint32_t n = p.experts + 2, parts = max(1024u / n, 1u), run = (p.ctas + parts - 1) / parts;
+    const uint32_t n = p.experts + 2, parts = max(1024u / n, 1u), per = (p.ctas + kJoinCtas - 1) / kJoinCtas, run = (per + parts - 1) / parts;
+    const uint32_t first = min(cluster.block_rank() * per, p.ctas), past = min(first + per, p.ctas);
     float *sums = shared;
     int32_t *hits = reinterpret_cast<int32_t *>(shared + parts * n);
     for (uint32_t i = threadIdx.x; i < parts * n; i += 1024) {
-        const uint32_t part = i / n, c = i - part * n, b1 = min((part + 1) * run, p.ctas);
+        const uint32_t part = i / n, c = i - part * n, b1 = min(first + (part + 1) * run, past);
         float s = 0.0f;
         int32_t h = 0;
-        for (uint32_t b0 = part * run; b0 < b1; b0 += 16) {
-            float x[16];
-            int32_t y[16];
+        for (uint32_t b0 = first + part * run; b0 < b1; b0 += 8) {
+            float x[8];
+            int32_t y[8];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 x[j] = b0 + j < b1 && c + 1 < n ? gload<float>(p.sums + (uint64_t)(b0 + j) * (n - 1) + c) : 0.0f;
                 y[j] = b0 + j < b1 ? gload<int32_t>(p.hits + (uint64_t)(b0 + j) * n + c) : 0;
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 s = __fadd_rn(s, x[j]);
                 h += y[j];
             }
@@ -373,8 +385,27 @@ __global__ void __launch_bounds__(1024) route_join_kernel(const __grid_constant_
         sums[c] = s;
         hits[c] = h;
     }
-    __syncthreads();
-    finish_losses(p, sums, hits);
+    cluster.sync();
+    if (cluster.block_rank() == 0)
+        for (uint32_t c = threadIdx.x; c < n; c += 1024) {
+            float s[kJoinCtas];
+            int32_t h[kJoinCtas];
+#pragma unroll
+            for (int k = 0; k < kJoinCtas; ++k) {
+                s[k] = cluster.map_shared_rank(sums, k)[c];
+                h[k] = cluster.map_shared_rank(hits, k)[c];
+            }
+#pragma unroll
+            for (int k = 1; k < kJoinCtas; ++k) {
+                s[0] = __fadd_rn(s[0], s[k]);
+                h[0] += h[k];
+            }
+            sums[c] = s[0];
+            hits[c] = h[0];
+        }
+    cluster.sync(); // the others' memory has been read
+    if (cluster.block_rank() == 0)
+        finish_losses(p, sums, hits);
 }
 
 template <int DT, int L, int V, int N> __global__ void __launch_bounds__(kRouteThreads) route_grad_kernel(const __grid_constant__ RouteParams p)
@@ -415,7 +446,7 @@ template <int DT, int L, int V, int N> __global__ void __launch_bounds__(kRouteT
         float kept = 0.0f, gw = 0.0f;
 #pragma unroll
         for (int s0 = 0; s0 < kMine; ++s0) {
-            q[s0] = id[s0] >= 0 ? expf(__fsub_rn(ld_value<DT>(row, (uint32_t)id[s0]), lse)) : 0.0f;
+            q[s0] = id[s0] >= 0 ? exp_of(__fsub_rn(ld_value<DT>(row, (uint32_t)id[s0]), lse)) : 0.0f;
             kept = __fadd_rn(kept, q[s0]);
             gw = __fmaf_rn(g[s0], q[s0], gw);
         }
@@ -434,7 +465,7 @@ template <int DT, int L, int V, int N> __global__ void __launch_bounds__(kRouteT
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const uint32_t c = column<L, N>(lane, i);
-            f[i] = live && c < E ? expf(__fsub_rn(f[i], lse)) : 0.0f;
+            f[i] = live && c < E ? exp_of(__fsub_rn(f[i], lse)) : 0.0f;
             inner = __fmaf_rn(c < E ? pull[c] : 0.0f, f[i], inner);
         }
         inner = group_sum<L>(inner);
@@ -588,7 +619,7 @@ ccl_status_t route_impl(const void *logits, size_t ntokens, size_t experts, size
     cudaError_t e = launch_route<false>(dtype, p, pl.ctas, pl.threads, stream);
     if (e == cudaSuccess && pl.ctas > 1) {
         const size_t n = experts + 2, parts = std::max<size_t>(1024 / n, 1);
-        e = launch_chained(route_join_kernel, dim3(1), dim3(1024), parts * n * 8, stream, p);
+        e = launch_chained(route_join_kernel, dim3(kJoinCtas), dim3(1024), parts * n * 8, stream, p);
         if (e == cudaSuccess)
             count_launches(1);
     }
