@@ -5,8 +5,8 @@
 // columns rounded up to 32, so that every row of codes is whole 32-byte
 // vectors.  Bound by memory bandwidth: each value is read once and written
 // once.  A thread takes a whole block, so that no value crosses lanes; where
-// the source's rows are no whole vectors a warp takes a block, a lane a value,
-// so that its loads still run along the row.
+// the rows are no whole vectors, values pass a warp's 32 x 32 in shared memory,
+// so that its accesses still run along a row.
 #include <vector>
 
 #include "../../include/ccl.h"
@@ -69,32 +69,43 @@ template <int DT, int W> __global__ void __launch_bounds__(kActThreads) act8_pac
         st32(p.codes + i * kActBlock, lo, hi);
         gstore<uint8_t>(p.bytes + i, (uint8_t)byte);
     } else {
+        // a warp takes 32 blocks: their values a block at a time, a lane a value,
+        // turned in shared memory so that a lane then has a block
+        __shared__ float turned[kActThreads / 32][32][33];
         const uint32_t lane = threadIdx.x & 31;
-        const uint64_t warps = (uint64_t)gridDim.x * (kActThreads / 32);
-        constexpr int AHEAD = 4;
-        for (uint64_t i0 = (uint64_t)blockIdx.x * (kActThreads / 32) + threadIdx.x / 32; i0 < p.blocks; i0 += AHEAD * warps) {
-            float f[AHEAD];
+        float(*mine)[33] = turned[threadIdx.x / 32];
+        const uint64_t i0 = ((uint64_t)blockIdx.x * (kActThreads / 32) + threadIdx.x / 32) * 32;
+        if (i0 >= p.blocks)
+            return;
+        uint64_t r = row_of(p, i0);
+        uint32_t b = (uint32_t)(i0 - r * p.per);
+        const uint32_t n = (uint32_t)umin64(32, p.blocks - i0);
 #pragma unroll
-            for (int j = 0; j < AHEAD; ++j) {
-                const uint64_t i = i0 + j * warps;
-                f[j] = 0.0f;
-                if (i < p.blocks) {
-                    const uint64_t r = row_of(p, i);
-                    const uint32_t c = (uint32_t)(i - r * p.per) * kActBlock + lane;
-                    if (c < p.cols)
-                        f[j] = ld_value<DT>(p.x + r * p.pitch, c);
+        for (uint32_t j0 = 0; j0 < 32; j0 += 8) {
+            float v[8];
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) {
+                const uint32_t c = b * kActBlock + lane;
+                v[j] = j0 + j < n && c < p.cols ? ld_value<DT>(p.x + r * p.pitch, c) : 0.0f;
+                if (++b == p.per) {
+                    b = 0;
+                    ++r;
                 }
             }
 #pragma unroll
-            for (int j = 0; j < AHEAD; ++j) {
-                const uint64_t i = i0 + j * warps;
-                const uint32_t byte = act8_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(f[j]) & 0x7fffffffu));
-                if (i < p.blocks) {
-                    gstore<uint8_t>(p.codes + i * kActBlock + lane, byte == kActNan ? 0 : (uint8_t)act8_code(f[j], act8_inverse(byte)));
-                    if (lane == 0)
-                        gstore<uint8_t>(p.bytes + i, (uint8_t)byte);
-                }
-            }
+            for (uint32_t j = 0; j < 8; ++j)
+                mine[j0 + j][lane] = v[j];
+        }
+        __syncwarp();
+        if (lane < n) {
+            float f[32];
+            uint4 lo, hi;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                f[j] = mine[lane][j];
+            const uint32_t byte = act8_encode(f, lo, hi);
+            st32(p.codes + (i0 + lane) * kActBlock, lo, hi);
+            gstore<uint8_t>(p.bytes + i0 + lane, (uint8_t)byte);
         }
     }
 }
@@ -123,14 +134,34 @@ template <int DT, int W> __global__ void __launch_bounds__(kActThreads) act8_unp
                     st16(dst + j * 16, pack<DT>(f + j * V));
             }
     } else {
+        __shared__ float turned[kActThreads / 32][32][33];
         const uint32_t lane = threadIdx.x & 31;
-        const uint64_t warps = (uint64_t)gridDim.x * (kActThreads / 32);
-        for (uint64_t i = (uint64_t)blockIdx.x * (kActThreads / 32) + threadIdx.x / 32; i < p.blocks; i += warps) {
-            const uint64_t r = row_of(p, i);
-            const uint32_t c = (uint32_t)(i - r * p.per) * kActBlock + lane;
-            const float q = (float)(int8_t)gload<uint8_t>(p.codes + i * kActBlock + lane);
+        float(*mine)[33] = turned[threadIdx.x / 32];
+        const uint64_t i0 = ((uint64_t)blockIdx.x * (kActThreads / 32) + threadIdx.x / 32) * 32;
+        if (i0 >= p.blocks)
+            return;
+        uint64_t r = row_of(p, i0);
+        uint32_t b = (uint32_t)(i0 - r * p.per);
+        const uint32_t n = (uint32_t)umin64(32, p.blocks - i0);
+        if (lane < n) {
+            uint4 lo, hi;
+            float f[32];
+            ld32(p.codes + (i0 + lane) * kActBlock, lo, hi);
+            act8_decode(lo, hi, act8_step(gload<uint8_t>(p.bytes + i0 + lane)), f);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                mine[lane][j] = f[j];
+        }
+        __syncwarp();
+#pragma unroll 8
+        for (uint32_t j = 0; j < n; ++j) {
+            const uint32_t c = b * kActBlock + lane;
             if (c < p.cols)
-                st_value<DT>(p.x + r * p.pitch, c, __fmul_rn(q, act8_step(gload<uint8_t>(p.bytes + i))));
+                st_value<DT>(p.x + r * p.pitch, c, mine[j][lane]);
+            if (++b == p.per) {
+                b = 0;
+                ++r;
+            }
         }
     }
 }
@@ -168,13 +199,10 @@ ccl_status_t act8_impl(bool pack, const void *x, size_t rows, size_t cols, size_
     p.per = (uint32_t)per;
     const uintptr_t all = (uintptr_t)x | p.pitch | cols * es;
     const int width = all % 32 == 0 ? 32 : all % 16 == 0 ? 16 : 0;
-    const bool vec = width != 0;
     // a thread a block: the grid's 2^31 CTAs hold 2^39 of them, and 2^31 rows of 2^24 columns have 2^50
-    if (vec && p.blocks > (uint64_t)0x7fffffff * kActThreads)
+    if (p.blocks > (uint64_t)0x7fffffff * kActThreads)
         return CCL_ERR_INVALID_ARG;
-    const uint64_t per_cta = vec ? kActThreads : kActThreads / 32;
-    const uint64_t ctas = (p.blocks + per_cta - 1) / per_cta;
-    const dim3 grid((unsigned)(vec ? ctas : std::min<uint64_t>(ctas, 8 * 152))), block(kActThreads);
+    const dim3 grid((unsigned)((p.blocks + kActThreads - 1) / kActThreads)), block(kActThreads);
     void (*k)(Act8Params);
 #define CCL_ACT8_KERNEL(kernel)                                                                                        \
     (dtype == CCL_FP32 ? (width == 32 ? kernel<DT_FP32, 32> : width == 16 ? kernel<DT_FP32, 16> : kernel<DT_FP32, 0>)  \

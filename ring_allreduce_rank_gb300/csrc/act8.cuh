@@ -35,12 +35,12 @@ __device__ __forceinline__ float act8_inverse(uint32_t byte) { return __uint_as_
 // 2^e; infinity for a block of NaN, whose codes are 0.
 __device__ __forceinline__ float act8_step(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// A value's code in the low byte: 1.5 * 2^23 + q has q in its last bits.
-__device__ __forceinline__ uint32_t act8_code(float x, float inverse)
-{
-    const float q = __fmul_rn(x, inverse); // exact, or below half a step
-    return __float_as_uint(__fadd_rn(fminf(fmaxf(q, -127.0f), 127.0f), 12582912.0f));
-}
+// A value's code in the low byte: 1.5 * 2^23 + x / 2^e, rounded once, has the
+// nearest integer in its last bits.  Only a block at the largest step can hold
+// more than 127 of them.
+__device__ __forceinline__ uint32_t act8_code(float x, float inverse) { return __float_as_uint(__fmaf_rn(x, inverse, 12582912.0f)); }
+
+__device__ __forceinline__ float act8_clamp(float x) { return fminf(fmaxf(x, -0x1.fcp127f), 0x1.fcp127f); } // 127 * 2^121
 
 // Codes of 32 values, four a word, and the block's byte.
 __device__ __forceinline__ uint32_t act8_encode(const float *f, uint4 &lo, uint4 &hi)
@@ -58,9 +58,16 @@ __device__ __forceinline__ uint32_t act8_encode(const float *f, uint4 &lo, uint4
     } else {
         const float inverse = act8_inverse(byte);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            w[i] = __byte_perm(__byte_perm(act8_code(f[4 * i], inverse), act8_code(f[4 * i + 1], inverse), 0x0040),
-                               __byte_perm(act8_code(f[4 * i + 2], inverse), act8_code(f[4 * i + 3], inverse), 0x0040), 0x5410);
+        for (int i = 0; i < 8; ++i) {
+            float x[4] = {f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
+            if (byte == kActMost) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    x[k] = act8_clamp(x[k]);
+            }
+            w[i] = __byte_perm(__byte_perm(act8_code(x[0], inverse), act8_code(x[1], inverse), 0x0040),
+                               __byte_perm(act8_code(x[2], inverse), act8_code(x[3], inverse), 0x0040), 0x5410);
+        }
     }
     lo = make_uint4(w[0], w[1], w[2], w[3]);
     hi = make_uint4(w[4], w[5], w[6], w[7]);

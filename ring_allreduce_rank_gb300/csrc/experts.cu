@@ -41,13 +41,13 @@ namespace {
 constexpr int kTileM = 256, kTileN = 256, kTileK = 64; // a CTA pair's tile
 constexpr int kOperandBytes = 128 * kTileK * 2;        // one CTA's part of A or B in a stage
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kStages = 6, kTurnStages = 4; // the latter beside the room to turn values in
-constexpr int kThreads2 = 384; // producer, issuer, tensor memory, one idle warp, eight epilogue warps
-constexpr int kEpiWarps = 8;
-constexpr int kTurnFloats = 32 * 33; // an epilogue warp's 32 x 32 values, rows padded against bank conflicts
+constexpr int kStages = 6, kStagedStages = 5; // the latter beside the room that outputs are staged in
+constexpr int kEpiWarps = 8, kFewThreads = 128 + 32 * kEpiWarps; // expert_few_kernel's
+// Staging: 32 rows of 128 bf16 columns for each of the four groups of epilogue
+// warps.  The pitch puts eight rows' 16 bytes in different banks.
+constexpr uint32_t kPitch = 272, kStaging = 32 * kPitch;
 constexpr int kTableBytes = 3 * (CCL_MAX_EXPERTS + 2) * 4;
-constexpr int kGemmSmem = 1024 /* alignment */ + kTableBytes +
-                          std::max(kStages * kStageBytes, kTurnStages * kStageBytes + 16 * kTurnFloats * 4);
+constexpr int kGemmSmem = 1024 /* alignment */ + kTableBytes + std::max(kStages * kStageBytes, kStagedStages * kStageBytes + 4 * (int)kStaging);
 constexpr int kGroupM = 8; // row tiles walked before the next column tile
 constexpr uint32_t kPad = kTileK; // an expert's rows in the padded layout are a multiple of this
 constexpr int kFewStages = 6;
@@ -56,11 +56,13 @@ constexpr uint32_t kFewMost = 128;    // tokens of one tile
 
 enum Epilogue { EPI_GATED = 0, EPI_STORE = 1, EPI_BACKWARD = 2, EPI_WEIGHTS = 3 };
 
-// Epilogue warps of expert_gemm_kernel: two a scheduler for g and u, whose 64
-// values of a row take the registers, else four, which hide one another's
-// latencies.
-template <int EPI> constexpr int kEpilogueWarps = EPI == EPI_GATED ? kEpiWarps : 16;
-template <int EPI> constexpr int kGemmThreads = 128 + 32 * kEpilogueWarps<EPI>;
+// Epilogue warps of expert_gemm_kernel.  A lane has a row and writes 32 bytes of
+// it at a time; eight warps hide behind the products of a long K, which sixteen
+// slow down by 5 %.  Rows that no 16-byte vector divides are staged in shared
+// memory by sixteen, four of which share 32 rows, so that a warp writes along a
+// row (many experts' weight gradients of 530 x 1809: 459 -> 266 us; for whole
+// vectors the barriers cost more than full lines gain, 44 -> 60 us).
+constexpr int kDirect = 8, kStaged = 16;
 
 // C[M, N] = sum over segments of A_s[M, K] B_s[N, K]^T for each expert: M its
 // rows, or for EPI_WEIGHTS K its rows.
@@ -87,7 +89,6 @@ struct ExpertParams {
     uint32_t ldh;
     int padded;  // A's rows are those of the padded layout
     uint32_t half; // columns of B that a CTA of the pair brings: half a tile's
-    int vectors; // every output row is 16-byte aligned and whole vectors of 8 columns
     unsigned long long wait_ns;
     // expert_few_kernel
     float *partial; // [splits][rows][column tiles * 256]
@@ -275,66 +276,177 @@ template <bool MN> __device__ __forceinline__ void load_expert(uint32_t dst, con
 
 constexpr uint32_t kNanBits = 0x7fffffffu;
 
+// act(g) and act'(g) as activation() has them, in fewer instructions: the
+// epilogues of products over a short K are bound by these.  With a = g s,
+// SiLU' = s + a (1 - s), and GELU's (tanh form) the same times the inner
+// derivative of its second term.
+__device__ __forceinline__ void gate(int act, float g, float &a, float &da)
+{
+    constexpr float c2 = 1.5957691216057308f; // 2 sqrt(2/pi)
+    if (act == CCL_ACT_SILU) {
+        const float s = sigmoid(g);
+        a = __fmul_rn(g, s);
+        da = __fmaf_rn(a, __fadd_rn(1.0f, -s), s);
+    } else {
+        const float gg = __fmul_rn(g, g);
+        const float s = sigmoid(__fmul_rn(g, __fmaf_rn(0.044715f * c2, gg, c2)));
+        const float t = __fadd_rn(1.0f, -s), as = __fmul_rn(g, s);
+        a = as;
+        da = t == 0.0f ? s : __fmaf_rn(__fmul_rn(as, t), __fmaf_rn(3 * 0.044715f * c2, gg, c2), s);
+        da = s == 0.0f ? 0.0f : da; // where the polynomial has overflowed
+    }
+}
+
 __device__ __forceinline__ void store32(uint16_t *q, const float *f)
 {
     st32(q, pack<DT_BF16>(f), pack<DT_BF16>(f + 8));
     st32(q + 16, pack<DT_BF16>(f + 16), pack<DT_BF16>(f + 24));
 }
 
-// 32 columns of a row of g and u, a block each: h, and their 8 bits.  What
-// would lie past the last column is zero.
-__device__ __forceinline__ void finish_gated(const ExpertParams &p, uint64_t at, float *g, float *u)
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
-    if (p.codes[0]) {
-        uint4 lo, hi;
-        uint32_t b = act8_encode(g, lo, hi);
-        st32(p.codes[0] + at, lo, hi);
-        gstore<uint8_t>(p.scales[0] + at / kActBlock, (uint8_t)b);
-        b = act8_encode(u, lo, hi);
-        st32(p.codes[1] + at, lo, hi);
-        gstore<uint8_t>(p.scales[1] + at / kActBlock, (uint8_t)b);
-    }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        float a, da;
-        activation(p.act, g[i], a, da);
-        g[i] = __fmul_rn(a, u[i]);
-    }
-    store32(p.h + at, g);
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// What the backward epilogue reads of a block: the codes of g and u.
+__device__ __forceinline__ void shared_store16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ uint4 shared_load16(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t shared_load4(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// The barrier of the 128 threads that share 32 rows, and the same with the
+// question whether all say yes.
+__device__ __forceinline__ void rows_sync(uint32_t quarter) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + quarter) : "memory"); }
+
+__device__ __forceinline__ bool rows_all(uint32_t quarter, bool yes)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+                 "barrier.cta.red.and.pred p, %1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r)
+                 : "r"(1 + quarter), "r"((uint32_t)yes)
+                 : "memory");
+    return r != 0;
+}
+
+// 32 staged columns of a lane's row, packed in pairs.
+__device__ __forceinline__ void stage32(uint32_t at, const uint32_t *w)
+{
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+        shared_store16(at + 4 * i, w[i], w[i + 1], w[i + 2], w[i + 3]);
+}
+
+// Staged rows (at most 32, of `cols` <= 128 columns) to out, rows `ld` apart, by
+// 128 threads: as words, with single values at the ends.  A warp takes every
+// fourth row, all of the parity of its first.
+__device__ __forceinline__ void staged_out(uint32_t staging, uint16_t *out, uint64_t ld, uint32_t rows, uint32_t cols)
+{
+    const uint32_t lane = threadIdx.x & 31, r0 = threadIdx.x / 128 - 1;
+    if (r0 >= rows || cols == 0)
+        return;
+    uint16_t *dst = out + r0 * ld;
+    uint32_t src = staging + r0 * kPitch;
+    const uint32_t odd = ((uintptr_t)dst & 2) / 2, n = (rows - r0 + 3) / 4; // words begin at column `odd`
+    const bool first = 2 * lane + odd + 1 < cols, second = 2 * lane + 64 + odd + 1 < cols;
+    const bool edge = lane == 0 ? odd : lane == 1 ? cols > odd && (cols - odd) % 2 : false; // the columns that no word holds
+    const uint32_t at = lane == 0 ? 0 : cols - 1;
+    const uint32_t shift = odd * 16;
+#pragma unroll 2
+    for (uint32_t r = 0; r < n; ++r, dst += 4 * ld, src += 4 * kPitch) {
+        uint32_t a = shared_load4(src + 4 * lane), b = shared_load4(src + 4 * lane + 128);
+        if (odd) {
+            a = __funnelshift_r(a, shared_load4(src + 4 * lane + 4), shift);
+            b = __funnelshift_r(b, shared_load4(src + 4 * lane + 132), shift);
+        }
+        if (first)
+            gstore<uint32_t>(dst + 2 * lane + odd, a);
+        if (second)
+            gstore<uint32_t>(dst + 2 * lane + 64 + odd, b);
+        if (edge)
+            gstore<uint16_t>(dst + at, (uint16_t)(shared_load4(src + at / 2 * 4) >> at % 2 * 16));
+    }
+}
+
+// The other way: what the rows hold now.
+__device__ __forceinline__ void staged_in(uint32_t staging, const uint16_t *out, uint64_t ld, uint32_t rows, uint32_t cols)
+{
+    const uint32_t lane = threadIdx.x & 31;
+#pragma unroll 2
+    for (uint32_t r = threadIdx.x / 128 - 1; r < rows; r += 4)
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) {
+            const uint32_t c = lane + 32 * k;
+            const uint16_t v = c < cols ? gload<uint16_t>(out + r * ld + c) : (uint16_t)0;
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(staging + r * kPitch + 2 * c), "h"(v) : "memory");
+        }
+}
+
+// A block of g (k = 0) or u (k = 1) of a row in 8 bits.
+__device__ __forceinline__ void keep(const ExpertParams &p, int k, uint64_t at, const float *f)
+{
+    uint4 lo, hi;
+    const uint32_t b = act8_encode(f, lo, hi);
+    st32(p.codes[k] + at, lo, hi);
+    gstore<uint8_t>(p.scales[k] + at / kActBlock, (uint8_t)b);
+}
+
+// h of sixteen columns of a row.  What would lie past the last column is zero.
+__device__ __forceinline__ void finish_gated(const ExpertParams &p, uint64_t at, float *g, const float *u)
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float a, da;
+        gate(p.act, g[i], a, da);
+        g[i] = __fmul_rn(a, u[i]);
+    }
+    st32(p.h + at, pack<DT_BF16>(g), pack<DT_BF16>(g + 8));
+}
+
+// What the backward epilogue reads of a block: the codes of g and u, and steps.
 struct Saved {
     uint4 g[2], u[2];
-    uint8_t bg, bu;
+    float sg, su;
     __device__ __forceinline__ void load(const ExpertParams &p, uint64_t at, bool in)
     {
-        bg = bu = 0;
         if (!in)
             return;
         ld32(p.codes[0] + at, g[0], g[1]);
         ld32(p.codes[1] + at, u[0], u[1]);
-        bg = gload<uint8_t>(p.scales[0] + at / kActBlock);
-        bu = gload<uint8_t>(p.scales[1] + at / kActBlock);
+        sg = act8_step(gload<uint8_t>(p.scales[0] + at / kActBlock));
+        su = act8_step(gload<uint8_t>(p.scales[1] + at / kActBlock));
     }
 };
 
 // dh to dg, du and h, sixteen columns of a row: the first or second half of a block.
 __device__ __forceinline__ void finish_backward(const ExpertParams &p, uint64_t to, const Saved &s, uint32_t second, const float *v)
 {
-    const float sg = act8_step(s.bg), su = act8_step(s.bu);
     const uint4 cg = s.g[second], cu = s.u[second];
     const uint32_t wg[4] = {cg.x, cg.y, cg.z, cg.w}, wu[4] = {cu.x, cu.y, cu.z, cu.w};
     float h[16], dg[16], du[16];
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
         float g[4], u[4];
-        act8_decode4(wg[j / 4], sg, g);
-        act8_decode4(wu[j / 4], su, u);
+        act8_decode4(wg[j / 4], s.sg, g);
+        act8_decode4(wu[j / 4], s.su, u);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             float a, da;
-            activation(p.act, g[k], a, da);
+            gate(p.act, g[k], a, da);
             const float d = v[j + k];
             h[j + k] = __fmul_rn(a, u[k]);
             dg[j + k] = __fmul_rn(__fmul_rn(d, u[k]), da);
@@ -384,16 +496,16 @@ template <int EPI> __device__ __forceinline__ uint16_t *unit_out(const ExpertPar
 
 // ------------------------------------------------------------------ the product on CTA pairs
 
-template <int EPI, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(kGemmThreads<EPI>, 1) expert_gemm_kernel(const __grid_constant__ ExpertParams p)
+template <int EPI, bool A_MN, bool B_MN, int WARPS>
+__global__ void __launch_bounds__(128 + 32 * WARPS, 1) expert_gemm_kernel(const __grid_constant__ ExpertParams p)
 {
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t bars[2 * kStages + 4];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int gave_up;
     const uint32_t stages = (smem_u32(raw) + 1023) & ~1023u;
-    const uint32_t nstages = p.vectors ? kStages : kTurnStages;
-    uint8_t *behind = raw + (stages - smem_u32(raw)) + nstages * kStageBytes;
+    constexpr uint32_t nstages = WARPS == kStaged ? kStagedStages : kStages;
+    uint8_t *behind = raw + (stages - smem_u32(raw)) + nstages * kStageBytes + (WARPS == kStaged ? 4 * kStaging : 0);
     const Table table{reinterpret_cast<int32_t *>(behind), reinterpret_cast<int32_t *>(behind) + CCL_MAX_EXPERTS + 2,
                       reinterpret_cast<int32_t *>(behind) + 2 * (CCL_MAX_EXPERTS + 2)};
     const uint32_t full = smem_u32(&bars[0]), empty = smem_u32(&bars[kStages]);
@@ -409,7 +521,7 @@ __global__ void __launch_bounds__(kGemmThreads<EPI>, 1) expert_gemm_kernel(const
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
-            mbar_init(acc_empty + 8 * i, 2 * kEpilogueWarps<EPI>);
+            mbar_init(acc_empty + 8 * i, 2 * WARPS);
         }
         if ((gave_up = p.wait_ns == 0))
             atomicAdd(&g_expert_timeouts, 1ull);
@@ -518,12 +630,13 @@ __global__ void __launch_bounds__(kGemmThreads<EPI>, 1) expert_gemm_kernel(const
             ++t;
         }
     } else if (warp >= 4) {
-        // epilogue: warp w reads lanes 32 (w % 4) .. + 32 and every kStride-th 32 columns
-        constexpr uint32_t kStride = 32 * kEpilogueWarps<EPI> / 4;
-        const uint32_t c0 = (warp - 4) / 4 * 32;
-        const uint32_t lanes = (uint32_t)(warp & 3) * 32;
+        // epilogue: warp w reads lanes 32 (w % 4) .. + 32 and every kStride-th 32
+        // columns; the four warps that read the same lanes stage and write together
+        constexpr uint32_t kStride = 32 * WARPS / 4;
+        const uint32_t c0 = (warp - 4) / 4 * 32, quarter = warp & 3;
+        const uint32_t lanes = quarter * 32;
         const uint32_t leader_empty = in_cta(acc_empty, 0);
-        float *turn = reinterpret_cast<float *>(behind + kTableBytes) + (warp - 4) * kTurnFloats;
+        const uint32_t staging = stages + nstages * kStageBytes + quarter * kStaging;
         uint32_t t = 0, i = pair;
         for (; p.wait_ns && i < total; i += pairs) {
             const Unit u = unit_at<EPI>(p, table, i);
@@ -537,102 +650,135 @@ __global__ void __launch_bounds__(kGemmThreads<EPI>, 1) expert_gemm_kernel(const
             Saved ahead;
             if (EPI == EPI_BACKWARD)
                 ahead.load(p, (uint64_t)(u.row0 + in) * p.ldh + col0 + c0, in < u.rows && c0 < cols);
-            if (some) {
-                if (!__all_sync(0xffffffffu, mbar_wait(acc_full + 8 * buf, (t >> 1) & 1, &gave_up, p.wait_ns)))
-                    break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            }
+            bool ok = true;
+            if (some)
+                ok = __all_sync(0xffffffffu, mbar_wait(acc_full + 8 * buf, (t >> 1) & 1, &gave_up, p.wait_ns));
+            if (WARPS == kStaged)
+                ok = rows_all(quarter, ok); // none stays behind in a barrier; what was staged before is written
+            if (!ok)
+                break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tmem + buf * kTileN + (lanes << 16);
-            if (EPI == EPI_GATED) {
-                for (uint32_t c = c0; c < cols; c += kStride) {
-                    float g[32], v[32];
-                    tc_load32(acc + c, g);
-                    tc_load32(acc + u.half + c, v);
-                    if (in < u.rows)
-                        finish_gated(p, (uint64_t)(u.row0 + in) * p.ldh + col0 + c, g, v);
-                }
-            } else if (EPI == EPI_BACKWARD) {
-                for (uint32_t c = c0; c < cols; c += kStride) {
-                    Saved next;
-                    next.load(p, (uint64_t)(u.row0 + in) * p.ldh + col0 + c + kStride, in < u.rows && c + kStride < cols);
-                    const uint64_t to = (uint64_t)(u.pad0 + in) * p.ldh + col0 + c;
-#pragma unroll
-                    for (uint32_t h = 0; h < 2; ++h) {
-                        float v[16];
-                        tc_load16(acc + c + 16 * h, v);
-                        if (in < u.rows)
-                            finish_backward(p, to + 16 * h, ahead, h, v);
-                        else if (in < (u.rows + kPad - 1) / kPad * kPad)
-                            backward_zeros(p, to + 16 * h);
-                    }
-                    ahead = next;
-                }
-            } else {
-                uint32_t rows;
-                uint16_t *out = unit_out<EPI>(p, u, rows);
-                if (p.vectors) {
-                    // a lane keeps its row, sixteen columns at a time
-                    uint16_t *at = out + (uint64_t)in * q.n + col0;
-                    const uint32_t n = in < rows ? q.n - col0 : 0; // columns of this row from the tile's first on
-                    for (uint32_t c = c0; c < cols; c += kStride) {
-                        Vals16 old[2];
-#pragma unroll
-                        for (uint32_t h = 0; h < 2; ++h)
-                            if (p.accumulate && c + 16 * h < n)
-                                old[h].load(at + c + 16 * h, c + 16 * h + 8 < n);
-                        float v[32];
-                        if (some) {
-                            tc_load32(acc + c, v);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                v[j] = 0.0f;
-                        }
-#pragma unroll
-                        for (uint32_t h = 0; h < 2; ++h)
-                            if (c + 16 * h < n)
-                                finish_store(p, at + c + 16 * h, c + 16 * h + 8 < n, old[h], v + 16 * h);
-                    }
-                } else {
-                    // turned in shared memory, so that a warp's accesses run along a row
-                    for (uint32_t c = c0; c < cols; c += kStride) {
-                        float v[32];
-                        if (some) {
-                            tc_load32(acc + c, v);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                v[j] = 0.0f;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            turn[lane * 33 + j] = v[j];
-                        __syncwarp();
-                        const uint32_t col = col0 + c + lane;
-                        const uint32_t n = col >= q.n || in0 >= rows ? 0 : min(rows - in0, 32u);
-                        uint16_t *at = out + (uint64_t)in0 * q.n + col;
-                        for (uint32_t r0 = 0; r0 < 32; r0 += 8) { // eight rows' reads in flight
-                            float old[8];
-#pragma unroll
-                            for (uint32_t r = 0; r < 8; ++r)
-                                old[r] = p.accumulate && r0 + r < n ? ld_value<DT_BF16>(at, (uint64_t)(r0 + r) * q.n) : 0.0f;
-#pragma unroll
-                            for (uint32_t r = 0; r < 8; ++r)
-                                if (r0 + r < n) {
-                                    const float x = turn[(r0 + r) * 33 + lane];
-                                    st_value<DT_BF16>(at, (uint64_t)(r0 + r) * q.n, p.accumulate ? __fadd_rn(old[r], x) : x);
-                                }
-                        }
-                        __syncwarp();
-                    }
-                }
-            }
-            if (some) {
+            auto release = [&] { // the accumulator has been read
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive_cluster(leader_empty + 8 * buf);
                 ++t;
+            };
+            if (EPI == EPI_GATED) {
+                for (uint32_t c = c0; c < cols && in0 < u.rows; c += kStride) {
+                    const uint64_t at = (uint64_t)(u.row0 + in) * p.ldh + col0 + c;
+                    if (p.codes[0]) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float f[32];
+                            tc_load32(acc + k * u.half + c, f);
+                            if (in < u.rows)
+                                keep(p, k, at, f);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) { // read again: few registers, many warps
+                        float g[16], v[16];
+                        tc_load16(acc + c + 16 * k, g);
+                        tc_load16(acc + u.half + c + 16 * k, v);
+                        if (in < u.rows)
+                            finish_gated(p, at + 16 * k, g, v);
+                    }
+                }
+                release();
+            } else if (EPI == EPI_BACKWARD) {
+                const bool behind = in < (u.rows + kPad - 1) / kPad * kPad; // the padding's zeros
+                for (uint32_t c = c0; c < cols && __any_sync(0xffffffffu, behind); c += kStride) {
+                    Saved next;
+                    next.load(p, (uint64_t)(u.row0 + in) * p.ldh + col0 + c + kStride, in < u.rows && c + kStride < cols);
+                    const uint64_t to = (uint64_t)(u.pad0 + in) * p.ldh + col0 + c;
+#pragma unroll
+                    for (uint32_t k = 0; k < 2; ++k) {
+                        float v[16];
+                        tc_load16(acc + c + 16 * k, v);
+                        if (in < u.rows)
+                            finish_backward(p, to + 16 * k, ahead, k, v);
+                        else if (behind)
+                            backward_zeros(p, to + 16 * k);
+                    }
+                    ahead = next;
+                }
+                release();
+            } else if (WARPS == kDirect) {
+                // a lane keeps its row, sixteen columns at a time of one half of
+                // the tile, what it adds to asked for one step ahead
+                uint32_t rows;
+                const uint32_t c1 = (warp - 4) / 4 * u.half;
+                uint16_t *at = unit_out<EPI>(p, u, rows) + (uint64_t)in * q.n + col0 + c1;
+                const uint32_t n = in < rows && col0 + c1 < q.n ? q.n - col0 - c1 : 0; // columns of this row from there on
+                Vals16 old;
+                if (p.accumulate && n)
+                    old.load(at, 8 < n);
+#pragma unroll 2
+                for (uint32_t c = 0; c < u.half && in0 < rows; c += 16) {
+                    float v[16];
+                    if (some) {
+                        tc_load16(acc + c1 + c, v);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            v[j] = 0.0f;
+                    }
+                    Vals16 next;
+                    if (p.accumulate && c + 16 < u.half && c + 16 < n)
+                        next.load(at + c + 16, c + 24 < n);
+                    if (c < n)
+                        finish_store(p, at + c, c + 8 < n, old, v);
+                    old = next;
+                }
+                if (some)
+                    release();
+            } else {
+                uint32_t rows;
+                uint16_t *out = unit_out<EPI>(p, u, rows) + (uint64_t)in0 * q.n + col0;
+                rows = rows > in0 ? min(rows - in0, 32u) : 0;
+                const uint32_t left = min(cols, q.n - col0);
+                for (uint32_t c = 0; c < cols && rows; c += kStride) {
+                    const bool mine = c + c0 < cols;
+                    const uint32_t wide = left > c ? min(left - c, 128u) : 0;
+                    uint32_t w[16];
+                    if (p.accumulate) {
+                        staged_in(staging, out + c, q.n, rows, wide);
+                        rows_sync(quarter);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint4 x = shared_load16(staging + lane * kPitch + 2 * c0 + 16 * k);
+                            w[4 * k] = x.x;
+                            w[4 * k + 1] = x.y;
+                            w[4 * k + 2] = x.z;
+                            w[4 * k + 3] = x.w;
+                        }
+                        rows_sync(quarter);
+                    }
+                    if (mine) {
+                        float v[32];
+                        if (some) {
+                            tc_load32(acc + c + c0, v);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = 0.0f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            w[j] = p.accumulate ? pack2(__fadd_rn(__uint_as_float(w[j] << 16), v[2 * j]),
+                                                        __fadd_rn(__uint_as_float(w[j] & 0xffff0000u), v[2 * j + 1]))
+                                                : pack2(v[2 * j], v[2 * j + 1]);
+                        stage32(staging + lane * kPitch + 2 * c0, w);
+                    }
+                    rows_sync(quarter);
+                    staged_out(staging, out + c, q.n, rows, wide);
+                    rows_sync(quarter);
+                }
+                if (some)
+                    release();
             }
         }
         // after a wait that gave up: NaN in everything that could not be computed
@@ -644,13 +790,17 @@ __global__ void __launch_bounds__(kGemmThreads<EPI>, 1) expert_gemm_kernel(const
             const uint32_t cols = EPI == EPI_GATED ? u.half : 2 * u.half, col0 = u.n * (EPI == EPI_GATED ? 1 : 2) * p.half;
             const bool none = EPI == EPI_WEIGHTS && u.kblocks == 0; // no sum to give up
             for (uint32_t c = c0; c < cols; c += kStride) {
-                float v[32], w[32];
+                float v[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                    v[j] = w[j] = nan;
+                    v[j] = nan;
                 if (EPI == EPI_GATED) {
-                    if (in < u.rows)
-                        finish_gated(p, (uint64_t)(u.row0 + in) * p.ldh + col0 + c, v, w);
+                    const uint64_t at = (uint64_t)(u.row0 + in) * p.ldh + col0 + c;
+                    if (in < u.rows) {
+                        store32(p.h + at, v);
+                        for (int k = 0; k < 2 && p.codes[0]; ++k)
+                            keep(p, k, at, v);
+                    }
                 } else if (EPI == EPI_BACKWARD) {
                     const uint64_t to = (uint64_t)(u.pad0 + in) * p.ldh + col0 + c;
                     if (in < u.rows) {
@@ -697,14 +847,14 @@ template <int EPI> __device__ __forceinline__ void finish_lane(const ExpertParam
             for (int k = 0; k < 2; ++k) {
                 const uint32_t b = act8_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(x[k]) & 0x7fffffffu));
                 if (in) {
-                    gstore<int8_t>(p.codes[k] + at, b == kActNan ? (int8_t)0 : (int8_t)(act8_code(x[k], act8_inverse(b)) & 0xff));
+                    gstore<int8_t>(p.codes[k] + at, b == kActNan ? (int8_t)0 : (int8_t)(act8_code(act8_clamp(x[k]), act8_inverse(b)) & 0xff));
                     if (col % kActBlock == 0)
                         gstore<uint8_t>(p.scales[k] + at / kActBlock, (uint8_t)b);
                 }
             }
         }
         float a, da;
-        activation(p.act, v, a, da);
+        gate(p.act, v, a, da);
         if (in)
             st_value<DT_BF16>(p.h, at, __fmul_rn(a, w));
     } else if (in) {
@@ -733,7 +883,7 @@ template <int EPI> __device__ __forceinline__ Unit few_unit_at(const ExpertParam
     return u;
 }
 
-template <int EPI> __global__ void __launch_bounds__(kThreads2, 1) expert_few_kernel(const __grid_constant__ ExpertParams p)
+template <int EPI> __global__ void __launch_bounds__(kFewThreads, 1) expert_few_kernel(const __grid_constant__ ExpertParams p)
 {
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t bars[2 * kFewStages + 4];
@@ -1207,17 +1357,24 @@ cudaLaunchConfig_t pair_launch(cudaLaunchAttribute *attr, unsigned pairs, unsign
 }
 
 // units: the most that the launch can have.
-template <int EPI, bool A_MN, bool B_MN> cudaError_t launch_gemm(const ExpertParams &p, uint64_t units, cudaStream_t stream)
+template <int EPI, bool A_MN, bool B_MN, int WARPS = kDirect> cudaError_t launch_gemm(const ExpertParams &p, uint64_t units, cudaStream_t stream)
 {
     static std::atomic<unsigned long long> ready{0};
-    cudaError_t e = large_smem_once(reinterpret_cast<const void *>(expert_gemm_kernel<EPI, A_MN, B_MN>), kGemmSmem, ready);
+    cudaError_t e = large_smem_once(reinterpret_cast<const void *>(expert_gemm_kernel<EPI, A_MN, B_MN, WARPS>), kGemmSmem, ready);
     if (e != cudaSuccess)
         return e;
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = pair_launch(attr, (unsigned)std::max<uint64_t>(1, std::min<uint64_t>(units, kPairs)), kGemmThreads<EPI>, stream);
-    if ((e = cudaLaunchKernelEx(&cfg, expert_gemm_kernel<EPI, A_MN, B_MN>, p)) == cudaSuccess)
+    const cudaLaunchConfig_t cfg = pair_launch(attr, (unsigned)std::max<uint64_t>(1, std::min<uint64_t>(units, kPairs)), 128 + 32 * WARPS, stream);
+    if ((e = cudaLaunchKernelEx(&cfg, expert_gemm_kernel<EPI, A_MN, B_MN, WARPS>, p)) == cudaSuccess)
         count_launches(1);
     return e;
+}
+
+// Outputs whose every row is 16-byte aligned and whole vectors of 8 columns are
+// written directly.
+template <int EPI, bool A_MN, bool B_MN> cudaError_t launch_out(const ExpertParams &p, bool vectors, uint64_t units, cudaStream_t stream)
+{
+    return vectors ? launch_gemm<EPI, A_MN, B_MN, kDirect>(p, units, stream) : launch_gemm<EPI, A_MN, B_MN, kStaged>(p, units, stream);
 }
 
 template <int EPI> cudaError_t launch_few(ExpertParams &p, uint64_t tiles, cudaStream_t stream)
@@ -1231,7 +1388,7 @@ template <int EPI> cudaError_t launch_few(ExpertParams &p, uint64_t tiles, cudaS
     const uint64_t units = tiles * p.prob[0].nt * p.splits;
     if (units > 0x3fffffff)
         return cudaErrorInvalidValue;
-    if ((e = launch_chained(expert_few_kernel<EPI>, dim3((unsigned)std::min<uint64_t>(units, kSms)), dim3(kThreads2), smem, stream, p)) != cudaSuccess)
+    if ((e = launch_chained(expert_few_kernel<EPI>, dim3((unsigned)std::min<uint64_t>(units, kSms)), dim3(kFewThreads), smem, stream, p)) != cudaSuccess)
         return e;
     count_launches(1);
     if (p.splits > 1) {
@@ -1317,11 +1474,25 @@ ExpertParams params_of(const ExpertArgs &a, const ExpertPlan &pl)
     return p;
 }
 
-// Columns of a pair's tile: 256, whose products reuse what they read most, or
-// fewer where that leaves pairs without a tile (units of 256 columns: `wide`).
-uint32_t half_tile(uint64_t wide)
+// Half the columns of a pair's tile: 128, whose products reuse what they read
+// most, or fewer where that shortens the rounds of tiles (row tiles x columns).
+// A block of K takes a pair about 0.35 us, and little less at half and quarter
+// width; an epilogue, which runs beside the next tile's products, `epilogue` us
+// at full width.
+uint32_t half_tile(uint64_t row_tiles, uint64_t columns, uint64_t kblocks, double epilogue)
 {
-    return wide * 2 <= kPairs ? 32 : wide <= kPairs ? 64 : 128;
+    uint32_t best = 128;
+    double cost = 0;
+    for (uint32_t half = 128; half >= 32; half /= 2) {
+        const double rounds = (double)((row_tiles * ((columns + 2 * half - 1) / (2 * half)) + kPairs - 1) / kPairs);
+        const double products = (double)kblocks * (half == 128 ? 0.35 : half == 64 ? 0.33 : 0.31), after = 0.7 + epilogue * half / 128;
+        const double c = rounds * std::max(products, after) + std::min(products, after);
+        if (half == 128 || c < cost * 0.95) {
+            best = half;
+            cost = c;
+        }
+    }
+    return best;
 }
 
 void set_problem(Problem &q, uint64_t n, uint32_t tile, uint64_t k, uint32_t segs)
@@ -1378,20 +1549,20 @@ ccl_status_t expert_ffn_impl(const ExpertArgs &a, void *out, cudaStream_t stream
         return from_cuda(launch_few<EPI_STORE>(p, tiles, stream));
     }
     const uint64_t tiles = a.r / kTileM + active; // at most
-    p.half = half_tile(tiles * tiles_of(a.f, 128));
+    const uint64_t likely = std::max(active, a.r / kTileM + active / 2);
+    p.half = half_tile(likely, 2 * a.f, tiles_of(a.d, kTileK), a.codes ? 5.0 : 3.5);
     set_problem(q, a.f, p.half, a.d, 1);
-    p.vectors = 1;
     if (!encode_rows(&q.a[0], x, false) || !encode_experts(&q.b[0], w2[0], a.e, false) || !encode_experts(&q.b[1], w2[1], a.e, false))
         return CCL_ERR_CUDA;
     if (cudaError_t e = launch_gemm<EPI_GATED, false, false>(p, tiles * q.nt, stream))
         return from_cuda(e);
-    p.half = half_tile(tiles * tiles_of(a.d, kTileN));
+    const bool vectors = a.d % 8 == 0 && (uintptr_t)out % 16 == 0;
+    p.half = half_tile(likely, a.d, tiles_of(a.f, kTileK), vectors ? 2.5 : 4.0);
     set_problem(q, a.d, 2 * p.half, a.f, 1);
     q.out = out;
-    p.vectors = a.d % 8 == 0 && (uintptr_t)out % 16 == 0;
     if (!encode_rows(&q.a[0], h, false) || !encode_experts(&q.b[0], wd, a.e, false))
         return CCL_ERR_CUDA;
-    return from_cuda(launch_gemm<EPI_STORE, false, false>(p, tiles * q.nt, stream));
+    return from_cuda(launch_out<EPI_STORE, false, false>(p, vectors, tiles * q.nt, stream));
 }
 
 ccl_status_t expert_ffn_grad_impl(const ExpertArgs &a, const void *dy, void *dx, void *dwg, void *dwu, void *dwd, int accumulate, cudaStream_t stream)
@@ -1470,11 +1641,11 @@ ccl_status_t expert_ffn_grad_impl(const ExpertArgs &a, const void *dy, void *dx,
     if ((e = launch_chained(expert_pad_kernel, dim3((unsigned)std::min<uint64_t>(most, 8 * kSms), pad.nrows + (unsigned)pad.weights.n), dim3(256), 0, stream, pad)))
         return from_cuda(e);
     count_launches(1);
-    const uint64_t tiles = a.r / kTileM + std::min<uint64_t>(a.r, a.e); // at most
+    const uint64_t active = std::min<uint64_t>(a.r, a.e), tiles = a.r / kTileM + active; // at most
+    const uint64_t likely = std::max(active, a.r / kTileM + active / 2);
     Problem &q = p.prob[0];
-    p.half = half_tile(tiles * tiles_of(a.f, kTileN));
+    p.half = half_tile(likely, a.f, tiles_of(a.d, kTileK), 7.0);
     set_problem(q, a.f, 2 * p.half, a.d, 1);
-    p.vectors = 1;
     p.padded = !direct_y;
     if (!encode_rows(&q.a[0], direct_y ? ly : y, false) || !encode_experts(&q.b[0], wd, a.e, true))
         return CCL_ERR_CUDA;
@@ -1482,24 +1653,27 @@ ccl_status_t expert_ffn_grad_impl(const ExpertArgs &a, const void *dy, void *dx,
         return from_cuda(e);
     p.padded = 1;
     if (dx) {
-        p.half = half_tile(tiles * tiles_of(a.d, kTileN));
+        const bool vectors = a.d % 8 == 0 && (uintptr_t)dx % 16 == 0;
+        p.half = half_tile(likely, a.d, 2 * tiles_of(a.f, kTileK), vectors ? 2.5 : 4.0);
         set_problem(q, a.d, 2 * p.half, a.f, 2);
         q.out = dx;
-        p.vectors = a.d % 8 == 0 && (uintptr_t)dx % 16 == 0;
         for (int i = 0; i < 2; ++i)
             if (!encode_rows(&q.a[i], d2[i], false) || !encode_experts(&q.b[i], w2[i], a.e, true))
                 return CCL_ERR_CUDA;
-        if ((e = launch_gemm<EPI_STORE, false, true>(p, tiles * q.nt, stream)))
+        if ((e = launch_out<EPI_STORE, false, true>(p, vectors, tiles * q.nt, stream)))
             return from_cuda(e);
     }
     if (!need_x && !dwd)
         return CCL_OK;
     // the weight gradients asked for, in one launch
     p.accumulate = accumulate != 0;
-    p.vectors = a.d % 8 == 0 && a.f % 8 == 0;
+    bool vectors = a.d % 8 == 0 && a.f % 8 == 0;
     p.nprob = 0;
     uint64_t units = 0;
-    p.half = half_tile(a.e * ((dwg != nullptr) + (dwu != nullptr) + (dwd != nullptr)) * tiles_of(a.f, kTileM) * tiles_of(a.d, kTileN));
+    for (void *g : {dwg, dwu, dwd})
+        vectors = vectors && (uintptr_t)g % 16 == 0;
+    p.half = half_tile(a.e * ((dwg != nullptr) + (dwu != nullptr) + (dwd != nullptr)) * tiles_of(a.f, kTileM), a.d,
+                       tiles_of(a.r / active, kTileK), vectors ? 2.5 : 4.0);
     const Matrix *am[3] = {&d2[0], &d2[1], &y}, *bm[3] = {&x, &x, &h};
     void *out[3] = {dwg, dwu, dwd};
     for (int i = 0; i < 3; ++i)
@@ -1509,7 +1683,6 @@ ccl_status_t expert_ffn_grad_impl(const ExpertArgs &a, const void *dy, void *dx,
             o.mt = tiles_of(o.m, kTileM);
             set_problem(o, bm[i]->cols, 2 * p.half, 0, 1);
             o.out = out[i];
-            p.vectors = p.vectors && (uintptr_t)out[i] % 16 == 0;
             o.direct_a = i == 2 && direct_y;
             o.direct_b = i < 2 && direct_x;
             if (!encode_rows(&o.a[0], *am[i], true) || !encode_rows(&o.b[0], *bm[i], true) || (o.direct_a && !encode_rows(&o.a[1], ly, true)) ||
@@ -1517,7 +1690,7 @@ ccl_status_t expert_ffn_grad_impl(const ExpertArgs &a, const void *dy, void *dx,
                 return CCL_ERR_CUDA;
             units += (uint64_t)o.mt * o.nt * a.e;
         }
-    return from_cuda(launch_gemm<EPI_WEIGHTS, true, true>(p, units, stream));
+    return from_cuda(launch_out<EPI_WEIGHTS, true, true>(p, vectors, units, stream));
 }
 
 } // namespace
