@@ -592,7 +592,7 @@ ccl_status_t ccl_route_grad(const void *logits, size_t ntokens, size_t experts, 
  * first_expert + e has rows [offsets[e], offsets[e + 1]), offsets[0] = 0.  An id outside [first_expert, first_expert + experts)
  * (-1, or an expert of another rank) has place -1.  work:
  * ccl_plan_expert_order_work_bytes bytes, 256-byte aligned, not shared with a
- * concurrent call (0 bytes up to 4096 choices).  One launch, or three. */
+ * concurrent call (0 bytes up to 16384 choices).  One launch, or three. */
 ccl_status_t ccl_expert_order(const int32_t *ids, size_t ntokens, size_t top, int32_t first_expert, size_t experts,
                               int32_t *offsets, int32_t *place, void *work, size_t work_bytes, cudaStream_t stream);
 ccl_status_t ccl_plan_expert_order_work_bytes(size_t ntokens, size_t top, size_t experts, size_t *bytes);

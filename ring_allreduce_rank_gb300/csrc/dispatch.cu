@@ -3,10 +3,12 @@
 // of the experts' rows, and its gradients.
 //
 // Order: a stable counting sort of the ntokens * top choices by expert.  Up to
-// 4096 of them one CTA counts, scans and places, each warp a run of its own;
-// more take three chained launches: the runs' counts, one scan per expert over
-// the runs, the places (a choice's rank within its run comes from match.any of
-// a warp's 32, so that no atomic decides an order).
+// 4096 of them one CTA counts, scans and places, each warp a run of its own, up
+// to 16384 a cluster of eight does, in half the host's time of the three chained
+// launches that more take (6 us against 11, which is what a call of that size
+// costs; on the device 32768 take the cluster 10.3 us and the three 8.4): the
+// runs' counts, one scan per expert over the runs, the places.  A choice's rank within its run comes from match.any of a
+// warp's 32, so that no atomic decides an order.
 //
 // Dispatch: rows[place[t][s]] = x[t]: every token's row is read once and
 // written top times.  Combine: out[t] = sum over s of w[t][s] rows[place[t][s]],
@@ -15,17 +17,22 @@
 // token's rows.  All three are bound by memory bandwidth; a group of threads
 // takes a token, each 32-byte vector (16 where a row is no multiple of it) of
 // its rows with every row's load in flight before the first sum.
+#include <cooperative_groups.h>
+
 #include <vector>
 
 #include "../../include/ccl.h"
 #include "ccl_internal.h"
 #include "step_ops.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace ccl {
 namespace {
 
 constexpr size_t kMaxChoices = 0x7fffffff, kMaxDim = (size_t)1 << 24;
-constexpr uint32_t kFewChoices = 4096;
+constexpr uint32_t kFewChoices = 4096, kClusterChoices = 16384;
+constexpr int kOrderCtas = 8; // one portable cluster
 constexpr int kOrderThreads = 256, kOrderWarps = kOrderThreads / 32;
 constexpr uint32_t kFewCounters = 10240; // one CTA's counters, warps x experts
 
@@ -76,29 +83,75 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t v, uint32_t lane, uint32_
     return s - v;
 }
 
-// Everything in one CTA: counters[warp][expert] in shared memory.
-__global__ void __launch_bounds__(1024) order_few_kernel(const __grid_constant__ OrderParams p)
+// Everything in one launch, by one CTA or a cluster of them: counters[warp][expert]
+// in shared memory, a warp a run, and the CTAs' counts from one another's.
+template <int CTAS> __global__ void __launch_bounds__(1024) order_few_kernel(const __grid_constant__ OrderParams p)
 {
     chain_entry();
-    __shared__ int32_t counters[kFewCounters];
+    __shared__ int32_t counters[kFewCounters], mine[CCL_MAX_EXPERTS];
     __shared__ uint32_t sums[32];
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, rank = blockIdx.x;
     for (uint32_t i = threadIdx.x; i < warps * p.experts; i += blockDim.x)
         counters[i] = 0;
     __syncthreads();
-    const uint32_t i0 = min(warp * p.run, p.n), i1 = min(i0 + p.run, p.n);
-    int32_t *mine = counters + warp * p.experts;
-    for (uint32_t i = i0; i < i1; i += 32)
-        count32(mine, expert_of(p, i + lane, i1), p.experts, lane);
+    const uint32_t i0 = min((rank * warps + warp) * p.run, p.n), i1 = min(i0 + p.run, p.n);
+    int32_t *own = counters + warp * p.experts;
+    // the run's experts, eight loads in flight; the first 256 choices' stay for the places
+    constexpr uint32_t kHeld = 8;
+    uint32_t held[kHeld], more[kHeld];
+    auto fetch = [&](uint32_t *e, uint32_t i) {
+#pragma unroll
+        for (uint32_t j = 0; j < kHeld; ++j)
+            e[j] = expert_of(p, i + 32 * j + lane, i1);
+    };
+    auto count = [&](const uint32_t *e, uint32_t i, bool place) {
+#pragma unroll
+        for (uint32_t j = 0; j < kHeld; ++j)
+            if (i + 32 * j < i1) {
+                const uint32_t at = count32(own, e[j], p.experts, lane);
+                if (place && i + 32 * j + lane < i1)
+                    gstore<int32_t>(p.place + i + 32 * j + lane, e[j] < p.experts ? (int32_t)at : -1);
+            }
+    };
+    fetch(held, i0);
+    count(held, i0, false);
+    for (uint32_t i = i0 + 32 * kHeld; i < i1; i += 32 * kHeld) {
+        fetch(more, i);
+        count(more, i, false);
+    }
     __syncthreads();
-    // experts in order, within one the warps: a thread takes the counters of one expert at a time
+    if (CTAS > 1) {
+        for (uint32_t e = threadIdx.x; e < p.experts; e += blockDim.x) {
+            int32_t n = 0;
+#pragma unroll 8
+            for (uint32_t w = 0; w < warps; ++w)
+                n += counters[w * p.experts + e];
+            mine[e] = n;
+        }
+        cg::this_cluster().sync();
+    }
+    // experts in order, within one the CTAs, within those the warps: a thread takes an expert
     uint32_t before = 0;
     for (uint32_t e0 = 0; e0 < p.experts; e0 += blockDim.x) {
         const uint32_t e = e0 + threadIdx.x;
-        uint32_t n = 0, all;
-        if (e < p.experts)
-            for (uint32_t w = 0; w < warps; ++w)
-                n += (uint32_t)counters[w * p.experts + e];
+        uint32_t n = 0, lower = 0, all;
+        if (e < p.experts) {
+            if (CTAS > 1) {
+                uint32_t c[CTAS];
+#pragma unroll
+                for (int k = 0; k < CTAS; ++k)
+                    c[k] = (uint32_t)cg::this_cluster().map_shared_rank(mine, k)[e];
+#pragma unroll
+                for (int k = 0; k < CTAS; ++k) {
+                    n += c[k];
+                    lower += (uint32_t)k < rank ? c[k] : 0;
+                }
+            } else {
+#pragma unroll 8
+                for (uint32_t w = 0; w < warps; ++w)
+                    n += (uint32_t)counters[w * p.experts + e];
+            }
+        }
         uint32_t at = warp_scan(n, lane, all);
         if (lane == 31)
             sums[warp] = all;
@@ -110,29 +163,42 @@ __global__ void __launch_bounds__(1024) order_few_kernel(const __grid_constant__
         }
         __syncthreads();
         at += before + sums[warp];
+        const uint32_t past = at + n;
         if (e < p.experts) {
-            gstore<int32_t>(p.offsets + e, (int32_t)at);
-            if (e + 1 == p.experts)
-                gstore<int32_t>(p.offsets + p.experts, (int32_t)(at + n));
-            for (uint32_t w = 0; w < warps; ++w) {
-                const uint32_t c = (uint32_t)counters[w * p.experts + e];
-                counters[w * p.experts + e] = (int32_t)at;
-                at += c;
+            if (rank == 0) {
+                gstore<int32_t>(p.offsets + e, (int32_t)at);
+                if (e + 1 == p.experts)
+                    gstore<int32_t>(p.offsets + p.experts, (int32_t)past);
+            }
+            at += lower;
+            for (uint32_t w0 = 0; w0 < warps; w0 += 8) {
+                uint32_t c[8];
+#pragma unroll
+                for (uint32_t w = 0; w < 8; ++w)
+                    c[w] = w0 + w < warps ? (uint32_t)counters[(w0 + w) * p.experts + e] : 0;
+#pragma unroll
+                for (uint32_t w = 0; w < 8; ++w) {
+                    if (w0 + w < warps)
+                        counters[(w0 + w) * p.experts + e] = (int32_t)at;
+                    at += c[w];
+                }
             }
         }
         __syncthreads();
-        if (e0 + blockDim.x < p.experts) { // at most 1024 experts and warps x experts counters: a rare second round
-            if (e == e0 + blockDim.x - 1)
-                sums[0] = at;
+        if (e0 + blockDim.x < p.experts) { // fewer threads than experts: a rare second round
+            if (threadIdx.x == blockDim.x - 1)
+                sums[0] = past;
             __syncthreads();
             before = sums[0];
             __syncthreads();
         }
     }
-    for (uint32_t i = i0; i < i1; i += 32) {
-        const uint32_t e = expert_of(p, i + lane, i1), at = count32(mine, e, p.experts, lane);
-        if (i + lane < i1)
-            gstore<int32_t>(p.place + i + lane, e < p.experts ? (int32_t)at : -1);
+    if (CTAS > 1)
+        cg::this_cluster().sync(); // the counts have been read before any of the CTAs goes
+    count(held, i0, true);
+    for (uint32_t i = i0 + 32 * kHeld; i < i1; i += 32 * kHeld) {
+        fetch(more, i);
+        count(more, i, true);
     }
 }
 
@@ -317,46 +383,65 @@ template <int DT, int W> __global__ void __launch_bounds__(128) dispatch_kernel(
 
 constexpr int kSlots = 4; // rows of a token whose loads are in flight together
 
+// kSlots of a token's rows and weights.
+struct Slots {
+    uint32_t row[kSlots];
+    float w[kSlots];
+    __device__ __forceinline__ void load(const RowsParams &p, uint64_t t, uint32_t s0)
+    {
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s) {
+            row[s] = s0 + s < p.top ? (uint32_t)gload<int32_t>(p.place + t * p.top + s0 + s) : 0xffffffffu;
+            w[s] = p.weights && s0 + s < p.top ? gload<float>(p.weights + t * p.top + s0 + s) : 1.0f;
+        }
+    }
+};
+
 template <int DT, int W> __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ RowsParams p)
 {
     chain_entry();
     const uint64_t t = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
     if (t >= p.ntokens)
         return;
-    const int32_t *place = p.place + t * p.top;
-    const float *weights = p.weights ? p.weights + t * p.top : nullptr;
+    constexpr int N = Vec<DT, W>::N, AHEAD = W == 0 ? 4 : 1; // single elements: four of a row in flight
     char *dst = p.out + t * p.out_pitch;
-    for (uint32_t i = threadIdx.x; i < p.items; i += blockDim.x) {
-        constexpr int N = Vec<DT, W>::N;
-        float acc[N], f[N];
+    Slots slots;
+    slots.load(p, t, 0);
+    for (uint32_t i0 = threadIdx.x; i0 < p.items; i0 += AHEAD * blockDim.x) {
+        float acc[AHEAD][N], f[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-            acc[k] = 0.0f;
+        for (int j = 0; j < AHEAD; ++j)
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                acc[j][k] = 0.0f;
         for (uint32_t s0 = 0; s0 < p.top; s0 += kSlots) {
-            Vec<DT, W> v[kSlots];
-            uint32_t row[kSlots];
-            float w[kSlots];
+            if (p.top > kSlots)
+                slots.load(p, t, s0);
+            Vec<DT, W> v[AHEAD][kSlots];
 #pragma unroll
-            for (int s = 0; s < kSlots; ++s) {
-                row[s] = s0 + s < p.top ? (uint32_t)gload<int32_t>(place + s0 + s) : 0xffffffffu;
-                w[s] = weights && s0 + s < p.top ? gload<float>(weights + s0 + s) : 1.0f;
-            }
+            for (int j = 0; j < AHEAD; ++j)
 #pragma unroll
-            for (int s = 0; s < kSlots; ++s)
-                if (row[s] < p.nrows)
-                    v[s].load(p.in + row[s] * p.in_pitch, i);
+                for (int s = 0; s < kSlots; ++s)
+                    if (slots.row[s] < p.nrows && i0 + j * blockDim.x < p.items)
+                        v[j][s].load(p.in + slots.row[s] * p.in_pitch, i0 + j * blockDim.x);
 #pragma unroll
-            for (int s = 0; s < kSlots; ++s)
-                if (row[s] < p.nrows) {
-                    v[s].get(f);
+            for (int j = 0; j < AHEAD; ++j)
 #pragma unroll
-                    for (int k = 0; k < N; ++k)
-                        acc[k] = __fmaf_rn(w[s], f[k], acc[k]);
-                }
+                for (int s = 0; s < kSlots; ++s)
+                    if (slots.row[s] < p.nrows && i0 + j * blockDim.x < p.items) {
+                        v[j][s].get(f);
+#pragma unroll
+                        for (int k = 0; k < N; ++k)
+                            acc[j][k] = __fmaf_rn(slots.w[s], f[k], acc[j][k]);
+                    }
         }
-        Vec<DT, W> o;
-        o.set(acc);
-        o.store(dst, i);
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            if (i0 + j * blockDim.x < p.items) {
+                Vec<DT, W> o;
+                o.set(acc[j]);
+                o.store(dst, i0 + j * blockDim.x);
+            }
     }
 }
 
@@ -368,17 +453,16 @@ template <int DT, int W, bool DOTS> __global__ void __launch_bounds__(256) combi
     __shared__ float sums[8][kSlots];
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (uint64_t t = blockIdx.x; t < p.ntokens; t += gridDim.x) {
-        const int32_t *place = p.place + t * p.top;
         const char *dy = p.dy + t * p.dy_pitch;
         for (uint32_t s0 = 0; s0 < p.top; s0 += kSlots) {
-            uint32_t row[kSlots];
-            float w[kSlots], dot[kSlots];
+            Slots slots;
+            slots.load(p, t, s0);
+            const uint32_t(&row)[kSlots] = slots.row;
+            const float(&w)[kSlots] = slots.w;
+            float dot[kSlots];
 #pragma unroll
-            for (int s = 0; s < kSlots; ++s) {
-                row[s] = s0 + s < p.top ? (uint32_t)gload<int32_t>(place + s0 + s) : 0xffffffffu;
-                w[s] = p.weights && s0 + s < p.top ? gload<float>(p.weights + t * p.top + s0 + s) : 1.0f;
+            for (int s = 0; s < kSlots; ++s)
                 dot[s] = 0.0f;
-            }
             for (uint32_t i = threadIdx.x; i < p.items; i += blockDim.x) {
                 constexpr int N = Vec<DT, W>::N;
                 Vec<DT, W> y, v[kSlots], o;
@@ -434,7 +518,7 @@ template <int DT, int W, bool DOTS> __global__ void __launch_bounds__(256) combi
 // ------------------------------------------------------------------ host side
 
 struct OrderPlan {
-    uint32_t n, run, runs, warps; // warps: of the one CTA, 0 where there are several launches
+    uint32_t n, run, runs, warps, ctas; // warps: of a CTA of the one launch, 0 where there are several
     size_t counts, bytes;
 };
 
@@ -444,9 +528,10 @@ bool plan_order(size_t ntokens, size_t top, size_t experts, OrderPlan *p)
         return false;
     *p = OrderPlan{};
     p->n = (uint32_t)(ntokens * top);
-    if (p->n <= kFewChoices) {
+    if (p->n <= kClusterChoices) {
+        p->ctas = p->n <= kFewChoices ? 1 : kOrderCtas;
         p->warps = std::max<uint32_t>(1, std::min<uint32_t>({32, (p->n + 31) / 32, kFewCounters / (uint32_t)std::max<size_t>(experts, 1)}));
-        p->run = ((p->n + p->warps - 1) / p->warps + 31) / 32 * 32;
+        p->run = ((p->n + p->ctas * p->warps - 1) / (p->ctas * p->warps) + 31) / 32 * 32;
         return true;
     }
     // a run a warp, eight of them on every SM, but no fewer choices than experts whose counts it writes
@@ -494,7 +579,24 @@ ccl_status_t order_impl(const int32_t *ids, size_t ntokens, size_t top, int32_t 
     p.run = pl.run;
     cudaError_t e;
     if (pl.warps) {
-        if ((e = launch_chained(order_few_kernel, dim3(1), dim3(32 * pl.warps), 0, stream, p)) == cudaSuccess)
+        if (pl.ctas == 1) {
+            e = launch_chained(order_few_kernel<1>, dim3(1), dim3(32 * pl.warps), 0, stream, p);
+        } else {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(kOrderCtas);
+            cfg.blockDim = dim3(32 * pl.warps);
+            cfg.stream = stream;
+            cudaLaunchAttribute attr[2];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = kOrderCtas;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[1].val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 2;
+            e = cudaLaunchKernelEx(&cfg, order_few_kernel<kOrderCtas>, p);
+        }
+        if (e == cudaSuccess)
             count_launches(1);
         return from_cuda(e);
     }

@@ -37,7 +37,7 @@ def _route_grad(L, z=1 * T40, n=100, e=8, zs=8, dt=0, ids=2 * T40, top=2, norm=1
     return L.ccl_route_grad(z, n, e, zs, dt, ids, top, norm, lse, counts, load, gw, b, c, grad, gs, None)
 
 
-def _order(L, ids=1 * T40, n=5000, top=2, first=0, e=8, off=2 * T40, place=3 * T40, work=4 * T40, nbytes=1 << 24):
+def _order(L, ids=1 * T40, n=50000, top=2, first=0, e=8, off=2 * T40, place=3 * T40, work=4 * T40, nbytes=1 << 24):
     return L.ccl_expert_order(ids, n, top, first, e, off, place, work, nbytes, None)
 
 
@@ -150,8 +150,8 @@ def test_plans():
     # one CTA needs no working space; several leave a row of sums each
     assert ccl.ccl_plan_route_work_bytes(8, 256) == 0 and ccl.ccl_plan_route_work_bytes(256, 64) == 0
     assert ccl.ccl_plan_route_work_bytes(1 << 20, 256) == -(-152 * 257 * 4 // 256) * 256 + -(-152 * 258 * 4 // 256) * 256
-    assert ccl.ccl_plan_expert_order_work_bytes(512, 8, 64) == 0
-    assert ccl.ccl_plan_expert_order_work_bytes(4097, 1, 64) == -(-65 * 64 * 4 // 256) * 256 + 256
+    assert ccl.ccl_plan_expert_order_work_bytes(8192, 8, 64) == 0
+    assert ccl.ccl_plan_expert_order_work_bytes(65537, 1, 64) == 64 * 1025 * 4 + 256  # 1025 runs of 64
     # backward: h, dg and du in rows of whole blocks, and x and grad_out, every expert's rows padded to a multiple of 64
     r, e, d, f = 1000, 4, 512, 776
     padded = -(-(r + 63 * e) // 64) * 64
