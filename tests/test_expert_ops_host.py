@@ -150,7 +150,7 @@ def test_plans():
     # one CTA needs no working space; several leave a row of sums each
     assert ccl.ccl_plan_route_work_bytes(8, 256) == 0 and ccl.ccl_plan_route_work_bytes(256, 64) == 0
     assert ccl.ccl_plan_route_work_bytes(1 << 20, 256) == -(-152 * 257 * 4 // 256) * 256 + -(-152 * 258 * 4 // 256) * 256
-    assert ccl.ccl_plan_expert_order_work_bytes(8192, 8, 64) == 0
+    assert ccl.ccl_plan_expert_order_work_bytes(2048, 8, 64) == 0
     assert ccl.ccl_plan_expert_order_work_bytes(65537, 1, 64) == 64 * 1025 * 4 + 256  # 1025 runs of 64
     # backward: h, dg and du in rows of whole blocks, and x and grad_out, every expert's rows padded to a multiple of 64
     r, e, d, f = 1000, 4, 512, 776

@@ -29,10 +29,11 @@ def order(ids, experts, first=0, **kw):
     return offsets, place
 
 
-# one choice; one CTA with few and all of its warps; experts that limit the warps; either side of 4096 and of 65536, where a cluster
+# one choice; one CTA with few and all of its warps; experts that limit the warps; either side of 4096 and of 16384, where a cluster
 # and several launches take over, the cluster with fewer threads than experts; several runs a CTA
 @pytest.mark.parametrize("T,K,E", [(1, 1, 1), (1, 8, 8), (7, 3, 5), (33, 1, 1024), (512, 8, 64), (500, 8, 700), (4096, 1, 1024), (4097, 1, 3), (1025, 4, 64),
-                                   (9000, 8, 1024), (100000, 2, 16), (1 << 20, 1, 1), (70001, 6, 333)])
+                                   (2048, 8, 64), (16385, 1, 64), (5000, 3, 1024), (2001, 7, 400), (9001, 7, 400), (9000, 8, 1024), (100000, 2, 16),
+                                   (1 << 20, 1, 1), (70001, 6, 333)])
 def test_order(T, K, E):
     g = torch.Generator(device=DEV).manual_seed(T + E)
     ids = (torch.randn(T, K, generator=g, device=DEV).abs() * E / 3).to(I32).clamp_(max=E)  # uneven, E itself is none
