@@ -93,7 +93,9 @@ struct ExpertParams {
     // expert_few_kernel
     float *partial; // [splits][rows][column tiles * 256]
     uint32_t splits, npad, stages;
-    int early; // the weights and the offsets may be read before the kernel before this one has ended
+    // the offsets (and by expert_few_kernel the weights) may be read before the
+    // kernel before this one, which began after they were there, has ended
+    int early;
 };
 
 __device__ unsigned long long g_expert_timeouts;
@@ -542,8 +544,11 @@ __global__ void __launch_bounds__(128 + 32 * WARPS, 1) expert_gemm_kernel(const 
     cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = tmem_slot;
-    chain_entry();
+    if (!p.early)
+        chain_entry();
     make_table(p, table, kTileM);
+    if (p.early)
+        chain_entry();
     const uint32_t total = units_of<EPI>(p, table);
 
     if (warp == 0 && lane == 0) {
@@ -1556,6 +1561,7 @@ ccl_status_t expert_ffn_impl(const ExpertArgs &a, void *out, cudaStream_t stream
         return CCL_ERR_CUDA;
     if (cudaError_t e = launch_gemm<EPI_GATED, false, false>(p, tiles * q.nt, stream))
         return from_cuda(e);
+    p.early = 1;
     const bool vectors = a.d % 8 == 0 && (uintptr_t)out % 16 == 0;
     p.half = half_tile(likely, a.d, tiles_of(a.f, kTileK), vectors ? 2.5 : 4.0);
     set_problem(q, a.d, 2 * p.half, a.f, 1);
@@ -1647,6 +1653,7 @@ ccl_status_t expert_ffn_grad_impl(const ExpertArgs &a, const void *dy, void *dx,
     p.half = half_tile(likely, a.f, tiles_of(a.d, kTileK), 7.0);
     set_problem(q, a.f, 2 * p.half, a.d, 1);
     p.padded = !direct_y;
+    p.early = 1;
     if (!encode_rows(&q.a[0], direct_y ? ly : y, false) || !encode_experts(&q.b[0], wd, a.e, true))
         return CCL_ERR_CUDA;
     if ((e = launch_gemm<EPI_BACKWARD, false, true>(p, tiles * q.nt, stream)))

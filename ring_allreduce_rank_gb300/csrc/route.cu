@@ -33,9 +33,10 @@ namespace {
 constexpr int kJoinCtas = 8; // one portable cluster
 constexpr size_t kMaxTokens = 0x7fffffff;
 constexpr int kRouteThreads = 256; // route_grad_kernel's
-// route_kernel's, at most: one CTA an SM with eight values a lane, so that 152
-// rows of partial sums are left; two with 32, whose lanes take 128 registers.
-constexpr int route_threads(int values) { return values <= 8 ? 1024 : 256; }
+// route_kernel's, at most: one CTA an SM with eight or sixteen values a lane, so
+// that 152 rows of partial sums are left; two with 32.  Lanes take 64 to 128
+// registers.
+constexpr int route_threads(int values) { return values <= 8 ? 1024 : values <= 16 ? 512 : 256; }
 
 struct RouteParams {
     const char *logits;
@@ -204,7 +205,7 @@ template <int DT, int L, int V, int N> __global__ void __launch_bounds__(route_t
                 v[i] = -INFINITY;
         }
     };
-    constexpr bool kAhead = V <= 8; // the next row's values fit beside this one's
+    constexpr bool kAhead = V <= 16; // the next row's values fit beside this one's
     float f[V], next[kAhead ? V : 1];
     if (kAhead)
         fetch(0, f);
@@ -530,9 +531,9 @@ bool plan_route(size_t ntokens, size_t experts, RoutePlan *p)
         return false;
     *p = RoutePlan{};
     p->lanes = experts <= 64 ? 8 : 32;
-    const size_t most = route_threads(experts <= 256 ? 8 : 32), groups = most / p->lanes, all = (ntokens + groups - 1) / groups;
+    const size_t most = route_threads(experts <= 256 ? 8 : experts <= 512 ? 16 : 32), groups = most / p->lanes, all = (ntokens + groups - 1) / groups;
     // one CTA for two rounds of rows: it needs no second launch
-    p->ctas = all <= 2 ? 1 : (uint32_t)std::min<size_t>(all, experts <= 256 ? 152 : 304);
+    p->ctas = all <= 2 ? 1 : (uint32_t)std::min<size_t>(all, experts <= 512 ? 152 : 304);
     p->threads = (uint32_t)std::min<size_t>(most, std::max<size_t>(ntokens * p->lanes + 31, 32) / 32 * 32);
     if (p->ctas > 1) {
         p->sums = up(p->ctas * (experts + 1) * 4);
@@ -559,6 +560,8 @@ template <int DT, bool GRAD> cudaError_t launch_route2(const RouteParams &p, uns
         return launch_route3<DT, 8, 8, GRAD>(p, ctas, threads, stream);
     if (p.experts <= 256)
         return launch_route3<DT, 32, 8, GRAD>(p, ctas, threads, stream);
+    if (p.experts <= 512)
+        return launch_route3<DT, 32, 16, GRAD>(p, ctas, threads, stream);
     return launch_route3<DT, 32, 32, GRAD>(p, ctas, threads, stream);
 }
 
