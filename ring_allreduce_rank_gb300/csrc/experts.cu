@@ -64,6 +64,23 @@ enum Epilogue { EPI_GATED = 0, EPI_STORE = 1, EPI_BACKWARD = 2, EPI_WEIGHTS = 3 
 // vectors the barriers cost more than full lines gain, 44 -> 60 us).
 constexpr int kDirect = 8, kStaged = 16;
 
+// Division of numbers below 2^31 by a number that the host knows: the multiplier
+// and shift of Granlund and Montgomery, "Division by invariant integers using
+// multiplication" (1994).  Each role of a CTA works out every unit it takes part
+// in, which the divider's chain made most of for the shortest products.
+struct Divisor {
+    uint32_t mul, shift, by;
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
+Divisor divisor(uint32_t by)
+{
+    uint32_t shift = 0;
+    while (shift < 31 && (1u << shift) < by)
+        ++shift;
+    return Divisor{(uint32_t)((((1ull << shift) - by) << 32) / by + 1), shift, by};
+}
+
 // C[M, N] = sum over segments of A_s[M, K] B_s[N, K]^T for each expert: M its
 // rows, or for EPI_WEIGHTS K its rows.
 struct Problem {
@@ -71,6 +88,7 @@ struct Problem {
     void *out;      // EPI_STORE: row stride n; EPI_WEIGHTS: [experts][m][n]
     uint32_t m, n;  // m: EPI_WEIGHTS only
     uint32_t mt, nt; // tiles (mt: EPI_WEIGHTS only)
+    Divisor by_nt, by_group; // nt, kGroupM * nt
     uint32_t kblocks, segs;
     // EPI_WEIGHTS: a[1], b[1] are the rows as they lie, which full blocks of K
     // are read from; the last, partial one is in the padded layout (a[0], b[0])
@@ -80,6 +98,7 @@ struct Problem {
 struct ExpertParams {
     Problem prob[3];
     uint32_t nprob;
+    Divisor by_expert; // EPI_WEIGHTS: an expert's units
     const int32_t *offsets;
     uint32_t experts, rows;
     int act, accumulate;
@@ -194,10 +213,7 @@ template <int EPI> __device__ __forceinline__ uint32_t units_of(const ExpertPara
 {
     if (EPI != EPI_WEIGHTS)
         return (uint32_t)t.tile0[p.experts] * p.prob[0].nt;
-    uint32_t n = 0;
-    for (uint32_t i = 0; i < p.nprob; ++i)
-        n += p.prob[i].mt * p.prob[i].nt;
-    return n * p.experts;
+    return p.by_expert.by * p.experts;
 }
 
 template <int EPI> __device__ __forceinline__ Unit unit_at(const ExpertParams &p, const Table &tb, uint32_t i)
@@ -206,11 +222,8 @@ template <int EPI> __device__ __forceinline__ Unit unit_at(const ExpertParams &p
     u.prob = u.split = 0;
     uint32_t t, mt;
     if (EPI == EPI_WEIGHTS) {
-        uint32_t per = 0;
-        for (uint32_t k = 0; k < p.nprob; ++k)
-            per += p.prob[k].mt * p.prob[k].nt;
-        u.expert = i / per;
-        t = i % per;
+        u.expert = p.by_expert(i);
+        t = i - u.expert * p.by_expert.by;
         while (t >= p.prob[u.prob].mt * p.prob[u.prob].nt) {
             t -= p.prob[u.prob].mt * p.prob[u.prob].nt;
             ++u.prob;
@@ -218,15 +231,22 @@ template <int EPI> __device__ __forceinline__ Unit unit_at(const ExpertParams &p
         mt = p.prob[u.prob].mt;
     } else {
         const uint32_t nt = p.prob[0].nt;
-        u.expert = expert_at(tb.tile0, p.experts, (int32_t)(i / nt));
+        u.expert = expert_at(tb.tile0, p.experts, (int32_t)p.prob[0].by_nt(i));
         t = i - (uint32_t)tb.tile0[u.expert] * nt;
         mt = (uint32_t)(tb.tile0[u.expert + 1] - tb.tile0[u.expert]);
     }
     const Problem &q = p.prob[u.prob];
-    const uint32_t per = kGroupM * q.nt, grp = t / per, in = t % per;
-    const uint32_t gm = min(mt - grp * kGroupM, (uint32_t)kGroupM);
-    u.m = grp * kGroupM + in % gm;
-    u.n = in / gm;
+    const uint32_t grp = q.by_group(t), in = t - grp * kGroupM * q.nt, gm = mt - grp * kGroupM;
+    if (gm >= kGroupM) {
+        u.n = in / kGroupM;
+        u.m = grp * kGroupM + in % kGroupM;
+    } else if (gm == 1) {
+        u.n = in;
+        u.m = grp * kGroupM;
+    } else {
+        u.n = in / gm;
+        u.m = grp * kGroupM + in % gm;
+    }
     u.row0 = (uint32_t)tb.row0[u.expert];
     u.rows = (uint32_t)tb.row0[u.expert + 1] - u.row0;
     u.pad0 = (uint32_t)tb.pad0[u.expert];
@@ -275,6 +295,29 @@ template <bool MN> __device__ __forceinline__ void load_expert(uint32_t dst, con
 }
 
 // ------------------------------------------------------------------ epilogues
+
+__device__ __forceinline__ void tc_load64(uint32_t addr, float *f)
+{
+    uint32_t r[64];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+                 "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+                 "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+                   "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+                   "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+                   "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+                   "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+                 : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+        f[i] = __uint_as_float(r[i]);
+}
 
 constexpr uint32_t kNanBits = 0x7fffffffu;
 
@@ -713,30 +756,29 @@ __global__ void __launch_bounds__(128 + 32 * WARPS, 1) expert_gemm_kernel(const 
                 release();
             } else if (WARPS == kDirect) {
                 // a lane keeps its row, sixteen columns at a time of one half of
-                // the tile, what it adds to asked for one step ahead
+                // the tile
                 uint32_t rows;
                 const uint32_t c1 = (warp - 4) / 4 * u.half;
                 uint16_t *at = unit_out<EPI>(p, u, rows) + (uint64_t)in * q.n + col0 + c1;
                 const uint32_t n = in < rows && col0 + c1 < q.n ? q.n - col0 - c1 : 0; // columns of this row from there on
-                Vals16 old;
-                if (p.accumulate && n)
-                    old.load(at, 8 < n);
-#pragma unroll 2
-                for (uint32_t c = 0; c < u.half && in0 < rows; c += 16) {
-                    float v[16];
+                for (uint32_t c = 0; c < u.half && in0 < rows; c += 64) { // the last columns read may be another half's
+                    Vals16 old[4];
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k)
+                        if (p.accumulate && c + 16 * k < min(n, u.half))
+                            old[k].load(at + c + 16 * k, c + 16 * k + 8 < n);
+                    float v[64];
                     if (some) {
-                        tc_load16(acc + c1 + c, v);
+                        tc_load64(acc + c1 + c, v);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
+                        for (int j = 0; j < 64; ++j)
                             v[j] = 0.0f;
                     }
-                    Vals16 next;
-                    if (p.accumulate && c + 16 < u.half && c + 16 < n)
-                        next.load(at + c + 16, c + 24 < n);
-                    if (c < n)
-                        finish_store(p, at + c, c + 8 < n, old, v);
-                    old = next;
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k)
+                        if (c + 16 * k < min(n, u.half))
+                            finish_store(p, at + c + 16 * k, c + 16 * k + 8 < n, old[k], v + 16 * k);
                 }
                 if (some)
                     release();
@@ -876,8 +918,8 @@ template <int EPI> __device__ __forceinline__ Unit few_unit_at(const ExpertParam
     u.prob = 0;
     u.split = i % p.splits;
     i /= p.splits;
-    u.n = i % q.nt;
-    const uint32_t t = i / q.nt;
+    const uint32_t t = q.by_nt(i);
+    u.n = i - t * q.nt;
     u.expert = expert_at(tb.tile0, p.experts, (int32_t)t);
     u.m = t - (uint32_t)tb.tile0[u.expert];
     u.row0 = (uint32_t)tb.row0[u.expert] + u.m * p.npad;
@@ -1504,6 +1546,8 @@ void set_problem(Problem &q, uint64_t n, uint32_t tile, uint64_t k, uint32_t seg
 {
     q.n = (uint32_t)n;
     q.nt = tiles_of(n, tile);
+    q.by_nt = divisor(q.nt);
+    q.by_group = divisor(kGroupM * q.nt);
     q.kblocks = tiles_of(k, kTileK);
     q.segs = segs;
 }
@@ -1695,9 +1739,10 @@ ccl_status_t expert_ffn_grad_impl(const ExpertArgs &a, const void *dy, void *dx,
             if (!encode_rows(&o.a[0], *am[i], true) || !encode_rows(&o.b[0], *bm[i], true) || (o.direct_a && !encode_rows(&o.a[1], ly, true)) ||
                 (o.direct_b && !encode_rows(&o.b[1], lx, true)))
                 return CCL_ERR_CUDA;
-            units += (uint64_t)o.mt * o.nt * a.e;
+            units += (uint64_t)o.mt * o.nt;
         }
-    return from_cuda(launch_out<EPI_WEIGHTS, true, true>(p, vectors, units, stream));
+    p.by_expert = divisor((uint32_t)units);
+    return from_cuda(launch_out<EPI_WEIGHTS, true, true>(p, vectors, units * a.e, stream));
 }
 
 } // namespace
