@@ -14,18 +14,26 @@
 //     of a product do not meet, and the epilogue writes an expert's own rows.
 //     Only in the weight gradients are rows summed over.  There every expert's
 //     rows begin at a multiple of 64 (a K block) in a padded layout of the work
-//     buffer, zeros behind them: x and the incoming gradient are copied there,
-//     x from its 8 bits if that is how it was kept, and h, dg and du are written
-//     there by the epilogue that makes them.
+//     buffer, zeros behind them: h, dg and du are written there by the epilogue
+//     that makes them, and of x and the incoming gradient the last, partial
+//     block of each expert is copied there (all rows, where TMA cannot address
+//     them or x is kept in 8 bits), so that no row, finite or not, reaches
+//     another expert's sums.
 //   - g and u are kept in 8 bits (act8.cuh): an epilogue thread holds 32
 //     consecutive columns of a row, which is a block.  The codes' rows are whole
 //     blocks, and zeros behind the last column come from the tensor maps.
 //   - Few rows an expert: the weights are the accumulator's rows and a tile of
 //     16 to 128 tokens its columns (expert_few_kernel), the sums cut along K when
-//     that leaves SMs idle.
+//     that leaves SMs idle.  (Cutting them on pairs was slower: 35 -> 41 us and
+//     the join for the gradient by 4026 rows of 320.)
 //
 // Bound by the tensor cores for many rows an expert, by reading the weights (and
-// writing their gradients) for few.
+// writing their gradients) for few.  Two experts of eight for each of 4096
+// tokens at 4096 x 11008, forward: 1.31-1.37 ms, at the power limit 1.45-1.53
+// (1.45-1.69 PFLOP/s; cuBLAS sustains 1.72 there), an eighth of the products
+// being of row tiles that an expert does not fill; the same for one token 94 us
+// (5.7 TB/s of weights, 0.85 of the copy bandwidth).  Forward and backward of
+// 32768 rows over 32 experts of 2048 x 1408: 1.36-1.5 ms, 1.1-1.25 PFLOP/s.
 #include <algorithm>
 #include <vector>
 
@@ -41,13 +49,13 @@ namespace {
 constexpr int kTileM = 256, kTileN = 256, kTileK = 64; // a CTA pair's tile
 constexpr int kOperandBytes = 128 * kTileK * 2;        // one CTA's part of A or B in a stage
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kStages = 6, kStagedStages = 5; // the latter beside the room that outputs are staged in
-constexpr int kEpiWarps = 8, kFewThreads = 128 + 32 * kEpiWarps; // expert_few_kernel's
-// Staging: 32 rows of 128 bf16 columns for each of the four groups of epilogue
-// warps.  The pitch puts eight rows' 16 bytes in different banks.
+constexpr int kStages = 6, kStagedStages = 4; // the latter beside the room that outputs are staged in
+constexpr int kEpiWarps = 8, kPairThreads = 128 + 32 * kEpiWarps; // beside them: producer, issuer, tensor memory, an idle warp
+// Staging: 32 rows of 128 bf16 columns for each of the epilogue warps.  The
+// pitch puts eight rows' 16 bytes in different banks.
 constexpr uint32_t kPitch = 272, kStaging = 32 * kPitch;
 constexpr int kTableBytes = 3 * (CCL_MAX_EXPERTS + 2) * 4;
-constexpr int kGemmSmem = 1024 /* alignment */ + kTableBytes + std::max(kStages * kStageBytes, kStagedStages * kStageBytes + 4 * (int)kStaging);
+constexpr int kGemmSmem = 1024 /* alignment */ + kTableBytes + std::max(kStages * kStageBytes, kStagedStages * kStageBytes + kEpiWarps * (int)kStaging);
 constexpr int kGroupM = 8; // row tiles walked before the next column tile
 constexpr uint32_t kPad = kTileK; // an expert's rows in the padded layout are a multiple of this
 constexpr int kFewStages = 6;
@@ -56,13 +64,13 @@ constexpr uint32_t kFewMost = 128;    // tokens of one tile
 
 enum Epilogue { EPI_GATED = 0, EPI_STORE = 1, EPI_BACKWARD = 2, EPI_WEIGHTS = 3 };
 
-// Epilogue warps of expert_gemm_kernel.  A lane has a row and writes 32 bytes of
-// it at a time; eight warps hide behind the products of a long K, which sixteen
-// slow down by 5 %.  Rows that no 16-byte vector divides are staged in shared
-// memory by sixteen, four of which share 32 rows, so that a warp writes along a
-// row (many experts' weight gradients of 530 x 1809: 459 -> 266 us; for whole
-// vectors the barriers cost more than full lines gain, 44 -> 60 us).
-constexpr int kDirect = 8, kStaged = 16;
+// An epilogue warp's lane has a row of the accumulator and writes 32 bytes of it
+// at a time.  Rows that no 16-byte vector divides are staged in shared memory
+// (STAGED), so that the warp writes words along a row (weight gradients of 73
+// experts of 530 x 1809: a value a lane 760 us, staged 220); for whole vectors
+// staging costs more than full lines gain (44 -> 60 us).  Launches with staged
+// outputs neither begin before the kernel before them has ended nor let the next
+// one begin.
 
 // Division of numbers below 2^31 by a number that the host knows: the multiplier
 // and shift of Granlund and Montgomery, "Division by invariant integers using
@@ -112,9 +120,7 @@ struct ExpertParams {
     // expert_few_kernel
     float *partial; // [splits][rows][column tiles * 256]
     uint32_t splits, npad, stages;
-    // the offsets (and by expert_few_kernel the weights) may be read before the
-    // kernel before this one, which began after they were there, has ended
-    int early;
+    int early; // the weights and the offsets may be read before the kernel before this one has ended
 };
 
 __device__ unsigned long long g_expert_timeouts;
@@ -373,57 +379,33 @@ __device__ __forceinline__ uint32_t shared_load4(uint32_t at)
     return v;
 }
 
-// The barrier of the 128 threads that share 32 rows, and the same with the
-// question whether all say yes.
-__device__ __forceinline__ void rows_sync(uint32_t quarter) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + quarter) : "memory"); }
-
-__device__ __forceinline__ bool rows_all(uint32_t quarter, bool yes)
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
-                 "barrier.cta.red.and.pred p, %1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(r)
-                 : "r"(1 + quarter), "r"((uint32_t)yes)
-                 : "memory");
-    return r != 0;
-}
-
-// 32 staged columns of a lane's row, packed in pairs.
-__device__ __forceinline__ void stage32(uint32_t at, const uint32_t *w)
-{
-#pragma unroll
-    for (int i = 0; i < 16; i += 4)
-        shared_store16(at + 4 * i, w[i], w[i + 1], w[i + 2], w[i + 3]);
-}
-
-// Staged rows (at most 32, of `cols` <= 128 columns) to out, rows `ld` apart, by
-// 128 threads: as words, with single values at the ends.  A warp takes every
-// fourth row, all of the parity of its first.
+// A warp's staged rows (at most 32, of `cols` <= 128 columns) to out, rows `ld`
+// apart: as words, with single values at the ends.  `step` 2 takes every second
+// row where rows of an odd length change their parity.
 __device__ __forceinline__ void staged_out(uint32_t staging, uint16_t *out, uint64_t ld, uint32_t rows, uint32_t cols)
 {
-    const uint32_t lane = threadIdx.x & 31, r0 = threadIdx.x / 128 - 1;
-    if (r0 >= rows || cols == 0)
-        return;
-    uint16_t *dst = out + r0 * ld;
-    uint32_t src = staging + r0 * kPitch;
-    const uint32_t odd = ((uintptr_t)dst & 2) / 2, n = (rows - r0 + 3) / 4; // words begin at column `odd`
-    const bool first = 2 * lane + odd + 1 < cols, second = 2 * lane + 64 + odd + 1 < cols;
-    const bool edge = lane == 0 ? odd : lane == 1 ? cols > odd && (cols - odd) % 2 : false; // the columns that no word holds
-    const uint32_t at = lane == 0 ? 0 : cols - 1;
-    const uint32_t shift = odd * 16;
-#pragma unroll 2
-    for (uint32_t r = 0; r < n; ++r, dst += 4 * ld, src += 4 * kPitch) {
-        uint32_t a = shared_load4(src + 4 * lane), b = shared_load4(src + 4 * lane + 128);
-        if (odd) {
-            a = __funnelshift_r(a, shared_load4(src + 4 * lane + 4), shift);
-            b = __funnelshift_r(b, shared_load4(src + 4 * lane + 132), shift);
+    const uint32_t lane = threadIdx.x & 31, step = ld % 2 ? 2 : 1;
+    for (uint32_t r0 = 0; r0 < step && r0 < rows && cols; ++r0) {
+        uint16_t *dst = out + r0 * ld;
+        uint32_t src = staging + r0 * kPitch;
+        const uint32_t odd = ((uintptr_t)dst & 2) / 2, n = (rows - r0 + step - 1) / step; // words begin at column `odd`
+        const bool first = 2 * lane + odd + 1 < cols, second = 2 * lane + 64 + odd + 1 < cols;
+        const bool edge = lane == 0 ? odd : lane == 1 ? cols > odd && (cols - odd) % 2 : false; // the columns that no word holds
+        const uint32_t at = lane == 0 ? 0 : cols - 1, shift = odd * 16;
+#pragma unroll 4
+        for (uint32_t r = 0; r < n; ++r, dst += step * ld, src += step * kPitch) {
+            uint32_t a = shared_load4(src + 4 * lane), b = shared_load4(src + 4 * lane + 128);
+            if (odd) {
+                a = __funnelshift_r(a, shared_load4(src + 4 * lane + 4), shift);
+                b = __funnelshift_r(b, shared_load4(src + 4 * lane + 132), shift);
+            }
+            if (first)
+                gstore<uint32_t>(dst + 2 * lane + odd, a);
+            if (second)
+                gstore<uint32_t>(dst + 2 * lane + 64 + odd, b);
+            if (edge)
+                gstore<uint16_t>(dst + at, (uint16_t)(shared_load4(src + at / 2 * 4) >> at % 2 * 16));
         }
-        if (first)
-            gstore<uint32_t>(dst + 2 * lane + odd, a);
-        if (second)
-            gstore<uint32_t>(dst + 2 * lane + 64 + odd, b);
-        if (edge)
-            gstore<uint16_t>(dst + at, (uint16_t)(shared_load4(src + at / 2 * 4) >> at % 2 * 16));
     }
 }
 
@@ -432,7 +414,7 @@ __device__ __forceinline__ void staged_in(uint32_t staging, const uint16_t *out,
 {
     const uint32_t lane = threadIdx.x & 31;
 #pragma unroll 2
-    for (uint32_t r = threadIdx.x / 128 - 1; r < rows; r += 4)
+    for (uint32_t r = 0; r < rows; ++r)
 #pragma unroll
         for (uint32_t k = 0; k < 4; ++k) {
             const uint32_t c = lane + 32 * k;
@@ -541,16 +523,16 @@ template <int EPI> __device__ __forceinline__ uint16_t *unit_out(const ExpertPar
 
 // ------------------------------------------------------------------ the product on CTA pairs
 
-template <int EPI, bool A_MN, bool B_MN, int WARPS>
-__global__ void __launch_bounds__(128 + 32 * WARPS, 1) expert_gemm_kernel(const __grid_constant__ ExpertParams p)
+template <int EPI, bool A_MN, bool B_MN, bool STAGED>
+__global__ void __launch_bounds__(kPairThreads, 1) expert_gemm_kernel(const __grid_constant__ ExpertParams p)
 {
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t bars[2 * kStages + 4];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int gave_up;
     const uint32_t stages = (smem_u32(raw) + 1023) & ~1023u;
-    constexpr uint32_t nstages = WARPS == kStaged ? kStagedStages : kStages;
-    uint8_t *behind = raw + (stages - smem_u32(raw)) + nstages * kStageBytes + (WARPS == kStaged ? 4 * kStaging : 0);
+    constexpr uint32_t nstages = STAGED ? kStagedStages : kStages;
+    uint8_t *behind = raw + (stages - smem_u32(raw)) + nstages * kStageBytes + (STAGED ? kEpiWarps * kStaging : 0);
     const Table table{reinterpret_cast<int32_t *>(behind), reinterpret_cast<int32_t *>(behind) + CCL_MAX_EXPERTS + 2,
                       reinterpret_cast<int32_t *>(behind) + 2 * (CCL_MAX_EXPERTS + 2)};
     const uint32_t full = smem_u32(&bars[0]), empty = smem_u32(&bars[kStages]);
@@ -566,7 +548,7 @@ __global__ void __launch_bounds__(128 + 32 * WARPS, 1) expert_gemm_kernel(const 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
-            mbar_init(acc_empty + 8 * i, 2 * WARPS);
+            mbar_init(acc_empty + 8 * i, 2 * kEpiWarps);
         }
         if ((gave_up = p.wait_ns == 0))
             atomicAdd(&g_expert_timeouts, 1ull);
@@ -587,11 +569,9 @@ __global__ void __launch_bounds__(128 + 32 * WARPS, 1) expert_gemm_kernel(const 
     cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = tmem_slot;
-    if (!p.early)
+    if (!STAGED)
         chain_entry();
     make_table(p, table, kTileM);
-    if (p.early)
-        chain_entry();
     const uint32_t total = units_of<EPI>(p, table);
 
     if (warp == 0 && lane == 0) {
@@ -678,13 +658,13 @@ __global__ void __launch_bounds__(128 + 32 * WARPS, 1) expert_gemm_kernel(const 
             ++t;
         }
     } else if (warp >= 4) {
-        // epilogue: warp w reads lanes 32 (w % 4) .. + 32 and every kStride-th 32
-        // columns; the four warps that read the same lanes stage and write together
-        constexpr uint32_t kStride = 32 * WARPS / 4;
-        const uint32_t c0 = (warp - 4) / 4 * 32, quarter = warp & 3;
-        const uint32_t lanes = quarter * 32;
+        // epilogue: warp w reads lanes 32 (w % 4) .. + 32 and every second 32
+        // columns, or of an output one half of the columns
+        constexpr uint32_t kStride = 32 * kEpiWarps / 4;
+        const uint32_t c0 = (warp - 4) / 4 * 32;
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32;
         const uint32_t leader_empty = in_cta(acc_empty, 0);
-        const uint32_t staging = stages + nstages * kStageBytes + quarter * kStaging;
+        const uint32_t staging = stages + nstages * kStageBytes + (warp - 4) * kStaging;
         uint32_t t = 0, i = pair;
         for (; p.wait_ns && i < total; i += pairs) {
             const Unit u = unit_at<EPI>(p, table, i);
@@ -701,8 +681,6 @@ __global__ void __launch_bounds__(128 + 32 * WARPS, 1) expert_gemm_kernel(const 
             bool ok = true;
             if (some)
                 ok = __all_sync(0xffffffffu, mbar_wait(acc_full + 8 * buf, (t >> 1) & 1, &gave_up, p.wait_ns));
-            if (WARPS == kStaged)
-                ok = rows_all(quarter, ok); // none stays behind in a barrier; what was staged before is written
             if (!ok)
                 break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -727,7 +705,7 @@ __global__ void __launch_bounds__(128 + 32 * WARPS, 1) expert_gemm_kernel(const 
                         }
                     }
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) { // read again: few registers, many warps
+                    for (int k = 0; k < 2; ++k) { // read again, which costs less than the registers
                         float g[16], v[16];
                         tc_load16(acc + c + 16 * k, g);
                         tc_load16(acc + u.half + c + 16 * k, v);
@@ -754,18 +732,24 @@ __global__ void __launch_bounds__(128 + 32 * WARPS, 1) expert_gemm_kernel(const 
                     ahead = next;
                 }
                 release();
-            } else if (WARPS == kDirect) {
-                // a lane keeps its row, sixteen columns at a time of one half of
-                // the tile
+            } else {
+                // one half of the tile's columns, 64 at a time
                 uint32_t rows;
                 const uint32_t c1 = (warp - 4) / 4 * u.half;
-                uint16_t *at = unit_out<EPI>(p, u, rows) + (uint64_t)in * q.n + col0 + c1;
-                const uint32_t n = in < rows && col0 + c1 < q.n ? q.n - col0 - c1 : 0; // columns of this row from there on
-                for (uint32_t c = 0; c < u.half && in0 < rows; c += 64) { // the last columns read may be another half's
+                uint16_t *out = unit_out<EPI>(p, u, rows) + (uint64_t)in0 * q.n + col0 + c1; // the warp's first row
+                rows = rows > in0 ? min(rows - in0, 32u) : 0;
+                const uint32_t wide = col0 + c1 < q.n ? min(q.n - col0 - c1, u.half) : 0; // columns that there are
+                if (STAGED && p.accumulate) {
+                    staged_in(staging, out, q.n, rows, wide);
+                    __syncwarp();
+                }
+                const uint32_t n = lane < rows ? wide : 0; // of this lane's row
+                uint16_t *at = out + (uint64_t)lane * q.n;
+                for (uint32_t c = 0; c < u.half && rows; c += 64) { // the last columns read may be the other half's
                     Vals16 old[4];
 #pragma unroll
                     for (uint32_t k = 0; k < 4; ++k)
-                        if (p.accumulate && c + 16 * k < min(n, u.half))
+                        if (!STAGED && p.accumulate && c + 16 * k < n)
                             old[k].load(at + c + 16 * k, c + 16 * k + 8 < n);
                     float v[64];
                     if (some) {
@@ -776,56 +760,37 @@ __global__ void __launch_bounds__(128 + 32 * WARPS, 1) expert_gemm_kernel(const 
                             v[j] = 0.0f;
                     }
 #pragma unroll
-                    for (uint32_t k = 0; k < 4; ++k)
-                        if (c + 16 * k < min(n, u.half))
+                    for (uint32_t k = 0; k < 4; ++k) {
+                        if (STAGED) {
+                            const uint32_t to = staging + lane * kPitch + 2 * (c + 16 * k); // 64 columns: inside the row of 128
+                            uint32_t w[8];
+#pragma unroll
+                            for (int j = 0; j < 8; j += 4) {
+                                uint4 x = make_uint4(0, 0, 0, 0);
+                                if (p.accumulate)
+                                    x = shared_load16(to + 4 * j);
+                                const uint32_t was[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int l = 0; l < 4; ++l) {
+                                    const float *f = v + 16 * k + 2 * (j + l);
+                                    w[j + l] = p.accumulate ? pack2(__fadd_rn(__uint_as_float(was[l] << 16), f[0]),
+                                                                    __fadd_rn(__uint_as_float(was[l] & 0xffff0000u), f[1]))
+                                                            : pack2(f[0], f[1]);
+                                }
+                                shared_store16(to + 4 * j, w[j], w[j + 1], w[j + 2], w[j + 3]);
+                            }
+                        } else if (c + 16 * k < n) {
                             finish_store(p, at + c + 16 * k, c + 16 * k + 8 < n, old[k], v + 16 * k);
+                        }
+                    }
                 }
                 if (some)
                     release();
-            } else {
-                uint32_t rows;
-                uint16_t *out = unit_out<EPI>(p, u, rows) + (uint64_t)in0 * q.n + col0;
-                rows = rows > in0 ? min(rows - in0, 32u) : 0;
-                const uint32_t left = min(cols, q.n - col0);
-                for (uint32_t c = 0; c < cols && rows; c += kStride) {
-                    const bool mine = c + c0 < cols;
-                    const uint32_t wide = left > c ? min(left - c, 128u) : 0;
-                    uint32_t w[16];
-                    if (p.accumulate) {
-                        staged_in(staging, out + c, q.n, rows, wide);
-                        rows_sync(quarter);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint4 x = shared_load16(staging + lane * kPitch + 2 * c0 + 16 * k);
-                            w[4 * k] = x.x;
-                            w[4 * k + 1] = x.y;
-                            w[4 * k + 2] = x.z;
-                            w[4 * k + 3] = x.w;
-                        }
-                        rows_sync(quarter);
-                    }
-                    if (mine) {
-                        float v[32];
-                        if (some) {
-                            tc_load32(acc + c + c0, v);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                v[j] = 0.0f;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            w[j] = p.accumulate ? pack2(__fadd_rn(__uint_as_float(w[j] << 16), v[2 * j]),
-                                                        __fadd_rn(__uint_as_float(w[j] & 0xffff0000u), v[2 * j + 1]))
-                                                : pack2(v[2 * j], v[2 * j + 1]);
-                        stage32(staging + lane * kPitch + 2 * c0, w);
-                    }
-                    rows_sync(quarter);
-                    staged_out(staging, out + c, q.n, rows, wide);
-                    rows_sync(quarter);
+                if (STAGED) {
+                    __syncwarp();
+                    staged_out(staging, out, q.n, rows, wide);
+                    __syncwarp();
                 }
-                if (some)
-                    release();
             }
         }
         // after a wait that gave up: NaN in everything that could not be computed
@@ -930,7 +895,7 @@ template <int EPI> __device__ __forceinline__ Unit few_unit_at(const ExpertParam
     return u;
 }
 
-template <int EPI> __global__ void __launch_bounds__(kFewThreads, 1) expert_few_kernel(const __grid_constant__ ExpertParams p)
+template <int EPI> __global__ void __launch_bounds__(kPairThreads, 1) expert_few_kernel(const __grid_constant__ ExpertParams p)
 {
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t bars[2 * kFewStages + 4];
@@ -1296,7 +1261,12 @@ uint32_t tiles_of(uint64_t n, uint32_t t) { return (uint32_t)((n + t - 1) / t); 
 
 constexpr uint64_t kMaxRows = 0x7fff0000, kMaxWidth = 1 << 24;
 constexpr uint32_t kMaxSplits = 16;
-// Up to so many rows an expert, on average, the weights are the accumulator's rows.
+// Rows an expert, on average, up to which a forward pass has the weights as the
+// accumulator's rows (expert_few_kernel).  Forward in us, so and on pairs: eight
+// experts of 4096 x 11008 with 16 rows each 333 and 362, with 64 372 and 371, with
+// 96 459 and 392; one of 4096 x 4096 with 64 36.5 and 47.4; three of 2048 x 2816
+// with 32 34.5 and 35.1; 32 of 512 x 1376 with 16 37.8 and 35.4, with 64 47.6 and
+// 36.8.
 constexpr uint64_t kFewRows = 64;
 
 // Parts that the sum over K is cut into, in expert_few_kernel: as ffn.cu's rule,
@@ -1386,11 +1356,11 @@ bool make_plan(size_t r, size_t e, size_t d, size_t f, bool backward, bool align
     return true;
 }
 
-cudaLaunchConfig_t pair_launch(cudaLaunchAttribute *attr, unsigned pairs, unsigned threads, cudaStream_t stream)
+cudaLaunchConfig_t pair_launch(cudaLaunchAttribute *attr, unsigned pairs, bool chained, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs);
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = dim3(kPairThreads);
     cfg.dynamicSmemBytes = kGemmSmem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1399,20 +1369,20 @@ cudaLaunchConfig_t pair_launch(cudaLaunchAttribute *attr, unsigned pairs, unsign
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = chained ? 2 : 1;
     return cfg;
 }
 
 // units: the most that the launch can have.
-template <int EPI, bool A_MN, bool B_MN, int WARPS = kDirect> cudaError_t launch_gemm(const ExpertParams &p, uint64_t units, cudaStream_t stream)
+template <int EPI, bool A_MN, bool B_MN, bool STAGED = false> cudaError_t launch_gemm(const ExpertParams &p, uint64_t units, cudaStream_t stream)
 {
     static std::atomic<unsigned long long> ready{0};
-    cudaError_t e = large_smem_once(reinterpret_cast<const void *>(expert_gemm_kernel<EPI, A_MN, B_MN, WARPS>), kGemmSmem, ready);
+    cudaError_t e = large_smem_once(reinterpret_cast<const void *>(expert_gemm_kernel<EPI, A_MN, B_MN, STAGED>), kGemmSmem, ready);
     if (e != cudaSuccess)
         return e;
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = pair_launch(attr, (unsigned)std::max<uint64_t>(1, std::min<uint64_t>(units, kPairs)), 128 + 32 * WARPS, stream);
-    if ((e = cudaLaunchKernelEx(&cfg, expert_gemm_kernel<EPI, A_MN, B_MN, WARPS>, p)) == cudaSuccess)
+    const cudaLaunchConfig_t cfg = pair_launch(attr, (unsigned)std::max<uint64_t>(1, std::min<uint64_t>(units, kPairs)), !STAGED, stream);
+    if ((e = cudaLaunchKernelEx(&cfg, expert_gemm_kernel<EPI, A_MN, B_MN, STAGED>, p)) == cudaSuccess)
         count_launches(1);
     return e;
 }
@@ -1421,7 +1391,7 @@ template <int EPI, bool A_MN, bool B_MN, int WARPS = kDirect> cudaError_t launch
 // written directly.
 template <int EPI, bool A_MN, bool B_MN> cudaError_t launch_out(const ExpertParams &p, bool vectors, uint64_t units, cudaStream_t stream)
 {
-    return vectors ? launch_gemm<EPI, A_MN, B_MN, kDirect>(p, units, stream) : launch_gemm<EPI, A_MN, B_MN, kStaged>(p, units, stream);
+    return vectors ? launch_gemm<EPI, A_MN, B_MN, false>(p, units, stream) : launch_gemm<EPI, A_MN, B_MN, true>(p, units, stream);
 }
 
 template <int EPI> cudaError_t launch_few(ExpertParams &p, uint64_t tiles, cudaStream_t stream)
@@ -1435,7 +1405,7 @@ template <int EPI> cudaError_t launch_few(ExpertParams &p, uint64_t tiles, cudaS
     const uint64_t units = tiles * p.prob[0].nt * p.splits;
     if (units > 0x3fffffff)
         return cudaErrorInvalidValue;
-    if ((e = launch_chained(expert_few_kernel<EPI>, dim3((unsigned)std::min<uint64_t>(units, kSms)), dim3(kFewThreads), smem, stream, p)) != cudaSuccess)
+    if ((e = launch_chained(expert_few_kernel<EPI>, dim3((unsigned)std::min<uint64_t>(units, kSms)), dim3(kPairThreads), smem, stream, p)) != cudaSuccess)
         return e;
     count_launches(1);
     if (p.splits > 1) {
@@ -1605,7 +1575,6 @@ ccl_status_t expert_ffn_impl(const ExpertArgs &a, void *out, cudaStream_t stream
         return CCL_ERR_CUDA;
     if (cudaError_t e = launch_gemm<EPI_GATED, false, false>(p, tiles * q.nt, stream))
         return from_cuda(e);
-    p.early = 1;
     const bool vectors = a.d % 8 == 0 && (uintptr_t)out % 16 == 0;
     p.half = half_tile(likely, a.d, tiles_of(a.f, kTileK), vectors ? 2.5 : 4.0);
     set_problem(q, a.d, 2 * p.half, a.f, 1);
@@ -1697,7 +1666,6 @@ ccl_status_t expert_ffn_grad_impl(const ExpertArgs &a, const void *dy, void *dx,
     p.half = half_tile(likely, a.f, tiles_of(a.d, kTileK), 7.0);
     set_problem(q, a.f, 2 * p.half, a.d, 1);
     p.padded = !direct_y;
-    p.early = 1;
     if (!encode_rows(&q.a[0], direct_y ? ly : y, false) || !encode_experts(&q.b[0], wd, a.e, true))
         return CCL_ERR_CUDA;
     if ((e = launch_gemm<EPI_BACKWARD, false, true>(p, tiles * q.nt, stream)))

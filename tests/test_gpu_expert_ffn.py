@@ -141,10 +141,11 @@ def check_backward(a, got, saved, act, x8=None, old=None):
 
 
 # rows of each expert, dim, ffn.  One row; experts without rows; ragged tiles; more rows than a tile; odd widths; both kernels of the forward pass
-# (an average of 64 rows lies between them), with and without sums cut along K
+# (an average of 64 rows lies between them), with and without sums cut along K, several tiles of few tokens, and large weights
 CASES = [([1], 8, 8), ([2], 64, 128), ([0, 1, 0, 1], 512, 1024), ([3, 0, 5, 1], 200, 72), ([7, 130, 0, 33], 136, 264), ([64, 64], 64, 32), ([63, 65, 1, 128], 96, 160),
          ([200], 264, 1032), ([257, 0, 300, 511], 256, 512), ([5, 4], 37, 41), ([100, 301, 0], 129, 255), ([1, 2, 3, 4, 5, 6, 7, 8], 1001, 333), ([1] * 40, 72, 136),
-         ([1000, 24], 512, 776), ([300, 700], 1536, 1000), ([16, 16, 200], 768, 1088), ([0, 0, 520], 1, 1)]
+         ([1000, 24], 512, 776), ([300, 700], 1536, 1000), ([16, 16, 200], 768, 1088), ([0, 0, 520], 1, 1),
+         ([100] + [1] * 39, 72, 136), ([50, 70], 2048, 8192), ([30, 33], 2048, 8191)]
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
