@@ -497,8 +497,8 @@ ccl_status_t ccl_gated_ffn_grad(const void *grad_out, const void *x, const void 
  * enough for ccl_gated_ffn of the same sizes. */
 ccl_status_t ccl_plan_gated_ffn_work_bytes(size_t ntokens, size_t dim, size_t ffn, int backward, int aligned, size_t *bytes);
 
-/* How often a wait of a gated feed-forward kernel on the current device for
- * its own copies or products ran out: 0 on a sound machine.  What such a kernel
+/* How often a wait of a gated feed-forward kernel (ccl_expert_ffn's too) on the
+ * current device for its own copies or products ran out: 0 on a sound machine.  What such a kernel
  * could not compute it writes as NaN, and so is every output that depends on
  * it.  Waits for the device. */
 ccl_status_t ccl_gated_ffn_timeouts(unsigned long long *count);

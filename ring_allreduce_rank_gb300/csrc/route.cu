@@ -582,6 +582,8 @@ ccl_status_t route_impl(const void *logits, size_t ntokens, size_t experts, size
     if (!valid_dtype(dtype) || !plan_route(ntokens, experts, &pl) || stride < experts || top == 0 || top > experts || top > CCL_MAX_EXPERT_TOP ||
         !extent(ntokens, experts, stride, elem_size(dtype), &lb))
         return CCL_ERR_INVALID_ARG;
+    if (ntokens * top > kMaxTokens) // choices are counted in 32 bits
+        return CCL_ERR_INVALID_ARG;
     if (!counts || !load || !importance || !loss || (ntokens && (!logits || !lse || !ids || !weights)) ||
         !element_aligned(elem_size(dtype), {logits}) || !element_aligned(4, {ids, weights, lse, counts, load, importance, loss}) ||
         (pl.bytes && (!work || (uintptr_t)work % 256 || work_bytes < pl.bytes)))
@@ -639,6 +641,8 @@ ccl_status_t route_grad_impl(const void *logits, size_t ntokens, size_t experts,
     if (!valid_dtype(dtype) || !plan_route(ntokens, experts, &pl) || stride < experts || grad_stride < experts || top == 0 || top > experts ||
         top > CCL_MAX_EXPERT_TOP || !extent(ntokens, experts, stride, es, &lb) || !extent(ntokens, experts, grad_stride, es, &gb) ||
         balance != balance || z != z)
+        return CCL_ERR_INVALID_ARG;
+    if (ntokens * top > kMaxTokens)
         return CCL_ERR_INVALID_ARG;
     if (ntokens == 0)
         return CCL_OK;

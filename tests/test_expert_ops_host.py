@@ -74,12 +74,12 @@ def _ffn_grad(L, dy=1 * T40, x=2 * T40, xc=None, xsc=None, off=3 * T40, wg=4 * T
 def refusals(L):
     for kw in (dict(dt=2), dict(zs=7), dict(e=0, zs=0), dict(e=1025, zs=1025), dict(top=0), dict(top=9), dict(e=64, zs=64, top=33), dict(n=1 << 31), dict(z=None),
                dict(ids=None), dict(w=None), dict(lse=None), dict(counts=None), dict(load=None), dict(imp=None), dict(loss=None), dict(work=None), dict(nbytes=0),
-               dict(work=9 * T40 + 16), dict(z=T40 + 2), dict(ids=2 * T40 + 2), dict(zs=1 << 62)):
+               dict(work=9 * T40 + 16), dict(z=T40 + 2), dict(ids=2 * T40 + 2), dict(zs=1 << 62), dict(n=1 << 30, nbytes=1 << 40)):
         assert _route(L, **kw) == INVALID, kw
     for kw in (dict(ids=T40 + 8), dict(load=6 * T40 + 4, imp=6 * T40), dict(lse=3 * T40), dict(valid=4 * T40), dict(work=5 * T40)):
         assert _route(L, **kw) == OVERLAP, kw
     for kw in (dict(dt=2), dict(zs=7), dict(gs=7), dict(top=0), dict(top=9), dict(b=NAN), dict(c=NAN), dict(z=None), dict(ids=None), dict(lse=None), dict(counts=None),
-               dict(load=None), dict(gw=None), dict(grad=None), dict(grad=9 * T40 + 1), dict(e=2000, zs=2000, gs=2000)):
+               dict(load=None), dict(gw=None), dict(grad=None), dict(grad=9 * T40 + 1), dict(e=2000, zs=2000, gs=2000), dict(n=1 << 30)):
         assert _route_grad(L, **kw) == INVALID, kw
     for kw in (dict(grad=T40 + 32), dict(grad=T40, gs=9), dict(grad=2 * T40), dict(grad=6 * T40)):
         assert _route_grad(L, **kw) == OVERLAP, kw
