@@ -1,7 +1,7 @@
 """The expert-parallel operators' tests again against the bounds-checking debug
 build: every global load and store of their kernels stays inside the call's own
 buffers (the tensor-memory copies of the feed-forward blocks, which the checks
-does not see, are bounded by their tensor maps)."""
+do not see, are bounded by their tensor maps)."""
 import os
 import subprocess
 import sys
