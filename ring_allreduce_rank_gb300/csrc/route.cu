@@ -33,10 +33,16 @@ namespace {
 constexpr int kJoinCtas = 8; // one portable cluster
 constexpr size_t kMaxTokens = 0x7fffffff;
 constexpr int kRouteThreads = 256; // route_grad_kernel's
+constexpr size_t kSms = 152;
 // route_kernel's, at most: one CTA an SM with eight or sixteen values a lane, so
 // that 152 rows of partial sums are left; two with 32.  Lanes take 64 to 128
-// registers.
+// registers.  (16384 tokens, forward: 256 experts 22.9 us, with 608 CTAs of 256
+// threads 26.1; 64 experts 9.0 and 9.5; 4096 x 512 15.2 and 19.8.)  Fewer tokens
+// are spread over CTAs of 256 (50 x 256 in one CTA of 1024, two rounds, 11.0 us,
+// in seven and a join 6.7; 256 x 64 9.4 and 6.4), but those that one CTA takes at
+// once stay in it (128 x 64 5.4 us, spread 6.1).
 constexpr int route_threads(int values) { return values <= 8 ? 1024 : values <= 16 ? 512 : 256; }
+constexpr size_t kFewRouteThreads = 256;
 
 struct RouteParams {
     const char *logits;
@@ -530,11 +536,16 @@ bool plan_route(size_t ntokens, size_t experts, RoutePlan *p)
     if (ntokens > kMaxTokens || experts == 0 || experts > CCL_MAX_EXPERTS)
         return false;
     *p = RoutePlan{};
-    p->lanes = experts <= 64 ? 8 : 32;
-    const size_t most = route_threads(experts <= 256 ? 8 : experts <= 512 ? 16 : 32), groups = most / p->lanes, all = (ntokens + groups - 1) / groups;
-    // one CTA for two rounds of rows: it needs no second launch
-    p->ctas = all <= 2 ? 1 : (uint32_t)std::min<size_t>(all, experts <= 512 ? 152 : 304);
-    p->threads = (uint32_t)std::min<size_t>(most, std::max<size_t>(ntokens * p->lanes + 31, 32) / 32 * 32);
+    p->lanes = experts <= 64 ? 8 : 32; // 16384 x 64: 8 lanes 9.0 us, 32 lanes 12.1
+    const size_t most = route_threads(experts <= 256 ? 8 : experts <= 512 ? 16 : 32);
+    if (ntokens * p->lanes <= most) { // one CTA, which needs no second launch
+        p->ctas = 1;
+        p->threads = (uint32_t)std::max<size_t>(ntokens * p->lanes + 31, 32) / 32 * 32;
+    } else {
+        const size_t rows = kFewRouteThreads / p->lanes; // that the smallest CTA takes at a time
+        p->ctas = (uint32_t)std::min<size_t>((ntokens + rows - 1) / rows, experts <= 512 ? kSms : 2 * kSms);
+        p->threads = (uint32_t)std::min(most, std::max(kFewRouteThreads, ((ntokens + p->ctas - 1) / p->ctas * p->lanes + 31) / 32 * 32));
+    }
     if (p->ctas > 1) {
         p->sums = up(p->ctas * (experts + 1) * 4);
         p->bytes = p->sums + up(p->ctas * (experts + 2) * 4);

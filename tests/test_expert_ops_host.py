@@ -148,7 +148,7 @@ def test_c_entries_refuse_before_launching():
 def test_plans():
     assert [ccl.ccl_plan_act8_width(c) for c in (0, 1, 32, 33, 11008)] == [0, 32, 32, 64, 11008]
     # one CTA needs no working space; several leave a row of sums each
-    assert ccl.ccl_plan_route_work_bytes(8, 256) == 0 and ccl.ccl_plan_route_work_bytes(256, 64) == 0
+    assert ccl.ccl_plan_route_work_bytes(8, 256) == 0 and ccl.ccl_plan_route_work_bytes(128, 64) == 0
     assert ccl.ccl_plan_route_work_bytes(1 << 20, 256) == -(-152 * 257 * 4 // 256) * 256 + -(-152 * 258 * 4 // 256) * 256
     assert ccl.ccl_plan_expert_order_work_bytes(2048, 8, 64) == 0
     assert ccl.ccl_plan_expert_order_work_bytes(65537, 1, 64) == 64 * 1025 * 4 + 256  # 1025 runs of 64
