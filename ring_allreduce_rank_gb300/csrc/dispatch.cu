@@ -16,7 +16,10 @@
 // w grad_out[t], grad_w = <grad_out[t], rows[place]>, in one pass over a
 // token's rows.  All three are bound by memory bandwidth; a group of threads
 // takes a token, each 32-byte vector (16 where a row is no multiple of it) of
-// its rows with every row's load in flight before the first sum.
+// its rows with every row's load in flight before the first sum.  8192 tokens of
+// 7168 bf16, 4 choices: dispatch 84.7 us (6.9 TB/s; in 16-byte vectors 87.0, in
+// elements 91.6), combine 82.0 (7.2 TB/s; 86.6, 230.6), its gradients 148.6 (7.1
+// TB/s; 151.6, 217.1).
 #include <cooperative_groups.h>
 
 #include <vector>
