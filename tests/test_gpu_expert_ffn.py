@@ -245,6 +245,19 @@ def test_accumulates_and_skips_gradients():
             assert torch.equal(one[k], got[name])
 
 
+@pytest.mark.parametrize("counts,D,F,lead", [([90, 0, 33], 37, 41, 0), ([600, 0, 1], 129, 255, 0), ([65, 0, 130], 301, 96, 1), ([40, 0, 70], 264, 129, 0),
+                                             ([10, 0, 300], 136, 264, 3), ([80, 0, 5], 1, 1, 0)])
+def test_accumulates_in_odd_rows(counts, D, F, lead):
+    a = inputs(counts, D, F, 8, lead=lead)
+    saved = saved_of(a["x"].shape[0], F)
+    forward(a, saved=saved)
+    old = {"d" + k: torch.randn(a[k].shape, device=DEV).to(BF16) for k in ("wg", "wu", "wd")}
+    more = backward(a, saved, old=old)
+    check_backward(a, more, saved, "silu", old=old)
+    for k in old:
+        assert torch.equal(more[k][1], old[k][1])  # an expert without rows
+
+
 def test_no_rows():
     e = lambda *s: torch.empty(*s, dtype=BF16, device=DEV)  # noqa: E731
     o = torch.zeros(4, device=DEV, dtype=I32)
