@@ -50,7 +50,7 @@ constexpr int kTileM = 256, kTileN = 256, kTileK = 64; // a CTA pair's tile
 constexpr int kOperandBytes = 128 * kTileK * 2;        // one CTA's part of A or B in a stage
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kStages = 6, kStagedStages = 4; // the latter beside the room that outputs are staged in
-constexpr int kEpiWarps = 8, kPairThreads = 128 + 32 * kEpiWarps; // beside them: producer, issuer, tensor memory, an idle warp
+constexpr int kEpiWarps = 8, kFewThreads = 128 + 32 * kEpiWarps; // expert_few_kernel's: beside them producer, issuer, tensor memory, an idle warp
 // Staging: 32 rows of 128 bf16 columns for each of the epilogue warps.  The
 // pitch puts eight rows' 16 bytes in different banks.
 constexpr uint32_t kPitch = 272, kStaging = 32 * kPitch;
@@ -63,6 +63,12 @@ constexpr int kFewBytes = 190 * 1024; // its stages', at most
 constexpr uint32_t kFewMost = 128;    // tokens of one tile
 
 enum Epilogue { EPI_GATED = 0, EPI_STORE = 1, EPI_BACKWARD = 2, EPI_WEIGHTS = 3 };
+// Epilogue warps of expert_gemm_kernel.  dh's epilogue has the most to do: over a
+// short K twelve are faster (the gradient by 4000 rows of 320, ffn 2944: 66.3 us
+// with eight, 63.9), over a long one equal (435).  The others' hide behind their
+// products, which sixteen slowed down by 5 %.
+template <int EPI> constexpr int kWarpsOf = EPI == EPI_BACKWARD ? 12 : kEpiWarps;
+template <int EPI> constexpr int kThreadsOf = 128 + 32 * kWarpsOf<EPI>;
 
 // An epilogue warp's lane has a row of the accumulator and writes 32 bytes of it
 // at a time.  Rows that no 16-byte vector divides are staged in shared memory
@@ -523,13 +529,13 @@ template <int EPI> __device__ __forceinline__ uint16_t *unit_out(const ExpertPar
 
 // ------------------------------------------------------------------ the product on CTA pairs
 
-// A warp loads, a lane of the pair's first CTA issues, eight warps work on the
-// accumulator before this one's.  8192 rows over 8 experts of 4096 x 11008: g, u
+// A warp loads, a lane of the pair's first CTA issues, eight or twelve warps work
+// on the accumulator before this one's.  8192 rows over 8 experts of 4096 x 11008: g, u
 // and h 908 us and y 466 (tensor pipe 89 and 91 % busy).  32768 rows over 32 of
 // 2048 x 1408: g, u, h and their 8 bits 255, y 137, dh with dg, du and h 172 (60 %:
 // its epilogue reads and writes 0.68 GB), dx 252 (84 %), weight gradients 379 (74 %).
 template <int EPI, bool A_MN, bool B_MN, bool STAGED>
-__global__ void __launch_bounds__(kPairThreads, 1) expert_gemm_kernel(const __grid_constant__ ExpertParams p)
+__global__ void __launch_bounds__(kThreadsOf<EPI>, 1) expert_gemm_kernel(const __grid_constant__ ExpertParams p)
 {
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t bars[2 * kStages + 4];
@@ -553,7 +559,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) expert_gemm_kernel(const __gr
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
-            mbar_init(acc_empty + 8 * i, 2 * kEpiWarps);
+            mbar_init(acc_empty + 8 * i, 2 * kWarpsOf<EPI>);
         }
         if ((gave_up = p.wait_ns == 0))
             atomicAdd(&g_expert_timeouts, 1ull);
@@ -664,8 +670,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) expert_gemm_kernel(const __gr
         }
     } else if (warp >= 4) {
         // epilogue: warp w reads lanes 32 (w % 4) .. + 32 and every second 32
-        // columns, or of an output one half of the columns
-        constexpr uint32_t kStride = 32 * kEpiWarps / 4;
+        // columns (EPI_BACKWARD: third), or of an output one half of the columns
+        constexpr uint32_t kStride = 32 * kWarpsOf<EPI> / 4;
         const uint32_t c0 = (warp - 4) / 4 * 32;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32;
         const uint32_t leader_empty = in_cta(acc_empty, 0);
@@ -904,7 +910,7 @@ template <int EPI> __device__ __forceinline__ Unit few_unit_at(const ExpertParam
 // accumulator.  Bound by reading the weights, each once for a tile of tokens: one
 // token by two experts of 4096 x 11008 61 us for g and u and 37 for y (5.9 and 4.9
 // TB/s).
-template <int EPI> __global__ void __launch_bounds__(kPairThreads, 1) expert_few_kernel(const __grid_constant__ ExpertParams p)
+template <int EPI> __global__ void __launch_bounds__(kFewThreads, 1) expert_few_kernel(const __grid_constant__ ExpertParams p)
 {
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t bars[2 * kFewStages + 4];
@@ -1371,11 +1377,11 @@ bool make_plan(size_t r, size_t e, size_t d, size_t f, bool backward, bool align
     return true;
 }
 
-cudaLaunchConfig_t pair_launch(cudaLaunchAttribute *attr, unsigned pairs, bool chained, cudaStream_t stream)
+cudaLaunchConfig_t pair_launch(cudaLaunchAttribute *attr, unsigned pairs, unsigned threads, bool chained, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs);
-    cfg.blockDim = dim3(kPairThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = kGemmSmem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1396,7 +1402,7 @@ template <int EPI, bool A_MN, bool B_MN, bool STAGED = false> cudaError_t launch
     if (e != cudaSuccess)
         return e;
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = pair_launch(attr, (unsigned)std::max<uint64_t>(1, std::min<uint64_t>(units, kPairs)), !STAGED, stream);
+    const cudaLaunchConfig_t cfg = pair_launch(attr, (unsigned)std::max<uint64_t>(1, std::min<uint64_t>(units, kPairs)), kThreadsOf<EPI>, !STAGED, stream);
     if ((e = cudaLaunchKernelEx(&cfg, expert_gemm_kernel<EPI, A_MN, B_MN, STAGED>, p)) == cudaSuccess)
         count_launches(1);
     return e;
@@ -1420,7 +1426,7 @@ template <int EPI> cudaError_t launch_few(ExpertParams &p, uint64_t tiles, cudaS
     const uint64_t units = tiles * p.prob[0].nt * p.splits;
     if (units > 0x3fffffff)
         return cudaErrorInvalidValue;
-    if ((e = launch_chained(expert_few_kernel<EPI>, dim3((unsigned)std::min<uint64_t>(units, kSms)), dim3(kPairThreads), smem, stream, p)) != cudaSuccess)
+    if ((e = launch_chained(expert_few_kernel<EPI>, dim3((unsigned)std::min<uint64_t>(units, kSms)), dim3(kFewThreads), smem, stream, p)) != cudaSuccess)
         return e;
     count_launches(1);
     if (p.splits > 1) {
