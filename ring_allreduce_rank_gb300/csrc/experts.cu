@@ -29,7 +29,7 @@
 //
 // Bound by the tensor cores for many rows an expert, by reading the weights (and
 // writing their gradients) for few.  Two experts of eight for each of 4096
-// tokens at 4096 x 11008, forward: 1.31-1.37 ms, at the power limit 1.45-1.53
+// tokens at 4096 x 11008, forward: 1.31-1.37 ms, at the power limit 1.45-1.55
 // (1.45-1.69 PFLOP/s; cuBLAS sustains 1.72 there), an eighth of the products
 // being of row tiles that an expert does not fill; the same for one token 94 us
 // (5.7 TB/s of weights, 0.85 of the copy bandwidth).  Forward and backward of
