@@ -538,10 +538,14 @@ bool plan_order(size_t ntokens, size_t top, size_t experts, OrderPlan *p)
         return true;
     }
     // a run a warp, eight of them on every SM, but no fewer choices than experts whose counts it writes
-    p->run = std::max<uint32_t>((uint32_t)(((size_t)p->n + 8 * 152 - 1) / (8 * 152)), (uint32_t)std::max<size_t>(experts, 64));
-    p->run = (p->run + 31) / 32 * 32;
+    constexpr size_t most = 8 * 152;
+    const uint32_t least = (uint32_t)((std::max<size_t>(experts, 64) + 31) / 32 * 32);
+    p->run = std::max(least, (uint32_t)((p->n + most - 1) / most + 31) / 32 * 32);
     p->runs = (p->n + p->run - 1) / p->run;
-    p->counts = up((size_t)experts * p->runs * 4);
+    // room for the most runs that so many choices or fewer are cut into: the
+    // length's steps of 32 make runs fewer again as the choices grow, and a buffer
+    // serves every call that is smaller than the one it was planned for
+    p->counts = up(experts * std::min(most, ((size_t)p->n + least - 1) / least) * 4);
     p->bytes = p->counts + up(experts * 4);
     return true;
 }
