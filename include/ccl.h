@@ -454,8 +454,9 @@ ccl_status_t ccl_embedding(const void *table, size_t rows, size_t dim, size_t ta
  * row (zeros where no token names it); accumulate != 0 adds to the rows that
  * a token names and leaves the others untouched (a tied output projection's
  * gradient, a further micro-batch).  work: device memory of
- * ccl_plan_embedding_grad_work_bytes bytes, 16-byte aligned, not shared with
- * a concurrent call; its contents need no initialisation.  Launches: the zero
+ * ccl_plan_embedding_grad_work_bytes bytes (fewer tokens may need more: for
+ * several batch sizes the largest of their plans), 16-byte aligned, not shared
+ * with a concurrent call; its contents need no initialisation.  Launches: the zero
  * rows (accumulate = 0), the sort (one launch for both up to 4096 tokens), the
  * sums, and the join when the tokens fill more than one run (of 8 to 32). */
 ccl_status_t ccl_embedding_grad(const void *grad_out, size_t grad_out_stride, const int64_t *ids, size_t ntokens,
@@ -494,7 +495,9 @@ ccl_status_t ccl_gated_ffn_grad(const void *grad_out, const void *x, const void 
  * aligned (else, or where a width is no multiple of 8, room for padded copies
  * of the inputs is included: the copy engine that feeds the tensor cores
  * addresses whole 16-byte vectors).  backward != 0: for ccl_gated_ffn_grad, and
- * enough for ccl_gated_ffn of the same sizes. */
+ * enough for ccl_gated_ffn of the same sizes.  Fewer tokens may need more bytes
+ * (their sums are cut into more parts): a buffer for several batch sizes has the
+ * largest of their plans. */
 ccl_status_t ccl_plan_gated_ffn_work_bytes(size_t ntokens, size_t dim, size_t ffn, int backward, int aligned, size_t *bytes);
 
 /* How often a wait of a gated feed-forward kernel (ccl_expert_ffn's too) on the
@@ -566,7 +569,7 @@ ccl_status_t ccl_distill_grad(const void *logits, size_t nrows, size_t vocab, si
  * counts nowhere.  A NaN or +inf makes its token's weights NaN (the ids stay in
  * range, NaN being the largest).  work: ccl_plan_route_work_bytes bytes, 256-byte
  * aligned, not shared with a concurrent call, contents irrelevant (0 bytes for
- * few tokens).  One launch, or two. */
+ * few tokens, and never fewer for more).  One launch, or two. */
 ccl_status_t ccl_route(const void *logits, size_t ntokens, size_t experts, size_t logits_stride, ccl_dtype_t dtype,
                        const uint8_t *valid, size_t top, int normalize, int32_t *ids, float *weights, float *lse,
                        int32_t *counts, float *load, float *importance, float *losses, void *work, size_t work_bytes,
@@ -591,8 +594,9 @@ ccl_status_t ccl_route_grad(const void *logits, size_t ntokens, size_t experts, 
  * choice, rows being ordered by expert, then token, then choice; expert
  * first_expert + e has rows [offsets[e], offsets[e + 1]), offsets[0] = 0.  An id outside [first_expert, first_expert + experts)
  * (-1, or an expert of another rank) has place -1.  work:
- * ccl_plan_expert_order_work_bytes bytes, 256-byte aligned, not shared with a
- * concurrent call (0 bytes up to 16384 choices).  One launch, or three. */
+ * ccl_plan_expert_order_work_bytes bytes (0 up to 16384 choices, and never fewer
+ * for more tokens), 256-byte aligned, not shared with a concurrent call.  One
+ * launch, or three. */
 ccl_status_t ccl_expert_order(const int32_t *ids, size_t ntokens, size_t top, int32_t first_expert, size_t experts,
                               int32_t *offsets, int32_t *place, void *work, size_t work_bytes, cudaStream_t stream);
 ccl_status_t ccl_plan_expert_order_work_bytes(size_t ntokens, size_t top, size_t experts, size_t *bytes);
@@ -672,7 +676,13 @@ ccl_status_t ccl_expert_ffn_grad(const void *grad_out, const void *x, const int8
                                  void *grad_w_gate, void *grad_w_up, void *grad_w_down, void *work, size_t work_bytes,
                                  cudaStream_t stream);
 
-/* Bytes of the work buffer; aligned and backward as for ccl_plan_gated_ffn_work_bytes. */
+/* Bytes of the work buffer; aligned and backward as for ccl_plan_gated_ffn_work_bytes.
+ * A buffer planned for more rows, everything else being equal, serves fewer too,
+ * although few rows may plan more bytes than many: ccl_expert_ffn then cuts its
+ * sums into the parts that fit, in another order, so with other roundings, and up
+ * to twice as slow (64 rows of one expert of 4096 x 4096 in the 0.5 MB of 65 rows
+ * 67 us, in their own 6.8 MB 36).  The largest of the plans of the batches that
+ * occur keeps every one at its speed and bits. */
 ccl_status_t ccl_plan_expert_ffn_work_bytes(size_t nrows, size_t experts, size_t dim, size_t ffn, int backward,
                                             int aligned, size_t *bytes);
 

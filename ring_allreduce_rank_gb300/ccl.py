@@ -969,8 +969,8 @@ def ccl_expert_ffn(x: torch.Tensor, offsets: torch.Tensor, w_gate: torch.Tensor,
     ([experts, dim, ffn]), bfloat16.  offsets ([experts + 1], int32) stays on the
     device.  saved: (codes [2, rows, ccl_plan_act8_width(ffn)] int8, scales [2,
     rows, width / 32] uint8), g and u kept in 8 bits for ccl_expert_ffn_grad.
-    work: a device buffer of at least ccl_plan_expert_ffn_work_bytes bytes
-    (allocated here when omitted)."""
+    work: a device buffer of at least ccl_plan_expert_ffn_work_bytes bytes for
+    these rows or for more (allocated here when omitted)."""
     codes, scales = saved if saved is not None else (None, None)
     dev = _on_gpu(x, offsets, w_gate, w_up, w_down, out, codes, scales, work)
     if dev != _current_device():

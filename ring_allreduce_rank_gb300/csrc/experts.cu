@@ -1291,11 +1291,12 @@ constexpr uint64_t kFewRows = 64;
 // take) and the join; tiles: those of the experts that can have rows.  One token
 // by two experts of 4096 x 11008 94 us, without cuts 154; 64 rows over four of
 // 2048 x 2816 39.0 and 45.5.
-uint32_t choose_splits(uint64_t tiles, uint64_t kblocks, uint64_t partial_bytes)
+// The parts' sums have to fit into `room` bytes.
+uint32_t choose_splits(uint64_t tiles, uint64_t kblocks, uint64_t partial_bytes, size_t room)
 {
     uint32_t best = 1;
     double cost = 0;
-    for (uint32_t s = 1; s <= kMaxSplits && s <= kblocks; ++s) {
+    for (uint32_t s = 1; s <= kMaxSplits && s <= kblocks && (s == 1 || s * partial_bytes <= room); ++s) {
         const double rounds = (double)((tiles * s + kSms - 1) / kSms);
         const double block = std::max(0.5, 0.005 * (double)std::min<uint64_t>(kSms, tiles * s));
         const double products = (double)kblocks / s * block;
@@ -1316,7 +1317,10 @@ struct ExpertPlan {
     size_t h, dg, du, x, y, wg, wu, wd, partial, bytes;
 };
 
-bool make_plan(size_t r, size_t e, size_t d, size_t f, bool backward, bool aligned, ExpertPlan *p)
+// room: the bytes that there are.  The sums over K are the only part of the buffer
+// that fewer bytes can do with: fewer rows have more parts, and a buffer that was
+// planned for a larger batch serves them with the parts that fit.
+bool make_plan(size_t r, size_t e, size_t d, size_t f, bool backward, bool aligned, size_t room, ExpertPlan *p)
 {
     if (r > kMaxRows || e > CCL_MAX_EXPERTS || d > kMaxWidth || f > kMaxWidth || r * std::max(d, f) > (1ull << 44) ||
         (uint64_t)d * f > (1ull << 38) /* an expert's stride in its tensor map */ || (uint64_t)e * d * f > (1ull << 44))
@@ -1369,8 +1373,9 @@ bool make_plan(size_t r, size_t e, size_t d, size_t f, bool backward, bool align
         p->npad = std::max(p->npad, 16u);
         const uint64_t tiles = std::max<uint64_t>(active, r / p->npad);
         const size_t up_bytes = r * (size_t)tiles_of(f, 128) * kTileN * 4, down_bytes = r * (size_t)tiles_of(d, kTileN) * kTileN * 4;
-        p->up_splits = choose_splits(tiles * tiles_of(f, 128), tiles_of(d, kTileK), up_bytes);
-        p->down_splits = choose_splits(tiles * tiles_of(d, kTileN), tiles_of(f, kTileK), down_bytes);
+        room = room > at ? (room - at) / kAlign * kAlign : 0;
+        p->up_splits = choose_splits(tiles * tiles_of(f, 128), tiles_of(d, kTileK), up_bytes, room);
+        p->down_splits = choose_splits(tiles * tiles_of(d, kTileN), tiles_of(f, kTileK), down_bytes, room);
         p->partial = take(std::max(p->up_splits > 1 ? p->up_splits * up_bytes : 0, p->down_splits > 1 ? p->down_splits * down_bytes : 0));
     }
     p->bytes = at;
@@ -1467,7 +1472,7 @@ ccl_status_t check_experts(const ExpertArgs &a, bool backward, bool aligned, Exp
         return CCL_ERR_INVALID_ARG;
     if (a.dtype != CCL_BF16)
         return CCL_ERR_UNSUPPORTED;
-    if (a.f == 0 || !make_plan(a.r, a.e, a.d, a.f, backward, aligned, plan))
+    if (a.f == 0 || !make_plan(a.r, a.e, a.d, a.f, backward, aligned, a.work_bytes, plan))
         return CCL_ERR_INVALID_ARG;
     return CCL_OK;
 }
@@ -1754,7 +1759,8 @@ extern "C" {
 ccl_status_t ccl_plan_expert_ffn_work_bytes(size_t nrows, size_t experts, size_t dim, size_t ffn, int backward, int aligned, size_t *bytes)
 {
     ExpertPlan f, b;
-    if (!bytes || ffn == 0 || !make_plan(nrows, experts, dim, ffn, false, aligned != 0, &f) || !make_plan(nrows, experts, dim, ffn, true, aligned != 0, &b))
+    if (!bytes || ffn == 0 || !make_plan(nrows, experts, dim, ffn, false, aligned != 0, SIZE_MAX, &f) ||
+        !make_plan(nrows, experts, dim, ffn, true, aligned != 0, SIZE_MAX, &b))
         return CCL_ERR_INVALID_ARG;
     *bytes = backward ? std::max(f.bytes, b.bytes) : f.bytes; // a backward pass's buffer serves the forward too
     return CCL_OK;
