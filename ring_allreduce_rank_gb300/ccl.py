@@ -921,6 +921,15 @@ def ccl_combine_grad(grad_out: torch.Tensor, place: torch.Tensor, rows: Optional
            "ccl_combine_grad")
 
 
+def _pair(pair, name: str):
+    """The tensors of a (codes, scales), or None twice."""
+    if pair is None:
+        return None, None
+    if isinstance(pair, torch.Tensor) or len(pair) != 2:
+        raise ValueError("%s must be (codes, scales)" % name)
+    return pair
+
+
 def _act8(pair, name: str, lead, cols: int):
     """Pointers of (codes, scales) of rows of `cols` values."""
     codes, scales = pair
@@ -971,7 +980,7 @@ def ccl_expert_ffn(x: torch.Tensor, offsets: torch.Tensor, w_gate: torch.Tensor,
     rows, width / 32] uint8), g and u kept in 8 bits for ccl_expert_ffn_grad.
     work: a device buffer of at least ccl_plan_expert_ffn_work_bytes bytes for
     these rows or for more (allocated here when omitted)."""
-    codes, scales = saved if saved is not None else (None, None)
+    codes, scales = _pair(saved, "saved")
     dev = _on_gpu(x, offsets, w_gate, w_up, w_down, out, codes, scales, work)
     if dev != _current_device():
         with torch.cuda.device(dev):
@@ -992,10 +1001,15 @@ def ccl_expert_ffn_grad(grad_out: torch.Tensor, x, offsets: torch.Tensor, w_gate
                         grad_w_down: Optional[torch.Tensor] = None, act="silu", accumulate: bool = False,
                         work: Optional[torch.Tensor] = None, stream=None) -> None:
     """The blocks' gradients (those given), from the saved pre-activations and
-    x: the tensor, or (codes, scales) as ccl_act8_pack keeps it; accumulate adds
-    to the weights' gradients."""
-    eight = not isinstance(x, torch.Tensor)
-    dev = _on_gpu(grad_out, *(x if eight else (x,)), offsets, w_gate, w_up, w_down, *saved, grad_x, grad_w_gate, grad_w_up,
+    x: the tensor, or (codes, scales) as ccl_act8_pack keeps it (None will do
+    where neither grad_w_gate nor grad_w_up is asked for); accumulate adds to
+    the weights' gradients."""
+    if saved is None:
+        raise ValueError("saved is needed: (codes, scales) as ccl_expert_ffn left it")
+    if x is None and (grad_w_gate is not None or grad_w_up is not None):
+        raise ValueError("x is needed for grad_w_gate and grad_w_up")
+    eight = x is not None and not isinstance(x, torch.Tensor)
+    dev = _on_gpu(grad_out, *(_pair(x, "x") if eight else (x,)), offsets, w_gate, w_up, w_down, *_pair(saved, "saved"), grad_x, grad_w_gate, grad_w_up,
                   grad_w_down, work)
     if dev != _current_device():
         with torch.cuda.device(dev):
