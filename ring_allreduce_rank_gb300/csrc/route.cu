@@ -422,9 +422,11 @@ __global__ void __cluster_dims__(kJoinCtas) __launch_bounds__(1024) route_join_k
 // us, single elements 65, with exp(z - lse) for p).  More rows' loads in flight
 // (the row's before its ids are there) gained nothing.  p is made as the forward
 // pass makes it, exp(z - m) over its sum: exp(z - lse) carries the rounding of
-// lse, |lse| 2^-24 of p, and is 1 for every expert of a row of -1e9.  The maximum
-// and the sum cost a tenth where the rows are many (calls in a graph: 131072 x 256
-// bf16 62.3 -> 68.7 us, 131072 x 64 25.9 -> 26.8, 16384 x 256 fp32 10.5 -> 10.5).
+// lse, |lse| 2^-24 of p, and is 1 for every expert of a row of -1e9.  The sums of
+// a row are reduced side by side (calls in a graph, with exp(z - lse), with the
+// maximum and the sums one after another, and as it is: 131072 x 256 bf16 62.3,
+// 68.7, 66.8 us; 131072 x 64 25.9, 26.8, 24.7; 16384 x 256 fp32 10.4, 10.5, 10.2;
+// 8 x 64 2.5, 2.5, 2.4).
 template <int DT, int L, int V, int N> __global__ void __launch_bounds__(kRouteThreads) route_grad_kernel(const __grid_constant__ RouteParams p)
 {
     chain_entry();
@@ -474,40 +476,41 @@ template <int DT, int L, int V, int N> __global__ void __launch_bounds__(kRouteT
             best = fmaxf(best, f[i]); // a NaN makes the sum one
         const uint32_t most = group_max<L>(ordered(best));
         const float m = most > kNothing ? from_ordered(most) : 0.0f;
-        float total = 0.0f;
+        // the row's sums side by side, of exp(z - m): of all, with the balance
+        // loss's pull, of the chosen, with their weights' gradients
+        float total = 0.0f, pulled = 0.0f, kept = 0.0f, gw = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             f[i] = exp_of(__fsub_rn(f[i], m));
             total = __fadd_rn(total, f[i]);
+            pulled = __fmaf_rn(own[i], f[i], pulled);
         }
-        total = group_sum<L>(total);
-        const float by = total != 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
-        float kept = 0.0f, gw = 0.0f;
 #pragma unroll
         for (int s0 = 0; s0 < kMine; ++s0) {
-            q[s0] = id[s0] >= 0 ? __fmul_rn(exp_of(__fsub_rn(ld_value<DT>(row, (uint32_t)id[s0]), m)), by) : 0.0f;
+            q[s0] = id[s0] >= 0 ? exp_of(__fsub_rn(ld_value<DT>(row, (uint32_t)id[s0]), m)) : 0.0f;
             kept = __fadd_rn(kept, q[s0]);
             gw = __fmaf_rn(g[s0], q[s0], gw);
         }
+        total = group_sum<L>(total);
+        pulled = group_sum<L>(pulled);
         kept = group_sum<L>(kept);
         gw = group_sum<L>(gw);
+        const float by = total != 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
+        // sum_i G_i p_i: the normalised weights' part is 0, their sum being constant
+        // (times 0, so that a gradient that is NaN or infinite shows in the whole row)
+        const float inner = __fmaf_rn(gw, p.normalize ? 0.0f : by, __fmul_rn(pulled, by));
         if (p.normalize && live) {
-            const float inv = __fdiv_rn(1.0f, kept), mean = __fmul_rn(gw, inv);
+            const float inv = __fdiv_rn(1.0f, kept), mean = __fmul_rn(gw, inv), each = __fmul_rn(total, inv);
 #pragma unroll
             for (int s0 = 0; s0 < kMine; ++s0)
-                g[s0] = id[s0] >= 0 ? __fmul_rn(__fsub_rn(g[s0], mean), inv) : 0.0f;
+                g[s0] = id[s0] >= 0 ? __fmul_rn(__fsub_rn(g[s0], mean), each) : 0.0f;
         }
-        float inner = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            f[i] = column<L, N>(lane, i) < E ? __fmul_rn(f[i], by) : 0.0f;
 #pragma unroll
         for (int s0 = 0; s0 < kMine; ++s0)
-            inner = __fmaf_rn(g[s0], q[s0], inner);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint32_t c = column<L, N>(lane, i);
-            f[i] = c < E ? __fmul_rn(f[i], by) : 0.0f;
-            inner = __fmaf_rn(own[i], f[i], inner);
-        }
-        inner = group_sum<L>(inner);
+            q[s0] = __fmul_rn(q[s0], by);
         const float off = __fmaf_rn(cz, lse, -inner);
         if (in) {
             char *out = p.grad + t * p.grad_pitch;
