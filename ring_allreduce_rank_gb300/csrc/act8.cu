@@ -1,6 +1,6 @@
 // act8.cu -- activations kept in 8 bits for the backward pass, and brought back.
 //
-// 9 bits for 8.25 of every 16 or 32: codes [rows][width], a byte a value, and
+// 8.25 bits a value instead of 16 or 32: codes [rows][width], a byte a value, and
 // bytes [rows][width / 32], a power of two a block (act8.cuh), width being the
 // columns rounded up to 32, so that every row of codes is whole 32-byte
 // vectors.  Bound by memory bandwidth: each value is read once and written

@@ -58,7 +58,7 @@ struct RouteParams {
     const float *grad_weights;
     float balance, z; // the losses' coefficients
     uint32_t ntokens, experts, top, ctas;
-    int normalize, vector;
+    int normalize;
 };
 
 constexpr uint32_t kNothing = 0x007fffffu, kNaN = 0xffffffffu; // ordered(-inf); any NaN
@@ -78,8 +78,11 @@ __device__ __forceinline__ float from_ordered(uint32_t k)
     return __uint_as_float(k == kNaN ? 0x7fffffffu : k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-// e^x for x <= 0, to 2 + 1.2 |x| units in the last place: as good as x, the
-// rounded difference of two logits, is for it.
+// e^x for x <= 0, to 2 + 1.2 |x| units in the last place: 1.4e-6 of a probability
+// e^-8 of the largest.  x, the rounded difference of two fp32 logits, is itself
+// good to |x| / 2 such units; of two bf16 logits it is often exact, and the error is
+// this function's.  expf, good to 2 units, takes 3 % more (131072 x 256 bf16 119 us
+// for 116, 16384 x 256 fp32 23.2 for 22.5, its gradient 10.8 for 10.2).
 __device__ __forceinline__ float exp_of(float x) { return __expf(x); }
 
 template <int L> __device__ __forceinline__ float group_sum(float v)
